@@ -166,12 +166,16 @@ def _codes_plain(y, scale):
     return q.clamp(-E4M3_MAX, E4M3_MAX).to(F8)
 
 
+def _scale_plain(amax):
+    return amax / torch.full_like(amax, E4M3_MAX)  # one correctly rounded division
+
+
 def _quantize_plain(w):
     """E4M3 codes [n, k] and FP32 scales [ceil(n/128), ceil(k/128)]."""
     n, k = w.shape
     bn, bk = _blocks(n), _blocks(k)
     f = torch.nn.functional.pad(w.float(), (0, bk * BLOCK - k, 0, bn * BLOCK - n)).view(bn, BLOCK, bk, BLOCK)
-    scale = f.abs().amax((1, 3), keepdim=True) / E4M3_MAX
+    scale = _scale_plain(f.abs().amax((1, 3), keepdim=True))
     codes = _codes_plain(f, scale).view(torch.uint8).view(bn * BLOCK, bk * BLOCK)[:n, :k].contiguous()
     return codes.view(F8), scale.view(bn, bk)
 
@@ -181,7 +185,7 @@ def _groups_plain(y):
     m, k = y.shape
     bk = _blocks(k)
     f = torch.nn.functional.pad(y, (0, bk * BLOCK - k)).view(m, bk, BLOCK)
-    scale = f.abs().amax(2, keepdim=True) / E4M3_MAX
+    scale = _scale_plain(f.abs().amax(2, keepdim=True))
     codes = _codes_plain(f, scale).view(torch.uint8).view(m, bk * BLOCK)[:, :k].contiguous()
     return codes.view(F8), scale.view(m, bk).t().contiguous()
 
@@ -308,7 +312,7 @@ def _exact_blocks(y, rows):
             most = cols.abs().amax(1)
             blocks = -(-most.shape[0] // rows)
             most = torch.nn.functional.pad(most, (0, blocks * rows - most.shape[0])).view(blocks, rows).amax(1)
-            scale = most / E4M3_MAX
+            scale = most / torch.full_like(most, E4M3_MAX)
             scales[r // rows:r // rows + blocks, b] = scale
             each = scale.float().double().repeat_interleave(rows)[: cols.shape[0], None]  # the scale as it is held
             values[r:r + strip, b * BLOCK:(b + 1) * BLOCK] = torch.where(
