@@ -325,6 +325,151 @@ int fp8w_gemv_argmax_ex(const w4a16_act_segment *seg, int nseg, int m, const fp8
                         float *logits, int64_t ld_logits, int32_t *argmax, float *logprob,
                         const int32_t *mask, int64_t ld_mask, const nvfp4_exec *ex);
 
+/*
+ * The verify step: the drafted positions' hidden rows through the target's own
+ * LM head in 8-bit floating point with one FP32 scale per block of 128, then
+ * the accepted drafts and the next token.
+ *
+ *   fp8b_quantize  load time: BF16 weight -> E4M3 codes + 128 x 128 block scales
+ *   fp8b_rmsnorm   residual addition + RMSNorm -> E4M3 rows + scales per 128 columns
+ *   fp8b_gemm      their product, one row to thousands
+ *   spec_verify    verification of drafted tokens from given uniform numbers
+ */
+
+/* Largest k of fp8b_rmsnorm (a row is held in one CTA's registers). */
+#define FP8B_MAX_K 32768
+/* Most drafted tokens per sequence of spec_verify. */
+#define SPEC_MAX_DRAFT 1024
+
+/* A block-scaled FP8 weight: E4M3 codes [n, k] row-major, 16-byte aligned; one
+ * FP32 scale per block of 128 rows and 128 columns (the last blocks may be
+ * ragged), scales [ceil(n/128), ceil(k/128)] row-major, 4-byte aligned.
+ * Dequantised weight: w[r][i] = scales[r/128][i/128] * e4m3(codes[r][i]). */
+typedef struct fp8b_weight {
+    const uint8_t *codes;
+    const float *scales;
+    int64_t n, k;            /* n >= 1; k a multiple of 16; both < 2^31 */
+} fp8b_weight;
+
+/* Block-scaled FP8 activations: E4M3 codes [m, ld] (16-byte aligned, ld >= k a
+ * multiple of 16), one FP32 scale per row and 128 columns, stored by column
+ * block: scales[b * ld_scales + r] for row r and columns 128 b .. 128 b + 127
+ * (ld_scales >= m, 4-byte aligned). */
+typedef struct fp8b_act {
+    uint8_t *codes;
+    int64_t ld;
+    float *scales;
+    int64_t ld_scales;
+    int64_t m, k;
+} fp8b_act;
+
+/*
+ * fp8b_quantize -- load-time BF16 -> block-scaled FP8 quantisation of w[n, k]:
+ *   s = fl32(amax / 448) per 128 x 128 block;
+ *   code = E4M3_RNE_satfinite(fl32(x / s)) with the sign of x; +0 where s = 0.
+ *   w_bf16   device BF16 [n, ld], 16-byte aligned, ld % 8 == 0, ld >= k.
+ *   n >= 1, k >= 16, k % 16 == 0.
+ *   codes    device uint8 [n, k], 16-byte aligned, written.
+ *   scales   device float [ceil(n/128), ceil(k/128)], written.
+ * Non-finite input: that block's results undefined, NVFP4_ERR_NONFINITE to
+ * dev_status.  Workspace: none.
+ */
+int fp8b_quantize(const void *w_bf16, int64_t n, int64_t k, int64_t ld, uint8_t *codes,
+                  float *scales, const nvfp4_exec *ex);
+
+/* Input of fp8b_rmsnorm (device pointers; BF16 rows 16-byte aligned with row
+ * strides that are multiples of 8 elements and at least k). */
+typedef struct fp8b_norm_input {
+    const void *x;            /* BF16 [m, ld_x]                                 */
+    int64_t ld_x;
+    const void *residual;     /* BF16 [m, ld_residual] or NULL: nothing added   */
+    int64_t ld_residual;
+    void *residual_out;       /* BF16 [m, ld_residual_out] or NULL: not written;
+                                 may be residual or x itself (same pointer and
+                                 stride), must not overlap them otherwise       */
+    int64_t ld_residual_out;
+    const void *gamma;        /* BF16 [k], 16-byte aligned, or NULL for no norm */
+    float eps;                /* >= 0                                           */
+} fp8b_norm_input;
+
+/*
+ * fp8b_rmsnorm -- one transformer sublayer's boundary, in one pass:
+ *   h = bf16(x + residual)                    (h = x without a residual)
+ *   y = h / sqrt(mean(h^2) + eps) * gamma     (y = h without gamma)
+ *   per row and 128 columns: s = fl32(max|y| / 448),
+ *   code = E4M3_RNE_satfinite(fl32(y / s)) with the sign of y; +0 where s = 0.
+ * h is the new residual stream (residual_out); the norm reads it as rounded, as
+ * the next sublayer will.  y stays in FP32 until its codes are rounded; sums are
+ * FP32 in a fixed order.  gamma as stored, as in w4a16_act_segment.
+ *   out   codes and scales written for rows 0..out->m-1; out->m >= 1,
+ *         out->k a multiple of 16, 16..FP8B_MAX_K.
+ * A row with a non-finite value, or whose sum of squares leaves FP32's range:
+ * that row's codes and scales undefined, NVFP4_ERR_NONFINITE to dev_status.
+ * Workspace: none.
+ */
+int fp8b_rmsnorm(const fp8b_norm_input *in, const fp8b_act *out, const nvfp4_exec *ex);
+
+/*
+ * fp8b_gemm -- C[m, n] = sum_b sa[b][m] * sw[n/128][b] * sum_{i in block b} a[m][i] w[n][i]
+ * over the 128-column blocks b: each block's sum on the FP8 tensor cores with
+ * FP32 accumulation, scaled and added in FP32, rounded once to the output type.
+ *   a      a->k == w->k; a->m >= 1 (one token to prefill sizes).
+ *   c      device [m, ldc] of c_dtype (F32 or BF16), ldc >= n, aligned to its type.
+ * Rows of C at or past m and columns past n are left as they were.
+ * Workspace: none.  Waits inside the kernel are bounded; one that runs out
+ * writes NVFP4_ERR_TIMEOUT to dev_status and leaves C incomplete.
+ */
+int fp8b_gemm(const fp8b_act *a, const fp8b_weight *w, void *c, int c_dtype, int64_t ldc,
+              const nvfp4_exec *ex);
+
+/* Input of spec_verify (device pointers; probabilities of one dtype, F32 or
+ * BF16, aligned to it; unit stride along the vocabulary). */
+typedef struct spec_verify_input {
+    const void *target;       /* [batch, g + 1, vocab]: the target's probabilities
+                                 before each draft, and after the last one      */
+    int64_t ld_target_seq;    /* elements between sequences                     */
+    int64_t ld_target_pos;    /* elements between positions                     */
+    const void *draft;        /* [batch, g, draft_vocab]: what the drafts were
+                                 sampled from; NULL: greedy drafts (q = 1)      */
+    int64_t ld_draft_seq, ld_draft_pos;
+    int64_t draft_vocab;      /* 1..vocab: a reduced-vocabulary draft head scores
+                                 the first rows; q = 0 past them                */
+    int dtype;
+    const int32_t *tokens;    /* [batch, ld_tokens] drafted tokens              */
+    int64_t ld_tokens;
+    const int32_t *num_draft; /* [batch] drafts per sequence, or NULL: all g    */
+    const float *accept_u;    /* [batch, ld_accept_u] uniform numbers in [0, 1) */
+    int64_t ld_accept_u;
+    const float *sample_u;    /* [batch] uniform numbers in [0, 1)              */
+    int64_t batch;            /* >= 1                                           */
+    int64_t g;                /* 0..SPEC_MAX_DRAFT                              */
+    int64_t vocab;            /* 1..2^31-1                                      */
+} spec_verify_input;
+
+/*
+ * spec_verify -- per sequence, with p_i, q_i the target's and the draft's row i:
+ *   draft i = 0, 1, ... is accepted while u_i q_i(d_i) < p_i(d_i) (compared
+ *   exactly); a = the number accepted before the first refusal.
+ *   The token after them is sampled from w = max(p_a - q_a, 0) after a refusal
+ *   (greedy drafts: p_a without the refused token) and from w = p_a when all
+ *   drafts were accepted: the lowest j with  w_0 + ... + w_j > r sum(w), r the
+ *   sequence's sample_u; the last j with w_j > 0 where rounding or r >= 1 leaves
+ *   none.  w without any mass falls back to p_a; p_a without any, to token 0.
+ * Sums are carried in two binary32 words and joined in binary64 (about 2^-46 of
+ * sum(w)), in a fixed order: the same call gives the same tokens.
+ *   out_tokens  device int32 [batch, ld_out], ld_out >= g + 1: the accepted drafts,
+ *               the sampled token, then -1 up to g.
+ *   accepted    device int32 [batch]: a.
+ * num_draft[s] < 0 marks a sequence as absent (a padded batch): its outputs are
+ * left as they were.  num_draft[s] > g counts as g, a token outside the vocabulary
+ * is refused (both: NVFP4_ERR_INDEX to dev_status).  A weight that is negative or
+ * not finite counts as 0 (not finite: NVFP4_ERR_NONFINITE to dev_status).
+ * Only the rows that decide are read: one target row and at most one draft row
+ * per sequence, besides the drafted tokens' own entries.  Workspace: none.
+ */
+int spec_verify(const spec_verify_input *in, int32_t *out_tokens, int64_t ld_out,
+                int32_t *accepted, const nvfp4_exec *ex);
+
 #ifdef __cplusplus
 }
 #endif

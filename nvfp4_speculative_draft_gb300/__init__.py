@@ -16,6 +16,10 @@ The calls keep the C names:
 * :func:`w4a16_gemm`         prefill C[m, n] = bf16(g * A . w~^T)
 * :func:`fp8w_quantize`, :func:`fp8w_gemv`, :func:`fp8w_gemv_argmax`,
   :func:`fp8w_gemv_argmax_ex`: the same contracts for per-row FP8 weights
+* :func:`fp8b_quantize`      BF16 [n, k] -> FP8 with one scale per 128 x 128 block
+* :func:`fp8b_rmsnorm`       residual addition + RMSNorm -> FP8 rows, one scale per 128 columns
+* :func:`fp8b_gemm`          the product of the two, one row to thousands
+* :func:`spec_verify`        verification of drafted tokens against the target's probabilities
 
 The C library checks what it can see (null pointers, sizes, leading
 dimensions, alignment); the extents, dtypes and devices of the tensors are
@@ -34,6 +38,15 @@ GPU, BF16 unless stated)::
     h = nd.w4a16_gemv([(embed_table, g_e, 1e-6, token), (hidden, g_h, 1e-6)], fc,
                       out_dtype=torch.bfloat16)         # embedding gathered by token
     c = nd.w4a16_gemm(prefill_activations, fc)          # [m, k] x [n, k]^T -> [m, n]
+
+The verify step of a speculative decoder (drafted positions through the target's
+own head, then the accepted drafts and the next token)::
+
+    head8 = nd.fp8b_quantize(w_target_head)              # load time
+    a, hidden = nd.fp8b_rmsnorm(x, norm_weight, 1e-6, residual=hidden)
+    logits = nd.fp8b_gemm(a, head8, out_dtype=torch.float32)   # [batch * (g + 1), vocab]
+    p = torch.softmax(logits.view(batch, g + 1, -1), -1)
+    tokens, accepted = nd.spec_verify(p, drafted, accept_u, sample_u, draft_probs=q)
 """
 import ctypes
 import os
@@ -65,8 +78,12 @@ def gemv_workspace_bytes(m: int, k: int) -> int:
 
 
 QUANTIZE_WS_BYTES = 16
+FP8B_BLOCK = 128
+FP8B_MAX_K = 32768
+SPEC_MAX_DRAFT = 1024
 EXPORTED = ("nvfp4_quantize", "w4a16_gemv", "w4a16_gemv_argmax", "w4a16_gemv_argmax_ex",
-            "w4a16_gemm", "fp8w_quantize", "fp8w_gemv", "fp8w_gemv_argmax", "fp8w_gemv_argmax_ex")
+            "w4a16_gemm", "fp8w_quantize", "fp8w_gemv", "fp8w_gemv_argmax", "fp8w_gemv_argmax_ex",
+            "fp8b_quantize", "fp8b_rmsnorm", "fp8b_gemm", "spec_verify")
 
 
 class Nvfp4Error(RuntimeError):
@@ -126,6 +143,34 @@ class _Fp8Weight(ctypes.Structure):
                 ("n", ctypes.c_int64), ("k", ctypes.c_int64)]
 
 
+class _Fp8BlockWeight(ctypes.Structure):
+    _fields_ = [("codes", ctypes.c_void_p), ("scales", ctypes.c_void_p),
+                ("n", ctypes.c_int64), ("k", ctypes.c_int64)]
+
+
+class _Fp8BlockActs(ctypes.Structure):
+    _fields_ = [("codes", ctypes.c_void_p), ("ld", ctypes.c_int64), ("scales", ctypes.c_void_p),
+                ("ld_scales", ctypes.c_int64), ("m", ctypes.c_int64), ("k", ctypes.c_int64)]
+
+
+class _NormInput(ctypes.Structure):
+    _fields_ = [("x", ctypes.c_void_p), ("ld_x", ctypes.c_int64),
+                ("residual", ctypes.c_void_p), ("ld_residual", ctypes.c_int64),
+                ("residual_out", ctypes.c_void_p), ("ld_residual_out", ctypes.c_int64),
+                ("gamma", ctypes.c_void_p), ("eps", ctypes.c_float)]
+
+
+class _VerifyInput(ctypes.Structure):
+    _fields_ = [("target", ctypes.c_void_p), ("ld_target_seq", ctypes.c_int64),
+                ("ld_target_pos", ctypes.c_int64), ("draft", ctypes.c_void_p),
+                ("ld_draft_seq", ctypes.c_int64), ("ld_draft_pos", ctypes.c_int64),
+                ("draft_vocab", ctypes.c_int64), ("dtype", ctypes.c_int),
+                ("tokens", ctypes.c_void_p), ("ld_tokens", ctypes.c_int64),
+                ("num_draft", ctypes.c_void_p), ("accept_u", ctypes.c_void_p),
+                ("ld_accept_u", ctypes.c_int64), ("sample_u", ctypes.c_void_p),
+                ("batch", ctypes.c_int64), ("g", ctypes.c_int64), ("vocab", ctypes.c_int64)]
+
+
 class _Exec(ctypes.Structure):
     _fields_ = [("stream", ctypes.c_void_p), ("workspace", ctypes.c_void_p),
                 ("workspace_bytes", ctypes.c_size_t), ("dev_status", ctypes.c_void_p)]
@@ -159,6 +204,10 @@ def load(path: str = LIB_PATH):
                                       i64, P(_Exec)]
     L.w4a16_gemv_argmax_noalloc.argtypes = [P(_Segment), i32, i32, P(_Weight), vp, i64, vp, vp,
                                             vp]
+    L.fp8b_quantize.argtypes = [vp, i64, i64, i64, vp, vp, P(_Exec)]
+    L.fp8b_rmsnorm.argtypes = [P(_NormInput), P(_Fp8BlockActs), P(_Exec)]
+    L.fp8b_gemm.argtypes = [P(_Fp8BlockActs), P(_Fp8BlockWeight), vp, i32, i64, P(_Exec)]
+    L.spec_verify.argtypes = [P(_VerifyInput), vp, i64, vp, P(_Exec)]
     for f in EXPORTED + ("w4a16_gemv_argmax_noalloc",):
         getattr(L, f).restype = ctypes.c_int
     _LIB = L
@@ -543,3 +592,216 @@ def fp8w_gemv_argmax_ex(segments: Sequence, weight: Fp8Weight, mask: Optional[to
     return _argmax_ex("fp8w_gemv_argmax_ex", segments, weight, weight.n, weight.check(), mask,
                       logprob, logits, out_logits, out_argmax, out_logprob, workspace, stream,
                       dev_status)
+
+
+# ------------------------------------------- the verify step (block-scaled FP8)
+
+@dataclass
+class Fp8BlockWeight:
+    """Device tensors of one block-scaled FP8 (E4M3) weight."""
+    codes: torch.Tensor   # uint8 [n, k]
+    scales: torch.Tensor  # float32 [ceil(n/128), ceil(k/128)]
+    n: int
+    k: int
+
+    def check(self) -> torch.device:
+        """Tensors consistent with (n, k) on one CUDA device; returns it."""
+        dev = _cuda_device(self.codes, "weight.codes")
+        _need(self.codes.dtype == torch.uint8 and self.codes.shape == (self.n, self.k)
+              and self.codes.is_contiguous(), "weight.codes must be contiguous uint8 [n, k]")
+        _need(isinstance(self.scales, torch.Tensor) and self.scales.dtype == torch.float32
+              and self.scales.device == dev and self.scales.is_contiguous()
+              and self.scales.shape == (-(-self.n // FP8B_BLOCK), -(-self.k // FP8B_BLOCK)),
+              f"weight.scales must be contiguous float32 [ceil(n/128), ceil(k/128)] on {dev}")
+        return dev
+
+    def c(self) -> _Fp8BlockWeight:
+        return _Fp8BlockWeight(self.codes.data_ptr(), self.scales.data_ptr(), self.n, self.k)
+
+
+@dataclass
+class Fp8BlockActs:
+    """Device tensors of block-scaled FP8 (E4M3) activations.  The scales are
+    stored by column block, so that a tile's tokens lie side by side."""
+    codes: torch.Tensor   # uint8 [m, k], rows may be padded
+    scales: torch.Tensor  # float32 [ceil(k/128), m], rows may be padded
+    m: int
+    k: int
+
+    def check(self) -> torch.device:
+        """Tensors consistent with (m, k) on one CUDA device; returns it."""
+        dev = _cuda_device(self.codes, "acts.codes")
+        _need(self.codes.dtype == torch.uint8 and self.codes.shape == (self.m, self.k)
+              and _rows(self.codes), "acts.codes must be uint8 [m, k] with unit column stride")
+        _need(isinstance(self.scales, torch.Tensor) and self.scales.dtype == torch.float32
+              and self.scales.device == dev and _rows(self.scales)
+              and self.scales.shape == (-(-self.k // FP8B_BLOCK), self.m),
+              f"acts.scales must be float32 [ceil(k/128), m] with unit column stride on {dev}")
+        return dev
+
+    def c(self) -> _Fp8BlockActs:
+        return _Fp8BlockActs(self.codes.data_ptr(), _ld(self.codes), self.scales.data_ptr(),
+                             _ld(self.scales), self.m, self.k)
+
+
+def _rows(t) -> bool:
+    """A 2-D tensor with unit column stride whose rows do not overlap."""
+    return t.dim() == 2 and (t.stride(1) == 1 or t.shape[1] <= 1) and \
+        (t.stride(0) >= t.shape[1] or t.shape[0] <= 1)
+
+
+def _ld(t) -> int:
+    """Row stride for the library: a single row's is its length rounded up to a
+    multiple of 16 (torch leaves the stride of an extent of 1 arbitrary)."""
+    return t.stride(0) if t.shape[0] > 1 else (t.shape[1] + 15) // 16 * 16
+
+
+def _run(call, device, stream, dev_status, *args):
+    """Call the library on `device` with args and an exec of the stream."""
+    if dev_status is not None:
+        _check_tensor(dev_status, "dev_status", torch.int32, device, (1,))
+    f = getattr(load(), call)
+    st = dev_status.data_ptr() if dev_status is not None else None
+    if torch.cuda.current_device() == device.index:
+        rc = f(*args, ctypes.byref(_Exec(_stream(stream), None, 0, st)))
+    else:
+        with torch.cuda.device(device):
+            rc = f(*args, ctypes.byref(_Exec(_stream(stream), None, 0, st)))
+    _check(call, rc)
+
+
+def fp8b_quantize(w: torch.Tensor, out: Optional[Fp8BlockWeight] = None, stream=None,
+                  dev_status: Optional[torch.Tensor] = None) -> Fp8BlockWeight:
+    """BF16 [n, k] (rows may be padded) -> E4M3 codes [n, k] and one FP32 scale per
+    128 x 128 block.  k is a multiple of 16."""
+    dev = _cuda_device(w, "w")
+    _check_tensor(w, "w", torch.bfloat16, dev, (0, 0))
+    n, k = w.shape
+    if out is None:
+        out = Fp8BlockWeight(torch.empty((n, k), dtype=torch.uint8, device=dev),
+                             torch.empty((-(-n // FP8B_BLOCK), -(-k // FP8B_BLOCK)),
+                                         dtype=torch.float32, device=dev), n, k)
+    _need(out.n == n and out.k == k, "out must be a weight of the same [n, k]")
+    _need(out.check() == dev, f"out must be on {dev}")
+    _run("fp8b_quantize", dev, stream, dev_status, w.data_ptr(), n, k, _ld(w),
+         out.codes.data_ptr(), out.scales.data_ptr())
+    return out
+
+
+def fp8b_rmsnorm(x: torch.Tensor, gamma: Optional[torch.Tensor], eps: float = 1e-6,
+                 residual: Optional[torch.Tensor] = None,
+                 residual_out: Optional[torch.Tensor] = None,
+                 out: Optional[Fp8BlockActs] = None, stream=None,
+                 dev_status: Optional[torch.Tensor] = None):
+    """h = bf16(x + residual); y = RMSNorm(h) * gamma; y quantised per row and 128
+    columns.  Returns (Fp8BlockActs, h), h the new residual stream, or None without
+    a residual.  x, residual BF16 [m, k]; gamma BF16 [k], or None for no norm (y = h).
+
+    ``residual_out`` (default: a new tensor) may be ``residual`` or ``x`` itself."""
+    dev = _cuda_device(x, "x")
+    _check_tensor(x, "x", torch.bfloat16, dev, (0, 0))
+    m, k = x.shape
+    if gamma is not None:
+        _check_tensor(gamma, "gamma", torch.bfloat16, dev, (k,), contiguous=True)
+        _need(gamma.shape[0] == k, f"gamma must have {k} elements")
+    if residual is not None:
+        _check_tensor(residual, "residual", torch.bfloat16, dev, (m, k))
+        _need(residual.shape == x.shape, "residual must have the shape of x")
+        if residual_out is None:
+            residual_out = torch.empty((m, k), dtype=torch.bfloat16, device=dev)
+    if residual_out is not None:
+        _check_tensor(residual_out, "residual_out", torch.bfloat16, dev, (m, k))
+        _need(residual_out.shape == x.shape, "residual_out must have the shape of x")
+    if out is None:
+        out = Fp8BlockActs(torch.empty((m, k), dtype=torch.uint8, device=dev),
+                           torch.empty((-(-k // FP8B_BLOCK), m), dtype=torch.float32, device=dev),
+                           m, k)
+    else:
+        _need(out.m == m and out.k == k, "out must be activations of the same [m, k]")
+        _need(out.check() == dev, f"out must be on {dev}")
+    inp = _NormInput(x.data_ptr(), _ld(x),
+                     residual.data_ptr() if residual is not None else None,
+                     _ld(residual) if residual is not None else 0,
+                     residual_out.data_ptr() if residual_out is not None else None,
+                     _ld(residual_out) if residual_out is not None else 0,
+                     gamma.data_ptr() if gamma is not None else None, float(eps))
+    _run("fp8b_rmsnorm", dev, stream, dev_status, ctypes.byref(inp), ctypes.byref(out.c()))
+    return out, residual_out
+
+
+def fp8b_gemm(acts: Fp8BlockActs, weight: Fp8BlockWeight, out_dtype=torch.bfloat16,
+              out: Optional[torch.Tensor] = None, stream=None,
+              dev_status: Optional[torch.Tensor] = None) -> torch.Tensor:
+    """C[m, n] = acts . weight^T in BF16 or FP32 (FP32 accumulation), for one row
+    or thousands."""
+    dev = weight.check()
+    _need(acts.check() == dev, f"acts must be on {dev}")
+    _need(acts.k == weight.k, f"acts must have k = {weight.k} columns, got {acts.k}")
+    if out is None:
+        out = torch.empty((acts.m, weight.n), dtype=out_dtype, device=dev)
+    _need(out.dtype in (torch.float32, torch.bfloat16), "out must be float32 or bfloat16")
+    _check_tensor(out, "out", out.dtype, dev, (acts.m, weight.n))
+    dt = DTYPE_F32 if out.dtype == torch.float32 else DTYPE_BF16
+    ldc = out.stride(0) if out.shape[0] > 1 else out.shape[1]
+    _run("fp8b_gemm", dev, stream, dev_status, ctypes.byref(acts.c()), ctypes.byref(weight.c()),
+         out.data_ptr(), dt, ldc)
+    return out
+
+
+def spec_verify(target_probs: torch.Tensor, draft_tokens: torch.Tensor, accept_u: torch.Tensor,
+                sample_u: torch.Tensor, draft_probs: Optional[torch.Tensor] = None,
+                num_draft: Optional[torch.Tensor] = None,
+                out_tokens: Optional[torch.Tensor] = None,
+                out_accepted: Optional[torch.Tensor] = None, stream=None,
+                dev_status: Optional[torch.Tensor] = None):
+    """Returns (tokens int32 [batch, g + 1], accepted int32 [batch]): the accepted
+    drafts, the token sampled after them, then -1.
+
+    target_probs [batch, g + 1, vocab] and draft_probs [batch, g, draft_vocab]
+    (draft_vocab <= vocab) are FP32 or BF16, both the same, with unit stride along
+    the vocabulary; draft_probs None: the drafts are greedy.  draft_tokens int32
+    [batch, g]; accept_u FP32 [batch, g] and sample_u FP32 [batch] uniform in [0, 1);
+    num_draft int32 [batch]: drafts per sequence (default g; negative: the sequence
+    is absent and its outputs are left as they were)."""
+    dev = _cuda_device(target_probs, "target_probs")
+    dt = target_probs.dtype
+    _need(dt in (torch.float32, torch.bfloat16), "target_probs must be float32 or bfloat16")
+    _need(target_probs.dim() == 3 and target_probs.shape[1] >= 1,
+          "target_probs must be [batch, g + 1, vocab]")
+    b, g, v = target_probs.shape[0], target_probs.shape[1] - 1, target_probs.shape[2]
+    _need(target_probs.stride(2) == 1 or v == 1, "target_probs must have unit vocabulary stride")
+    _check_tensor(draft_tokens, "draft_tokens", torch.int32, dev, (b, g))
+    _need(draft_tokens.shape == (b, g), f"draft_tokens must be [{b}, {g}]")
+    _check_tensor(accept_u, "accept_u", torch.float32, dev, (b, g))
+    _check_tensor(sample_u, "sample_u", torch.float32, dev, (b,))
+    dv = 0
+    if draft_probs is not None:
+        _need(isinstance(draft_probs, torch.Tensor) and draft_probs.dtype == dt
+              and draft_probs.device == dev, f"draft_probs must be {dt} on {dev}")
+        _need(draft_probs.dim() == 3 and draft_probs.shape[:2] == (b, g),
+              f"draft_probs must be [{b}, {g}, draft_vocab]")
+        dv = draft_probs.shape[2]
+        _need(1 <= dv <= v, f"draft_probs must score 1 to {v} tokens")
+        _need(draft_probs.stride(2) == 1 or dv == 1, "draft_probs must have unit vocabulary stride")
+    if num_draft is not None:
+        _check_tensor(num_draft, "num_draft", torch.int32, dev, (b,))
+    if out_tokens is None:
+        out_tokens = torch.empty((b, g + 1), dtype=torch.int32, device=dev)
+    else:
+        _check_tensor(out_tokens, "out_tokens", torch.int32, dev, (b, g + 1))
+    if out_accepted is None:
+        out_accepted = torch.empty(b, dtype=torch.int32, device=dev)
+    else:
+        _check_tensor(out_accepted, "out_accepted", torch.int32, dev, (b,))
+    inp = _VerifyInput(target_probs.data_ptr(), target_probs.stride(0), target_probs.stride(1),
+                       draft_probs.data_ptr() if dv and g else None,
+                       draft_probs.stride(0) if dv else 0, draft_probs.stride(1) if dv else 0, dv,
+                       DTYPE_F32 if dt == torch.float32 else DTYPE_BF16,
+                       draft_tokens.data_ptr() if g else None,
+                       draft_tokens.stride(0) if b > 1 else g,
+                       num_draft.data_ptr() if num_draft is not None else None,
+                       accept_u.data_ptr() if g else None, accept_u.stride(0) if b > 1 else g,
+                       sample_u.data_ptr(), b, g, v)
+    _run("spec_verify", dev, stream, dev_status, ctypes.byref(inp), out_tokens.data_ptr(),
+         out_tokens.stride(0) if b > 1 else out_tokens.shape[1], out_accepted.data_ptr())
+    return out_tokens, out_accepted

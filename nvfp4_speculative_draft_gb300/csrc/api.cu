@@ -80,6 +80,15 @@ int check_fp8_weight(const fp8w_weight* w) {
   return NVFP4_OK;
 }
 
+int check_fp8b_act(const fp8b_act* a) {
+  if (a == nullptr || a->codes == nullptr || a->scales == nullptr) return NVFP4_ERR_NULL;
+  if (a->m < 1 || a->m > 0x7FFFFFFF || a->k < 16 || a->k % 16 != 0 || a->k > 0x7FFFFFFF ||
+      a->ld < a->k || a->ld_scales < a->m)
+    return NVFP4_ERR_SHAPE;
+  if (!aligned16(a->codes) || a->ld % 16 != 0 || !aligned4(a->scales)) return NVFP4_ERR_ALIGN;
+  return NVFP4_OK;
+}
+
 int check_segments(const w4a16_act_segment* seg, int nseg, int m, int64_t k) {
   if (seg == nullptr) return NVFP4_ERR_NULL;
   if (nseg < 1 || nseg > 2) return NVFP4_ERR_SHAPE;
@@ -130,6 +139,8 @@ bool encode_tiled(CUtensorMap* map, CUtensorMapDataType type, cuuint32_t rank, v
 namespace {
 
 using nvfp4::aligned16;
+using nvfp4::aligned4;
+using nvfp4::check_fp8b_act;
 using nvfp4::check_fp8_weight;
 using nvfp4::check_segments;
 using nvfp4::check_weight;
@@ -294,6 +305,72 @@ int fp8w_gemv_argmax(const w4a16_act_segment* seg, int nseg, int m, const fp8w_w
     return NVFP4_ERR_WORKSPACE;
   return launch_gemv(seg, nseg, m, ref_of(w), logits, NVFP4_DTYPE_F32, ld_logits, true,
                      argmax, ex->workspace, ex->workspace_bytes, status_of(ex), stream_of(ex));
+}
+
+int fp8b_quantize(const void* w_bf16, int64_t n, int64_t k, int64_t ld, uint8_t* codes,
+                  float* scales, const nvfp4_exec* ex) {
+  if (w_bf16 == nullptr || codes == nullptr || scales == nullptr) return NVFP4_ERR_NULL;
+  if (n < 1 || k < 16 || k % 16 != 0 || ld < k || n > 0x7FFFFFFF || k > 0x7FFFFFFF)
+    return NVFP4_ERR_SHAPE;
+  if (!aligned16(w_bf16) || !aligned16(codes) || !aligned4(scales) || ld % 8 != 0)
+    return NVFP4_ERR_ALIGN;
+  return launch_fp8b_quantize(w_bf16, n, k, ld, codes, scales, status_of(ex), stream_of(ex));
+}
+
+int fp8b_rmsnorm(const fp8b_norm_input* in, const fp8b_act* out, const nvfp4_exec* ex) {
+  if (in == nullptr || in->x == nullptr) return NVFP4_ERR_NULL;
+  int rc = check_fp8b_act(out);
+  if (rc) return rc;
+  const int64_t k = out->k;
+  if (k > FP8B_MAX_K) return NVFP4_ERR_SHAPE;
+  if (in->ld_x < k || (in->residual != nullptr && in->ld_residual < k) ||
+      (in->residual_out != nullptr && in->ld_residual_out < k) ||
+      (in->gamma != nullptr && !(in->eps >= 0.0f)))
+    return NVFP4_ERR_SHAPE;
+  if (!aligned16(in->x) || !aligned16(in->residual) || !aligned16(in->residual_out) ||
+      !aligned16(in->gamma) || in->ld_x % 8 != 0 ||
+      (in->residual != nullptr && in->ld_residual % 8 != 0) ||
+      (in->residual_out != nullptr && in->ld_residual_out % 8 != 0))
+    return NVFP4_ERR_ALIGN;
+  return launch_fp8b_rmsnorm(in, out, status_of(ex), stream_of(ex));
+}
+
+int fp8b_gemm(const fp8b_act* a, const fp8b_weight* w, void* c, int c_dtype, int64_t ldc,
+              const nvfp4_exec* ex) {
+  if (w == nullptr || w->codes == nullptr || w->scales == nullptr || c == nullptr)
+    return NVFP4_ERR_NULL;
+  int rc = check_fp8b_act(a);
+  if (rc) return rc;
+  if (c_dtype != NVFP4_DTYPE_F32 && c_dtype != NVFP4_DTYPE_BF16) return NVFP4_ERR_DTYPE;
+  if (w->n < 1 || w->n > 0x7FFFFFFF || w->k != a->k || ldc < w->n) return NVFP4_ERR_SHAPE;
+  if (!aligned16(w->codes) || !aligned4(w->scales) ||
+      (reinterpret_cast<uintptr_t>(c) & (c_dtype == NVFP4_DTYPE_F32 ? 3u : 1u)))
+    return NVFP4_ERR_ALIGN;
+  return launch_fp8b_gemm(a, w, c, c_dtype, ldc, status_of(ex), stream_of(ex));
+}
+
+int spec_verify(const spec_verify_input* in, int32_t* out_tokens, int64_t ld_out,
+                int32_t* accepted, const nvfp4_exec* ex) {
+  if (in == nullptr || in->target == nullptr || in->sample_u == nullptr || out_tokens == nullptr ||
+      accepted == nullptr || (in->g > 0 && (in->tokens == nullptr || in->accept_u == nullptr)))
+    return NVFP4_ERR_NULL;
+  if (in->dtype != NVFP4_DTYPE_F32 && in->dtype != NVFP4_DTYPE_BF16) return NVFP4_ERR_DTYPE;
+  if (in->batch < 1 || in->g < 0 || in->g > SPEC_MAX_DRAFT || in->vocab < 1 ||
+      in->vocab > 0x7FFFFFFF || in->ld_target_seq < 0 || in->ld_target_pos < 0 ||
+      ld_out < in->g + 1)
+    return NVFP4_ERR_SHAPE;
+  if (in->g > 0 && (in->ld_tokens < in->g || in->ld_accept_u < in->g)) return NVFP4_ERR_SHAPE;
+  if (in->g > 0 && in->draft != nullptr &&
+      (in->draft_vocab < 1 || in->draft_vocab > in->vocab || in->ld_draft_seq < 0 ||
+       in->ld_draft_pos < 0))
+    return NVFP4_ERR_SHAPE;
+  const uintptr_t each = in->dtype == NVFP4_DTYPE_F32 ? 3u : 1u;
+  if ((reinterpret_cast<uintptr_t>(in->target) & each) ||
+      (reinterpret_cast<uintptr_t>(in->draft) & each) || !aligned4(in->tokens) ||
+      !aligned4(in->num_draft) || !aligned4(in->accept_u) || !aligned4(in->sample_u) ||
+      !aligned4(out_tokens) || !aligned4(accepted))
+    return NVFP4_ERR_ALIGN;
+  return launch_spec_verify(in, out_tokens, ld_out, accepted, status_of(ex), stream_of(ex));
 }
 
 }  // extern "C"

@@ -47,6 +47,8 @@ __host__ __device__ __forceinline__ int64_t cdiv(int64_t a, int64_t b) { return 
 
 inline bool aligned16(const void* p) { return (reinterpret_cast<uintptr_t>(p) & 15u) == 0; }
 
+inline bool aligned4(const void* p) { return (reinterpret_cast<uintptr_t>(p) & 3u) == 0; }
+
 // Number of SMs of the current device (cached per device ordinal).
 int sm_count();
 
@@ -68,6 +70,7 @@ bool encode_tiled(CUtensorMap* map, CUtensorMapDataType type, cuuint32_t rank, v
 // nvfp4draft.h).
 int check_weight(const nvfp4_weight* w);
 int check_fp8_weight(const fp8w_weight* w);
+int check_fp8b_act(const fp8b_act* a);
 int check_segments(const w4a16_act_segment* seg, int nseg, int m, int64_t k);
 
 }  // namespace nvfp4
@@ -102,3 +105,11 @@ int launch_gemm(const void* a, int64_t m, int64_t lda, const nvfp4_weight* w, vo
                 int64_t ldc, void* workspace, size_t workspace_bytes, int32_t* dev_status,
                 cudaStream_t stream);
 size_t gemm_f16_workspace_bytes(int64_t m, int64_t k);
+int launch_fp8b_quantize(const void* w, int64_t n, int64_t k, int64_t ld, uint8_t* codes,
+                         float* scales, int32_t* dev_status, cudaStream_t stream);
+int launch_fp8b_rmsnorm(const fp8b_norm_input* in, const fp8b_act* out, int32_t* dev_status,
+                        cudaStream_t stream);
+int launch_fp8b_gemm(const fp8b_act* a, const fp8b_weight* w, void* c, int c_dtype, int64_t ldc,
+                     int32_t* dev_status, cudaStream_t stream);
+int launch_spec_verify(const spec_verify_input* in, int32_t* out_tokens, int64_t ld_out,
+                       int32_t* accepted, int32_t* dev_status, cudaStream_t stream);
