@@ -50,6 +50,7 @@ own head, then the accepted drafts and the next token)::
 """
 import ctypes
 import os
+import struct
 from dataclasses import dataclass
 from typing import Optional, Sequence
 
@@ -204,10 +205,11 @@ def load(path: str = LIB_PATH):
                                       i64, P(_Exec)]
     L.w4a16_gemv_argmax_noalloc.argtypes = [P(_Segment), i32, i32, P(_Weight), vp, i64, vp, vp,
                                             vp]
-    L.fp8b_quantize.argtypes = [vp, i64, i64, i64, vp, vp, P(_Exec)]
-    L.fp8b_rmsnorm.argtypes = [P(_NormInput), P(_Fp8BlockActs), P(_Exec)]
-    L.fp8b_gemm.argtypes = [P(_Fp8BlockActs), P(_Fp8BlockWeight), vp, i32, i64, P(_Exec)]
-    L.spec_verify.argtypes = [P(_VerifyInput), vp, i64, vp, P(_Exec)]
+    # structs by address: packed bytes, or byref() of the Structures above
+    L.fp8b_quantize.argtypes = [vp, i64, i64, i64, vp, vp, vp]
+    L.fp8b_rmsnorm.argtypes = [vp, vp, vp]
+    L.fp8b_gemm.argtypes = [vp, vp, vp, i32, i64, vp]
+    L.spec_verify.argtypes = [vp, vp, i64, vp, vp]
     for f in EXPORTED + ("w4a16_gemv_argmax_noalloc",):
         getattr(L, f).restype = ctypes.c_int
     _LIB = L
@@ -595,6 +597,70 @@ def fp8w_gemv_argmax_ex(segments: Sequence, weight: Fp8Weight, mask: Optional[to
 
 
 # ------------------------------------------- the verify step (block-scaled FP8)
+#
+# A single token's kernels take a few microseconds, so these calls are written for
+# little host time: one expression per tensor decides whether it is as asked (the
+# message is formed only when it is not), and the C structs are packed as bytes.
+
+_PACK_EXEC = struct.Struct("PPNP").pack           # nvfp4_exec
+_PACK_NORM = struct.Struct("PqPqPqPf4x").pack     # fp8b_norm_input
+_PACK_ACTS = struct.Struct("PqPqqq").pack         # fp8b_act
+_PACK_WEIGHT = struct.Struct("PPqq").pack         # fp8b_weight
+_PACK_VERIFY = struct.Struct("PqqPqqqiPqPPqPqqq").pack  # spec_verify_input
+_BF16, _F32, _I32, _U8 = torch.bfloat16, torch.float32, torch.int32, torch.uint8
+
+
+def _is(t, dtype, dev, shape) -> bool:
+    """A tensor of exactly that dtype, device and shape."""
+    return isinstance(t, torch.Tensor) and t.dtype is dtype and t.device == dev and t.shape == shape
+
+
+def _is_rows(t, dtype, dev, shape) -> bool:
+    """The same, 2-D, with unit column stride and rows that do not overlap."""
+    if not _is(t, dtype, dev, shape):
+        return False
+    ld, one = t.stride()
+    return (one == 1 or shape[1] <= 1) and (ld >= shape[1] or shape[0] <= 1)
+
+
+def _refuse(name, t, dtype, dev, shape, more=""):
+    got = f"{t.dtype} {tuple(t.shape)} strides {t.stride()} on {t.device}" \
+        if isinstance(t, torch.Tensor) else type(t).__name__
+    raise ValueError(f"{name} must be {dtype} {tuple(shape)} on {dev}{more}, got {got}")
+
+
+_ROWS = " with unit column stride and rows that do not overlap"
+
+
+def _cuda(t, name):
+    if not (isinstance(t, torch.Tensor) and t.is_cuda):
+        raise ValueError(f"{name} must be a CUDA tensor")
+    return t.device
+
+
+def _ld(t) -> int:
+    """Row stride for the library: a single row's is its length rounded up to a
+    multiple of 16 (torch leaves the stride of an extent of 1 arbitrary)."""
+    return t.stride(0) if t.shape[0] > 1 else (t.shape[1] + 15) // 16 * 16
+
+
+def _run(call, dev, stream, dev_status, *args):
+    """Call the library with args and an exec, on the tensors' device: its current
+    stream is the default, and it is current during the call."""
+    if dev_status is not None and not (_is(dev_status, _I32, dev, dev_status.shape)
+                                       and dev_status.numel() >= 1):
+        _refuse("dev_status", dev_status, _I32, dev, (1,))
+    raw = torch._C._cuda_getCurrentRawStream(dev.index) if stream is None else _stream(stream)
+    ex = _PACK_EXEC(raw, 0, 0, dev_status.data_ptr() if dev_status is not None else 0)
+    f = getattr(_LIB or load(), call)
+    if torch.cuda.current_device() == dev.index:
+        rc = f(*args, ex)
+    else:
+        with torch.cuda.device(dev):
+            rc = f(*args, ex)
+    if rc != NVFP4_OK:
+        raise Nvfp4Error(call, rc)
+
 
 @dataclass
 class Fp8BlockWeight:
@@ -606,17 +672,17 @@ class Fp8BlockWeight:
 
     def check(self) -> torch.device:
         """Tensors consistent with (n, k) on one CUDA device; returns it."""
-        dev = _cuda_device(self.codes, "weight.codes")
-        _need(self.codes.dtype == torch.uint8 and self.codes.shape == (self.n, self.k)
-              and self.codes.is_contiguous(), "weight.codes must be contiguous uint8 [n, k]")
-        _need(isinstance(self.scales, torch.Tensor) and self.scales.dtype == torch.float32
-              and self.scales.device == dev and self.scales.is_contiguous()
-              and self.scales.shape == (-(-self.n // FP8B_BLOCK), -(-self.k // FP8B_BLOCK)),
-              f"weight.scales must be contiguous float32 [ceil(n/128), ceil(k/128)] on {dev}")
+        codes, scales = self.codes, self.scales
+        dev, shape = _cuda(codes, "weight.codes"), (self.n, self.k)
+        if not (_is(codes, _U8, dev, shape) and codes.is_contiguous()):
+            _refuse("weight.codes", codes, _U8, dev, shape, ", contiguous")
+        shape = ((self.n + 127) // FP8B_BLOCK, (self.k + 127) // FP8B_BLOCK)
+        if not (_is(scales, _F32, dev, shape) and scales.is_contiguous()):
+            _refuse("weight.scales", scales, _F32, dev, shape, ", contiguous")
         return dev
 
-    def c(self) -> _Fp8BlockWeight:
-        return _Fp8BlockWeight(self.codes.data_ptr(), self.scales.data_ptr(), self.n, self.k)
+    def c(self) -> bytes:
+        return _PACK_WEIGHT(self.codes.data_ptr(), self.scales.data_ptr(), self.n, self.k)
 
 
 @dataclass
@@ -630,59 +696,34 @@ class Fp8BlockActs:
 
     def check(self) -> torch.device:
         """Tensors consistent with (m, k) on one CUDA device; returns it."""
-        dev = _cuda_device(self.codes, "acts.codes")
-        _need(self.codes.dtype == torch.uint8 and self.codes.shape == (self.m, self.k)
-              and _rows(self.codes), "acts.codes must be uint8 [m, k] with unit column stride")
-        _need(isinstance(self.scales, torch.Tensor) and self.scales.dtype == torch.float32
-              and self.scales.device == dev and _rows(self.scales)
-              and self.scales.shape == (-(-self.k // FP8B_BLOCK), self.m),
-              f"acts.scales must be float32 [ceil(k/128), m] with unit column stride on {dev}")
+        codes, scales = self.codes, self.scales
+        dev, shape = _cuda(codes, "acts.codes"), (self.m, self.k)
+        if not _is_rows(codes, _U8, dev, shape):
+            _refuse("acts.codes", codes, _U8, dev, shape, _ROWS)
+        shape = ((self.k + 127) // FP8B_BLOCK, self.m)
+        if not _is_rows(scales, _F32, dev, shape):
+            _refuse("acts.scales", scales, _F32, dev, shape, _ROWS)
         return dev
 
-    def c(self) -> _Fp8BlockActs:
-        return _Fp8BlockActs(self.codes.data_ptr(), _ld(self.codes), self.scales.data_ptr(),
-                             _ld(self.scales), self.m, self.k)
-
-
-def _rows(t) -> bool:
-    """A 2-D tensor with unit column stride whose rows do not overlap."""
-    return t.dim() == 2 and (t.stride(1) == 1 or t.shape[1] <= 1) and \
-        (t.stride(0) >= t.shape[1] or t.shape[0] <= 1)
-
-
-def _ld(t) -> int:
-    """Row stride for the library: a single row's is its length rounded up to a
-    multiple of 16 (torch leaves the stride of an extent of 1 arbitrary)."""
-    return t.stride(0) if t.shape[0] > 1 else (t.shape[1] + 15) // 16 * 16
-
-
-def _run(call, device, stream, dev_status, *args):
-    """Call the library on `device` with args and an exec of the stream."""
-    if dev_status is not None:
-        _check_tensor(dev_status, "dev_status", torch.int32, device, (1,))
-    f = getattr(load(), call)
-    st = dev_status.data_ptr() if dev_status is not None else None
-    if torch.cuda.current_device() == device.index:
-        rc = f(*args, ctypes.byref(_Exec(_stream(stream), None, 0, st)))
-    else:
-        with torch.cuda.device(device):
-            rc = f(*args, ctypes.byref(_Exec(_stream(stream), None, 0, st)))
-    _check(call, rc)
+    def c(self) -> bytes:
+        return _PACK_ACTS(self.codes.data_ptr(), _ld(self.codes), self.scales.data_ptr(),
+                          self.scales.stride(0) if self.k > FP8B_BLOCK else self.m, self.m, self.k)
 
 
 def fp8b_quantize(w: torch.Tensor, out: Optional[Fp8BlockWeight] = None, stream=None,
                   dev_status: Optional[torch.Tensor] = None) -> Fp8BlockWeight:
     """BF16 [n, k] (rows may be padded) -> E4M3 codes [n, k] and one FP32 scale per
     128 x 128 block.  k is a multiple of 16."""
-    dev = _cuda_device(w, "w")
-    _check_tensor(w, "w", torch.bfloat16, dev, (0, 0))
+    dev = _cuda(w, "w")
+    if w.dim() != 2 or not _is_rows(w, _BF16, dev, w.shape):
+        _refuse("w", w, _BF16, dev, ("n", "k"), _ROWS)
     n, k = w.shape
     if out is None:
-        out = Fp8BlockWeight(torch.empty((n, k), dtype=torch.uint8, device=dev),
-                             torch.empty((-(-n // FP8B_BLOCK), -(-k // FP8B_BLOCK)),
-                                         dtype=torch.float32, device=dev), n, k)
-    _need(out.n == n and out.k == k, "out must be a weight of the same [n, k]")
-    _need(out.check() == dev, f"out must be on {dev}")
+        out = Fp8BlockWeight(torch.empty((n, k), dtype=_U8, device=dev),
+                             torch.empty(((n + 127) // FP8B_BLOCK, (k + 127) // FP8B_BLOCK),
+                                         dtype=_F32, device=dev), n, k)
+    elif out.n != n or out.k != k or out.check() != dev:
+        raise ValueError(f"out must be a weight of [{n}, {k}] on {dev}")
     _run("fp8b_quantize", dev, stream, dev_status, w.data_ptr(), n, k, _ld(w),
          out.codes.data_ptr(), out.scales.data_ptr())
     return out
@@ -698,34 +739,33 @@ def fp8b_rmsnorm(x: torch.Tensor, gamma: Optional[torch.Tensor], eps: float = 1e
     a residual.  x, residual BF16 [m, k]; gamma BF16 [k], or None for no norm (y = h).
 
     ``residual_out`` (default: a new tensor) may be ``residual`` or ``x`` itself."""
-    dev = _cuda_device(x, "x")
-    _check_tensor(x, "x", torch.bfloat16, dev, (0, 0))
-    m, k = x.shape
+    dev = _cuda(x, "x")
+    shape = x.shape
+    if len(shape) != 2 or not _is_rows(x, _BF16, dev, shape):
+        _refuse("x", x, _BF16, dev, ("m", "k"), _ROWS)
+    m, k = shape
+    gp = rp = op = ld_r = ld_o = 0
     if gamma is not None:
-        _check_tensor(gamma, "gamma", torch.bfloat16, dev, (k,), contiguous=True)
-        _need(gamma.shape[0] == k, f"gamma must have {k} elements")
+        if not (_is(gamma, _BF16, dev, (k,)) and (gamma.stride(0) == 1 or k == 1)):
+            _refuse("gamma", gamma, _BF16, dev, (k,), ", contiguous")
+        gp = gamma.data_ptr()
     if residual is not None:
-        _check_tensor(residual, "residual", torch.bfloat16, dev, (m, k))
-        _need(residual.shape == x.shape, "residual must have the shape of x")
+        if not _is_rows(residual, _BF16, dev, shape):
+            _refuse("residual", residual, _BF16, dev, shape, _ROWS)
+        rp, ld_r = residual.data_ptr(), _ld(residual)
         if residual_out is None:
-            residual_out = torch.empty((m, k), dtype=torch.bfloat16, device=dev)
+            residual_out = torch.empty(shape, dtype=_BF16, device=dev)
     if residual_out is not None:
-        _check_tensor(residual_out, "residual_out", torch.bfloat16, dev, (m, k))
-        _need(residual_out.shape == x.shape, "residual_out must have the shape of x")
+        if not _is_rows(residual_out, _BF16, dev, shape):
+            _refuse("residual_out", residual_out, _BF16, dev, shape, _ROWS)
+        op, ld_o = residual_out.data_ptr(), _ld(residual_out)
     if out is None:
-        out = Fp8BlockActs(torch.empty((m, k), dtype=torch.uint8, device=dev),
-                           torch.empty((-(-k // FP8B_BLOCK), m), dtype=torch.float32, device=dev),
-                           m, k)
-    else:
-        _need(out.m == m and out.k == k, "out must be activations of the same [m, k]")
-        _need(out.check() == dev, f"out must be on {dev}")
-    inp = _NormInput(x.data_ptr(), _ld(x),
-                     residual.data_ptr() if residual is not None else None,
-                     _ld(residual) if residual is not None else 0,
-                     residual_out.data_ptr() if residual_out is not None else None,
-                     _ld(residual_out) if residual_out is not None else 0,
-                     gamma.data_ptr() if gamma is not None else None, float(eps))
-    _run("fp8b_rmsnorm", dev, stream, dev_status, ctypes.byref(inp), ctypes.byref(out.c()))
+        out = Fp8BlockActs(torch.empty(shape, dtype=_U8, device=dev),
+                           torch.empty(((k + 127) // FP8B_BLOCK, m), dtype=_F32, device=dev), m, k)
+    elif out.m != m or out.k != k or out.check() != dev:
+        raise ValueError(f"out must be activations of [{m}, {k}] on {dev}")
+    _run("fp8b_rmsnorm", dev, stream, dev_status,
+         _PACK_NORM(x.data_ptr(), _ld(x), rp, ld_r, op, ld_o, gp, eps), out.c())
     return out, residual_out
 
 
@@ -735,16 +775,20 @@ def fp8b_gemm(acts: Fp8BlockActs, weight: Fp8BlockWeight, out_dtype=torch.bfloat
     """C[m, n] = acts . weight^T in BF16 or FP32 (FP32 accumulation), for one row
     or thousands."""
     dev = weight.check()
-    _need(acts.check() == dev, f"acts must be on {dev}")
-    _need(acts.k == weight.k, f"acts must have k = {weight.k} columns, got {acts.k}")
+    if acts.check() != dev:
+        raise ValueError(f"acts must be on {dev}")
+    if acts.k != weight.k:
+        raise ValueError(f"acts must have k = {weight.k} columns, got {acts.k}")
+    shape = (acts.m, weight.n)
+    dt = out_dtype if out is None else out.dtype
+    if dt is not _BF16 and dt is not _F32:
+        raise ValueError("out must be float32 or bfloat16")
     if out is None:
-        out = torch.empty((acts.m, weight.n), dtype=out_dtype, device=dev)
-    _need(out.dtype in (torch.float32, torch.bfloat16), "out must be float32 or bfloat16")
-    _check_tensor(out, "out", out.dtype, dev, (acts.m, weight.n))
-    dt = DTYPE_F32 if out.dtype == torch.float32 else DTYPE_BF16
-    ldc = out.stride(0) if out.shape[0] > 1 else out.shape[1]
-    _run("fp8b_gemm", dev, stream, dev_status, ctypes.byref(acts.c()), ctypes.byref(weight.c()),
-         out.data_ptr(), dt, ldc)
+        out = torch.empty(shape, dtype=dt, device=dev)
+    elif not _is_rows(out, dt, dev, shape):
+        _refuse("out", out, dt, dev, shape, _ROWS)
+    _run("fp8b_gemm", dev, stream, dev_status, acts.c(), weight.c(), out.data_ptr(),
+         DTYPE_F32 if dt is _F32 else DTYPE_BF16, out.stride(0) if shape[0] > 1 else shape[1])
     return out
 
 
@@ -763,45 +807,48 @@ def spec_verify(target_probs: torch.Tensor, draft_tokens: torch.Tensor, accept_u
     [batch, g]; accept_u FP32 [batch, g] and sample_u FP32 [batch] uniform in [0, 1);
     num_draft int32 [batch]: drafts per sequence (default g; negative: the sequence
     is absent and its outputs are left as they were)."""
-    dev = _cuda_device(target_probs, "target_probs")
-    dt = target_probs.dtype
-    _need(dt in (torch.float32, torch.bfloat16), "target_probs must be float32 or bfloat16")
-    _need(target_probs.dim() == 3 and target_probs.shape[1] >= 1,
-          "target_probs must be [batch, g + 1, vocab]")
-    b, g, v = target_probs.shape[0], target_probs.shape[1] - 1, target_probs.shape[2]
-    _need(target_probs.stride(2) == 1 or v == 1, "target_probs must have unit vocabulary stride")
-    _check_tensor(draft_tokens, "draft_tokens", torch.int32, dev, (b, g))
-    _need(draft_tokens.shape == (b, g), f"draft_tokens must be [{b}, {g}]")
-    _check_tensor(accept_u, "accept_u", torch.float32, dev, (b, g))
-    _check_tensor(sample_u, "sample_u", torch.float32, dev, (b,))
-    dv = 0
+    dev = _cuda(target_probs, "target_probs")
+    dt, dims = target_probs.dtype, target_probs.shape
+    if dt is not _F32 and dt is not _BF16:
+        raise ValueError("target_probs must be float32 or bfloat16")
+    if len(dims) != 3 or dims[1] < 1 or (target_probs.stride(2) != 1 and dims[2] != 1):
+        _refuse("target_probs", target_probs, dt, dev, ("batch", "g + 1", "vocab"),
+                " with unit stride along the vocabulary")
+    b, g, v = dims[0], dims[1] - 1, dims[2]
+    if not _is_rows(draft_tokens, _I32, dev, (b, g)):
+        _refuse("draft_tokens", draft_tokens, _I32, dev, (b, g), _ROWS)
+    if not _is_rows(accept_u, _F32, dev, (b, g)):
+        _refuse("accept_u", accept_u, _F32, dev, (b, g), _ROWS)
+    if not (_is(sample_u, _F32, dev, (b,)) and (sample_u.stride(0) == 1 or b == 1)):
+        _refuse("sample_u", sample_u, _F32, dev, (b,), ", contiguous")
+    qp = q_seq = q_pos = dv = 0
     if draft_probs is not None:
-        _need(isinstance(draft_probs, torch.Tensor) and draft_probs.dtype == dt
-              and draft_probs.device == dev, f"draft_probs must be {dt} on {dev}")
-        _need(draft_probs.dim() == 3 and draft_probs.shape[:2] == (b, g),
-              f"draft_probs must be [{b}, {g}, draft_vocab]")
-        dv = draft_probs.shape[2]
-        _need(1 <= dv <= v, f"draft_probs must score 1 to {v} tokens")
-        _need(draft_probs.stride(2) == 1 or dv == 1, "draft_probs must have unit vocabulary stride")
+        dv = draft_probs.shape[-1] if isinstance(draft_probs, torch.Tensor) and draft_probs.dim() else 0
+        if not _is(draft_probs, dt, dev, (b, g, dv)) or not 1 <= dv <= v \
+                or (draft_probs.stride(2) != 1 and dv != 1):
+            _refuse("draft_probs", draft_probs, dt, dev, (b, g, f"1..{v}"),
+                    " with unit stride along the vocabulary")
+        if g:
+            qp, q_seq, q_pos = draft_probs.data_ptr(), draft_probs.stride(0), draft_probs.stride(1)
+    np_ = 0
     if num_draft is not None:
-        _check_tensor(num_draft, "num_draft", torch.int32, dev, (b,))
+        if not (_is(num_draft, _I32, dev, (b,)) and (num_draft.stride(0) == 1 or b == 1)):
+            _refuse("num_draft", num_draft, _I32, dev, (b,), ", contiguous")
+        np_ = num_draft.data_ptr()
     if out_tokens is None:
-        out_tokens = torch.empty((b, g + 1), dtype=torch.int32, device=dev)
+        out_tokens = torch.empty((b, g + 1), dtype=_I32, device=dev)
     else:
-        _check_tensor(out_tokens, "out_tokens", torch.int32, dev, (b, g + 1))
+        _check_tensor(out_tokens, "out_tokens", _I32, dev, (b, g + 1))
     if out_accepted is None:
-        out_accepted = torch.empty(b, dtype=torch.int32, device=dev)
+        out_accepted = torch.empty((b,), dtype=_I32, device=dev)
     else:
-        _check_tensor(out_accepted, "out_accepted", torch.int32, dev, (b,))
-    inp = _VerifyInput(target_probs.data_ptr(), target_probs.stride(0), target_probs.stride(1),
-                       draft_probs.data_ptr() if dv and g else None,
-                       draft_probs.stride(0) if dv else 0, draft_probs.stride(1) if dv else 0, dv,
-                       DTYPE_F32 if dt == torch.float32 else DTYPE_BF16,
-                       draft_tokens.data_ptr() if g else None,
-                       draft_tokens.stride(0) if b > 1 else g,
-                       num_draft.data_ptr() if num_draft is not None else None,
-                       accept_u.data_ptr() if g else None, accept_u.stride(0) if b > 1 else g,
+        _check_tensor(out_accepted, "out_accepted", _I32, dev, (b,))
+    one = b == 1  # torch leaves the stride of an extent of 1 arbitrary
+    inp = _PACK_VERIFY(target_probs.data_ptr(), target_probs.stride(0), target_probs.stride(1),
+                       qp, q_seq, q_pos, dv, DTYPE_F32 if dt is _F32 else DTYPE_BF16,
+                       draft_tokens.data_ptr() if g else 0, g if one else draft_tokens.stride(0),
+                       np_, accept_u.data_ptr() if g else 0, g if one else accept_u.stride(0),
                        sample_u.data_ptr(), b, g, v)
-    _run("spec_verify", dev, stream, dev_status, ctypes.byref(inp), out_tokens.data_ptr(),
-         out_tokens.stride(0) if b > 1 else out_tokens.shape[1], out_accepted.data_ptr())
+    _run("spec_verify", dev, stream, dev_status, inp, out_tokens.data_ptr(),
+         out_tokens.shape[1] if one else out_tokens.stride(0), out_accepted.data_ptr())
     return out_tokens, out_accepted
