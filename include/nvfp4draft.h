@@ -340,6 +340,8 @@ int fp8w_gemv_argmax_ex(const w4a16_act_segment *seg, int nseg, int m, const fp8
 #define FP8B_MAX_K 32768
 /* Most drafted tokens per sequence of spec_verify. */
 #define SPEC_MAX_DRAFT 1024
+/* Largest vocabulary of spec_verify. */
+#define SPEC_MAX_VOCAB (1 << 30)
 
 /* A block-scaled FP8 weight: E4M3 codes [n, k] row-major, 16-byte aligned; one
  * FP32 scale per block of 128 rows and 128 columns (the last blocks may be
@@ -443,7 +445,7 @@ typedef struct spec_verify_input {
     const float *sample_u;    /* [batch] uniform numbers in [0, 1)              */
     int64_t batch;            /* >= 1                                           */
     int64_t g;                /* 0..SPEC_MAX_DRAFT                              */
-    int64_t vocab;            /* 1..2^31-1                                      */
+    int64_t vocab;            /* 1..SPEC_MAX_VOCAB                              */
 } spec_verify_input;
 
 /*

@@ -356,7 +356,7 @@ int spec_verify(const spec_verify_input* in, int32_t* out_tokens, int64_t ld_out
     return NVFP4_ERR_NULL;
   if (in->dtype != NVFP4_DTYPE_F32 && in->dtype != NVFP4_DTYPE_BF16) return NVFP4_ERR_DTYPE;
   if (in->batch < 1 || in->g < 0 || in->g > SPEC_MAX_DRAFT || in->vocab < 1 ||
-      in->vocab > 0x7FFFFFFF || in->ld_target_seq < 0 || in->ld_target_pos < 0 ||
+      in->vocab > SPEC_MAX_VOCAB || in->ld_target_seq < 0 || in->ld_target_pos < 0 ||
       ld_out < in->g + 1)
     return NVFP4_ERR_SHAPE;
   if (in->g > 0 && (in->ld_tokens < in->g || in->ld_accept_u < in->g)) return NVFP4_ERR_SHAPE;

@@ -92,43 +92,83 @@ __device__ __forceinline__ uint2 codes_of(uint4 v, float s, bool fast, uint64_t 
   return codes_exact(v, s);
 }
 
-// The same for eight binary32 values y (fast: s in [2^-126, 2^126]).
-__device__ __forceinline__ uint2 codes_of(const float (&y)[8], float s, bool fast, uint64_t rlo2,
-                                          uint64_t rhi2) {
-  if (s == 0.0f) return make_uint2(0u, 0u);
-  uint32_t lo[4], hi[4];
-  bool ok = fast;
-#pragma unroll
-  for (int j = 0; j < 4; ++j) {
-    uint64_t y2;
-    asm("mov.b64 %0, {%1, %2};" : "=l"(y2) : "f"(y[2 * j]), "f"(y[2 * j + 1]));
-    lo[j] = e4m3_pair2(mul_rz_f32x2(y2, rlo2));
-    hi[j] = e4m3_pair2(mul_rz_f32x2(y2, rhi2));
-    ok = ok && lo[j] == hi[j];
-  }
-  if (!ok) {
-#pragma unroll
-    for (int j = 0; j < 4; ++j)
-      lo[j] = e4m3_pair(__fdiv_rn(y[2 * j], s), __fdiv_rn(y[2 * j + 1], s));
-  }
-  return make_uint2(lo[0] | lo[1] << 16, lo[2] | lo[3] << 16);
-}
-
-// The scale of a block or row group and the reciprocal bounds its codes are
-// decided with.  With s in [2^-126, 2^126], 1/s is normal and finite and
-// rlo <= 1/s, rhi >= (1 + 2^-22)/s.
+// ---- block scales: quotients without a division per element
+//
+// s = RN(amax / 448), and each code from q = q0 + (x - s q0) y with y = 1/s to within
+// an ulp, q0 = RN(x y) (one step of Markstein, "Computation of elementary functions
+// on the IBM RISC System/6000 processor", 1990): the remainder is exact to 2^-23 of
+// an ulp of q, so q = RN(x/s + e), |e| < 2^-20 ulp.  For BF16 x and amax that is
+// fl32(x/s) wherever it decides a code: x and amax have 8 bits and a code border M
+// five, so where x/s is nearer than 2^-13 to M it is M (amax/448)/s, whose distance
+// from M in ulps is a multiple of about 2^-8 and never half of one.  For FP32 x (a
+// normalised row) q is fl32(x/s) but for a share of about 2^-20 of the quotients that
+// lie next to a border, themselves about 2^-19 of all.
+// fast: amax in [2^-80, 2^127), where no remainder that can decide a code
+// (|q| >= 2^-10) leaves binary32's normal range; divisions otherwise.
+// (A rounding test with a division in doubt, as above, costs more here: up to a per
+// cent of the quotients of BF16 values by a BF16 maximum lie on a border exactly.)
 struct Scale {
   float s;
   bool fast;
-  uint64_t rlo, rhi;
+  uint64_t y, neg;  // 1/s and -s, as pairs
 };
 __device__ __forceinline__ Scale scale_of(float amax) {
-  Scale r;
-  r.s = __fdiv_rn(amax, 448.0f);
-  r.fast = r.s >= 0x1p-126f && r.s <= 0x1p126f;
-  r.rlo = f32x2_splat(r.fast ? __frcp_rd(r.s) : 0.0f);
-  r.rhi = f32x2_splat(r.fast ? __fmul_ru(__frcp_ru(r.s), 1.0f + 0x1p-22f) : 0.0f);
+  Scale o;
+  o.fast = amax >= 0x1p-80f && amax < 0x1p127f;
+  constexpr float c = 1.0f / 448.0f;
+  const float q = amax * c;
+  o.s = o.fast ? fmaf(fmaf(-448.0f, q, amax), c, q) : __fdiv_rn(amax, 448.0f);
+  float y;
+  asm("rcp.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"(o.s));
+  o.y = f32x2_splat(y);
+  o.neg = f32x2_splat(-o.s);
+  return o;
+}
+__device__ __forceinline__ uint64_t mul_f32x2(uint64_t a, uint64_t b) {
+  uint64_t r;
+  asm("mul.rn.f32x2 %0, %1, %2;" : "=l"(r) : "l"(a), "l"(b));
   return r;
+}
+__device__ __forceinline__ uint64_t fma_f32x2(uint64_t a, uint64_t b, uint64_t c) {
+  uint64_t r;
+  asm("fma.rn.f32x2 %0, %1, %2, %3;" : "=l"(r) : "l"(a), "l"(b), "l"(c));
+  return r;
+}
+__device__ __forceinline__ void unpack_f32x2(uint64_t v, float& a, float& b) {
+  asm("mov.b64 {%0, %1}, %2;" : "=f"(a), "=f"(b) : "l"(v));
+}
+// Eight codes of four pairs (first element in the lowest byte).
+__device__ __forceinline__ uint2 codes_of(const uint64_t (&x)[4], const Scale& sc) {
+  uint32_t c[4];
+  if (sc.fast) {
+#pragma unroll
+    for (int j = 0; j < 4; ++j) {
+      const uint64_t q = mul_f32x2(x[j], sc.y);
+      c[j] = e4m3_pair2(fma_f32x2(fma_f32x2(sc.neg, q, x[j]), sc.y, q));
+    }
+  } else if (sc.s == 0.0f) {
+    return make_uint2(0u, 0u);
+  } else {
+#pragma unroll
+    for (int j = 0; j < 4; ++j) {
+      float a, b;
+      unpack_f32x2(x[j], a, b);
+      c[j] = e4m3_pair(__fdiv_rn(a, sc.s), __fdiv_rn(b, sc.s));
+    }
+  }
+  return make_uint2(c[0] | c[1] << 16, c[2] | c[3] << 16);
+}
+__device__ __forceinline__ void pairs_of(uint4 v, uint64_t (&x)[4]) {  // eight BF16 as FP32
+  x[0] = f32x2_of_bf16x2(v.x);
+  x[1] = f32x2_of_bf16x2(v.y);
+  x[2] = f32x2_of_bf16x2(v.z);
+  x[3] = f32x2_of_bf16x2(v.w);
+}
+
+__device__ __forceinline__ uint2 codes_of(uint4 v, const Scale& sc) {
+  uint64_t x[4];
+  pairs_of(v, x);
+  return codes_of(x, sc);
 }
 
 }  // namespace e4m3

@@ -19,11 +19,17 @@ constexpr int kBlock = 128;  // rows and columns of a weight block, columns of a
 // ------------------------------------------------------------ weights
 //
 // One CTA per 128 x 128 block: thread t holds the eight 16-byte vectors of rows
-// t/16 + 16 i, columns 8 (t % 16).., so a warp's load covers two rows x 256
-// bytes and a CTA has 32 KB in flight.
+// t/16 + 16 i, columns 8 (t % 16).., so a warp's load covers two rows x 256 bytes and
+// a CTA has 32 KB in flight.  Bound by HBM (3 bytes an element) once the quotients
+// cost few instructions: 151936 x 5120 takes 363 us, 6.44 TB/s, 0.95 of the measured
+// copy; with a rounding test and a division in doubt it took 432, with a second
+// correction step of the quotient 404.  Measured and not kept: a persistent CTA with
+// a TMA ring of blocks (390 us even without the quotients), 512 threads a block (377),
+// four CTAs an SM (392).
 constexpr int kQThreads = 256;
+constexpr int kQVecs = kBlock * kBlock / 8 / kQThreads;  // vectors of a thread
 
-__global__ void __launch_bounds__(kQThreads)
+__global__ void __launch_bounds__(kQThreads, 3)
 fp8b_quantize_kernel(const uint4* __restrict__ w, int64_t n, int64_t k, int64_t ldv,
                      uint2* __restrict__ codes, float* __restrict__ scales, int64_t kblocks,
                      int32_t* dev_status) {
@@ -32,15 +38,15 @@ fp8b_quantize_kernel(const uint4* __restrict__ w, int64_t n, int64_t k, int64_t 
   const int64_t col = bk * (kBlock / 8) + (threadIdx.x & 15);
   const int64_t row0 = bn * kBlock + (threadIdx.x >> 4);
   const bool colok = col < k / 8;
-  uint4 v[8];
+  uint4 v[kQVecs];
   uint32_t m2 = 0u;
 #pragma unroll
-  for (int i = 0; i < 8; ++i) {
-    const int64_t r = row0 + 16 * i;
+  for (int i = 0; i < kQVecs; ++i) {
+    const int64_t r = row0 + (kQThreads / 16) * i;
     v[i] = colok && r < n ? ld_u4(w + r * ldv + col) : make_uint4(0u, 0u, 0u, 0u);
   }
 #pragma unroll
-  for (int i = 0; i < 8; ++i) m2 = __vmaxu2(m2, mag_max8(v[i]));
+  for (int i = 0; i < kQVecs; ++i) m2 = __vmaxu2(m2, mag_max8(v[i]));
   uint32_t m = __reduce_max_sync(0xFFFFFFFFu, max(m2 & 0xFFFFu, m2 >> 16));
   if ((threadIdx.x & 31) == 0) red[threadIdx.x >> 5] = m;
   __syncthreads();
@@ -53,9 +59,9 @@ fp8b_quantize_kernel(const uint4* __restrict__ w, int64_t n, int64_t k, int64_t 
     if (m >= 0x7F80u) nvfp4::report(dev_status, NVFP4_ERR_NONFINITE);
   }
 #pragma unroll
-  for (int i = 0; i < 8; ++i) {
-    const int64_t r = row0 + 16 * i;
-    if (colok && r < n) codes[r * (k / 8) + col] = codes_of(v[i], sc.s, sc.fast, sc.rlo, sc.rhi);
+  for (int i = 0; i < kQVecs; ++i) {
+    const int64_t r = row0 + (kQThreads / 16) * i;
+    if (colok && r < n) codes[r * (k / 8) + col] = codes_of(v[i], sc);
   }
 }
 
@@ -63,7 +69,15 @@ fp8b_quantize_kernel(const uint4* __restrict__ w, int64_t n, int64_t k, int64_t 
 //
 // T threads per row (a multiple of 32), thread t holding the 8-element vectors
 // t, t + T, ...: sixteen neighbouring threads hold one 128-column group, whose
-// maximum four shuffles give.  blockDim = (T, rows per CTA).
+// maximum four shuffles give.  blockDim = (T, rows per CTA).  Without gamma the
+// groups are independent, and a row is split over gridDim.y CTAs.
+//
+// Bound by HBM (7 bytes an element with the residual) while it stays below about 20
+// instructions an element, hence the packed FP32 and BF16 arithmetic; 32 registers
+// keep 2048 threads on an SM.  8192 x 5120 with residual and gamma takes 45.4 us,
+// 6.49 TB/s, 0.96 of the measured copy (72.5 us with scalar arithmetic, divisions and
+// one vector a thread; a CTA that walks over rows with the next row's loads in flight
+// is slower, 55 us).  One row of 5120: 2.4 us, mostly the launch.
 struct NormParams {
   const uint4* x;
   const uint4* residual;
@@ -74,38 +88,39 @@ struct NormParams {
   int64_t ldx, ldr, ldo, ldc;  // in vectors of 8
   int64_t lds, m;
   int nvec;  // k / 8
-  float eps;
+  float eps, inv_k;
   int32_t* dev_status;
 };
 
-__device__ __forceinline__ void unpack(uint4 v, float (&f)[8]) {
-  const uint32_t u[4] = {v.x, v.y, v.z, v.w};
-#pragma unroll
-  for (int j = 0; j < 4; ++j) {
-    f[2 * j] = __uint_as_float(u[j] << 16);
-    f[2 * j + 1] = __uint_as_float(u[j] & 0xFFFF0000u);
-  }
+// bf16(fl32(a + b)), each half: fl32(a + b) keeps every bit that decides the
+// rounding to BF16 (a and b have 8 bits each), so one rounding gives the same.
+__device__ __forceinline__ uint32_t add_bf16x2(uint32_t a, uint32_t b) {
+  uint32_t d;
+  asm("add.rn.bf16x2 %0, %1, %2;" : "=r"(d) : "r"(a), "r"(b));
+  return d;
 }
-__device__ __forceinline__ uint32_t add_bf16x2(uint32_t a, uint32_t b) {  // bf16(fl32(a + b)), each half
-  const __nv_bfloat162 r =
-      __floats2bfloat162_rn(__uint_as_float(a << 16) + __uint_as_float(b << 16),
-                            __uint_as_float(a & 0xFFFF0000u) + __uint_as_float(b & 0xFFFF0000u));
-  return *reinterpret_cast<const uint32_t*>(&r);
+// max(m, |a|, |b|), NaN if any is
+__device__ __forceinline__ float max_abs(float m, float a, float b) {
+  float d;
+  asm("max.NaN.abs.f32 %0, %1, %2, %3;" : "=f"(d) : "f"(m), "f"(a), "f"(b));
+  return d;
 }
 
 constexpr int kNormMaxThreads = 1024;
 
-template <int V>
-__global__ void __launch_bounds__(kNormMaxThreads)
+// 32 registers a thread; 64 where each holds four vectors
+template <int V, int MAXT>
+__global__ void __launch_bounds__(MAXT, (V == 4 ? 1024 : 2048) / MAXT)
 fp8b_rmsnorm_kernel(const __grid_constant__ NormParams p) {
   __shared__ float part[kNormMaxThreads / 32];
   const int T = blockDim.x, t = threadIdx.x, lane = t & 31;
+  const int c0 = blockIdx.y * V * T + t;  // the thread's first vector
   const int64_t row = (int64_t)blockIdx.x * blockDim.y + threadIdx.y;
   const bool live = row < p.m;
   uint4 h[V];
 #pragma unroll
   for (int i = 0; i < V; ++i) {
-    const int c = t + i * T;
+    const int c = c0 + i * T;
     // not the read-only path: residual_out may be x or residual
     h[i] = live && c < p.nvec ? p.x[row * p.ldx + c] : make_uint4(0u, 0u, 0u, 0u);
   }
@@ -113,7 +128,7 @@ fp8b_rmsnorm_kernel(const __grid_constant__ NormParams p) {
     uint4 r[V];
 #pragma unroll
     for (int i = 0; i < V; ++i) {
-      const int c = t + i * T;
+      const int c = c0 + i * T;
       r[i] = live && c < p.nvec ? p.residual[row * p.ldr + c] : make_uint4(0u, 0u, 0u, 0u);
     }
 #pragma unroll
@@ -124,21 +139,24 @@ fp8b_rmsnorm_kernel(const __grid_constant__ NormParams p) {
   if (p.residual_out != nullptr) {
 #pragma unroll
     for (int i = 0; i < V; ++i) {
-      const int c = t + i * T;
+      const int c = c0 + i * T;
       if (live && c < p.nvec) p.residual_out[row * p.ldo + c] = h[i];
     }
   }
   float rstd = 1.0f;
   bool bad = false;
   if (p.gamma != nullptr) {
-    float ss = 0.0f;
+    uint64_t ss2 = 0ull;
 #pragma unroll
     for (int i = 0; i < V; ++i) {
-      float f[8];
-      unpack(h[i], f);
+      uint64_t f[4];
+      pairs_of(h[i], f);
 #pragma unroll
-      for (int j = 0; j < 8; ++j) ss = fmaf(f[j], f[j], ss);
+      for (int j = 0; j < 4; ++j) ss2 = fma_f32x2(f[j], f[j], ss2);
     }
+    float ss, s1;
+    unpack_f32x2(ss2, ss, s1);
+    ss += s1;
 #pragma unroll
     for (int d = 16; d > 0; d >>= 1) ss += __shfl_xor_sync(0xFFFFFFFFu, ss, d);
     const int warps = T / 32;
@@ -148,34 +166,48 @@ fp8b_rmsnorm_kernel(const __grid_constant__ NormParams p) {
     ss = 0.0f;
     for (int w = 0; w < warps; ++w) ss += mine[w];  // the same order in every thread
     bad = !(ss < __int_as_float(0x7F800000));
-    const float var = __fdiv_rn(ss, (float)(p.nvec * 8)) + p.eps;
-    rstd = var > 0.0f ? __fdiv_rn(1.0f, __fsqrt_rn(var)) : 0.0f;  // an all-zero row with eps 0
+    const float var = fmaf(ss, p.inv_k, p.eps);
+    rstd = var > 0.0f ? rsqrtf(var) : 0.0f;  // an all-zero row with eps 0
   }
+  const uint64_t rstd2 = f32x2_splat(rstd);
 #pragma unroll
   for (int i = 0; i < V; ++i) {
-    const int c = t + i * T;
+    const int c = c0 + i * T;
     const bool ok = live && c < p.nvec;
-    float y[8];
-    unpack(h[i], y);
+    uint64_t y[4];
+    pairs_of(h[i], y);
     if (p.gamma != nullptr) {
-      float g[8];
-      unpack(ok ? ld_u4(p.gamma + c) : make_uint4(0u, 0u, 0u, 0u), g);
+      uint64_t g[4];
+      pairs_of(ok ? ld_u4(p.gamma + c) : make_uint4(0u, 0u, 0u, 0u), g);
 #pragma unroll
-      for (int j = 0; j < 8; ++j) y[j] = (y[j] * rstd) * g[j];
+      for (int j = 0; j < 4; ++j) y[j] = mul_f32x2(mul_f32x2(y[j], rstd2), g[j]);
     }
-    uint32_t mag = 0u;  // magnitudes as bit patterns: NaN and infinity are the largest
+    float mag = 0.0f;
 #pragma unroll
-    for (int j = 0; j < 8; ++j) mag = max(mag, __float_as_uint(y[j]) & 0x7FFFFFFFu);
+    for (int j = 0; j < 4; ++j) {
+      float a, b;
+      unpack_f32x2(y[j], a, b);
+      mag = max_abs(mag, a, b);
+    }
 #pragma unroll
-    for (int d = 8; d > 0; d >>= 1) mag = max(mag, __shfl_xor_sync(0xFFFFFFFFu, mag, d));
-    bad = bad || mag >= 0x7F800000u;
-    const Scale sc = scale_of(__uint_as_float(mag));
+    for (int d = 8; d > 0; d >>= 1) mag = max_abs(mag, __shfl_xor_sync(0xFFFFFFFFu, mag, d), 0.0f);
+    bad = bad || !(mag < __int_as_float(0x7F800000));
+    const Scale sc = scale_of(mag);
     if (ok) {
-      p.codes[row * p.ldc + c] = codes_of(y, sc.s, sc.fast, sc.rlo, sc.rhi);
+      p.codes[row * p.ldc + c] = codes_of(y, sc);
       if ((lane & 15) == 0) p.scales[(int64_t)(c >> 4) * p.lds + row] = sc.s;
     }
   }
   if (live && bad) nvfp4::report(p.dev_status, NVFP4_ERR_NONFINITE);
+}
+
+template <int V, int MAXT>
+int launch_norm(const NormParams& p, int T, cudaStream_t stream) {
+  const int rows = T >= 256 ? 1 : 256 / T;  // of a CTA
+  const int64_t grid = nvfp4::cdiv(p.m, rows);
+  const unsigned cols = p.gamma != nullptr ? 1u : (unsigned)nvfp4::cdiv(p.nvec, V * T);
+  fp8b_rmsnorm_kernel<V, MAXT><<<dim3((unsigned)grid, cols), dim3(T, rows), 0, stream>>>(p);
+  return cudaGetLastError() == cudaSuccess ? NVFP4_OK : NVFP4_ERR_CUDA;
 }
 
 }  // namespace
@@ -207,18 +239,18 @@ int launch_fp8b_rmsnorm(const fp8b_norm_input* in, const fp8b_act* out, int32_t*
   p.m = out->m;
   p.nvec = (int)(out->k / 8);
   p.eps = in->eps;
+  p.inv_k = 1.0f / (float)out->k;
   p.dev_status = dev_status;
-  const int v = p.nvec <= 1024 ? 1 : p.nvec <= 2048 ? 2 : 4;
-  const int T = (int)nvfp4::cdiv(nvfp4::cdiv(p.nvec, v), 32) * 32;
-  const int rows = T >= 256 ? 1 : 256 / T;
-  const int64_t grid = nvfp4::cdiv(p.m, rows);
-  if (grid > 0x7FFFFFFF) return NVFP4_ERR_SHAPE;
-  const dim3 block(T, rows);
-  if (v == 1)
-    fp8b_rmsnorm_kernel<1><<<(unsigned)grid, block, 0, stream>>>(p);
-  else if (v == 2)
-    fp8b_rmsnorm_kernel<2><<<(unsigned)grid, block, 0, stream>>>(p);
-  else
-    fp8b_rmsnorm_kernel<4><<<(unsigned)grid, block, 0, stream>>>(p);
-  return cudaGetLastError() == cudaSuccess ? NVFP4_OK : NVFP4_ERR_CUDA;
+  const int warps = (int)nvfp4::cdiv(p.nvec, 32);  // one vector per thread
+  if (p.gamma == nullptr) return launch_norm<1, 256>(p, warps < 8 ? warps * 32 : 256, stream);
+  // A row on as many threads as it has vectors while rows are few (2.4 us against 2.65
+  // for one row of 5120); two vectors per thread once there are rows for every SM's
+  // 2048 threads (8192 rows: 45.4 us against 57.9); four where 1024 threads would not
+  // reach otherwise.
+  const bool many = p.m > 2 * nvfp4::sm_count();
+  const int v = p.nvec > 2048 ? 4 : p.nvec > 1024 || (many && p.nvec > 256) ? 2 : 1;
+  const int T = (int)nvfp4::cdiv(warps, v) * 32;
+  if (v == 4) return launch_norm<4, 1024>(p, T, stream);
+  if (v == 2) return T <= 320 ? launch_norm<2, 320>(p, T, stream) : launch_norm<2, 1024>(p, T, stream);
+  return T <= 256 ? launch_norm<1, 256>(p, T, stream) : launch_norm<1, 1024>(p, T, stream);
 }

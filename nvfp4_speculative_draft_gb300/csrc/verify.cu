@@ -33,7 +33,6 @@ namespace cg = cooperative_groups;
 constexpr int kThreads = 512;
 constexpr int kWarps = kThreads / 32;
 constexpr int kMaxCluster = 8;
-constexpr int kUnroll = 4;
 
 struct VerifyParams {
   const void* target;
@@ -61,12 +60,16 @@ template <typename T>
 struct Vec;
 template <>
 struct Vec<float> {
-  static constexpr int VE = 4;
+  static constexpr int VE = 4, kUnroll = 4;
   uint4 raw;
   __device__ __forceinline__ void load(const float* p) {
     asm volatile("ld.global.nc.v4.u32 {%0,%1,%2,%3}, [%4];"
                  : "=r"(raw.x), "=r"(raw.y), "=r"(raw.z), "=r"(raw.w)
                  : "l"(p));
+  }
+  __device__ __forceinline__ void load_elements(const float* p) {
+    raw = make_uint4(__float_as_uint(__ldg(p)), __float_as_uint(__ldg(p + 1)),
+                     __float_as_uint(__ldg(p + 2)), __float_as_uint(__ldg(p + 3)));
   }
   __device__ __forceinline__ void get(float (&f)[4]) const {
     f[0] = __uint_as_float(raw.x);
@@ -77,12 +80,19 @@ struct Vec<float> {
 };
 template <>
 struct Vec<__nv_bfloat16> {
-  static constexpr int VE = 8;
+  static constexpr int VE = 8, kUnroll = 2;
   uint4 raw;
   __device__ __forceinline__ void load(const __nv_bfloat16* p) {
     asm volatile("ld.global.nc.v4.u32 {%0,%1,%2,%3}, [%4];"
                  : "=r"(raw.x), "=r"(raw.y), "=r"(raw.z), "=r"(raw.w)
                  : "l"(p));
+  }
+  __device__ __forceinline__ void load_elements(const __nv_bfloat16* p) {
+    const unsigned short* u = reinterpret_cast<const unsigned short*>(p);
+    uint32_t w[4];
+#pragma unroll
+    for (int j = 0; j < 4; ++j) w[j] = (uint32_t)__ldg(u + 2 * j) | (uint32_t)__ldg(u + 2 * j + 1) << 16;
+    raw = make_uint4(w[0], w[1], w[2], w[3]);
   }
   __device__ __forceinline__ void get(float (&f)[8]) const {
     const uint32_t u[4] = {raw.x, raw.y, raw.z, raw.w};
@@ -99,9 +109,9 @@ template <typename T>
 struct Rows {
   const T* p;     // target row
   const T* q;     // draft row or nullptr
-  int64_t vocab;  // elements of p
-  int64_t qn;     // elements of q (0 without)
-  int64_t skip;   // greedy: the refused token, whose weight is max(p - 1, 0); else -1
+  int vocab;      // elements of p (at most 2^30: all indices of a row fit in 32 bits)
+  int qn;         // elements of q (0 without)
+  int skip;       // greedy: the refused token, whose weight is max(p - 1, 0); else -1
   int mis;        // elements from the 16-byte boundary at or before p to p
   bool qvec;      // q has the same misalignment: it can be read as vectors too
 };
@@ -127,10 +137,11 @@ __device__ __forceinline__ Sum warp_sum(Sum v) {  // the same value and order in
   return v;
 }
 
-// Inclusive prefix over the lanes, binary64.
-__device__ __forceinline__ double warp_prefix(double v, int lane) {
+// Inclusive prefix over the first N lanes (a power of two), binary64.
+template <int N>
+__device__ __forceinline__ double prefix(double v, int lane) {
 #pragma unroll
-  for (int d = 1; d < 32; d <<= 1) {
+  for (int d = 1; d < N; d <<= 1) {
     const double o = __shfl_up_sync(0xFFFFFFFFu, v, d);
     if (lane >= d) v += o;
   }
@@ -153,13 +164,13 @@ __device__ __forceinline__ void weight(float p, float q, float& hi, float& lo, b
 // wholly in the target row, wholly in or wholly past the draft's, and clear of
 // the refused token; the others (a few per row) are read element by element.
 template <typename T>
-__device__ __forceinline__ bool inner(const Rows<T>& r, int64_t i) {
+__device__ __forceinline__ bool inner(const Rows<T>& r, int i) {
   constexpr int VE = Vec<T>::VE;
   return i >= 0 && i + VE <= r.vocab && (i >= r.qn || i + VE <= r.qn) &&
          !(r.skip >= i && r.skip < i + VE);
 }
 template <typename T>
-__device__ __forceinline__ void edge_weight(const Rows<T>& r, int64_t i, float& hi, float& lo,
+__device__ __forceinline__ void edge_weight(const Rows<T>& r, int i, float& hi, float& lo,
                                             bool& bad) {
   hi = lo = 0.0f;
   if (i >= 0 && i < r.vocab) {
@@ -167,122 +178,111 @@ __device__ __forceinline__ void edge_weight(const Rows<T>& r, int64_t i, float& 
     weight(load_one(r.p + i), q, hi, lo, bad);
   }
 }
-// The draft's elements i..i+VE-1 (zeros past its end).
-template <typename T>
-__device__ __forceinline__ void load_q(const Rows<T>& r, int64_t i, float (&q)[Vec<T>::VE]) {
-  constexpr int VE = Vec<T>::VE;
-  if (i >= r.qn) {
-#pragma unroll
-    for (int j = 0; j < VE; ++j) q[j] = 0.0f;
-  } else if (r.qvec) {
-    Vec<T> b;
-    b.load(r.q + i);
-    b.get(q);
-  } else {
-#pragma unroll
-    for (int j = 0; j < VE; ++j) q[j] = load_one(r.q + i + j);
-  }
-}
 
-// Sum of the weights of vectors [v0, v1), by one warp.
+// One lane's sum of the weights of vectors v, v + step, ... below end.
 template <typename T>
-__device__ Sum segment_sum(const Rows<T>& r, int64_t v0, int64_t v1, int lane, bool& bad) {
-  constexpr int VE = Vec<T>::VE;
-  Sum sum{0.0f, 0.0f};
-  for (int64_t v = v0 + lane; v < v1; v += 32 * kUnroll) {
-    Vec<T> a[kUnroll];
-    float q[kUnroll][VE];
-    bool in[kUnroll];
+__device__ __forceinline__ Sum lane_sum(const Rows<T>& r, int v, int end, int step, bool& bad) {
+  constexpr int VE = Vec<T>::VE, U = Vec<T>::kUnroll;
+  Sum sum[2] = {{0.0f, 0.0f}, {0.0f, 0.0f}};  // two chains of dependent additions
+  for (; v < end; v += U * step) {
+    Vec<T> a[U], b[U];
+    bool in[U];
 #pragma unroll
-    for (int u = 0; u < kUnroll; ++u) {  // all loads first
-      const int64_t vv = v + 32 * u, i = vv * VE - r.mis;
-      in[u] = vv < v1 && inner(r, i);
+    for (int u = 0; u < U; ++u) {  // all loads first
+      const int vv = v + u * step, i = vv * VE - r.mis;
+      in[u] = vv < end && inner(r, i);
       if (in[u]) {
         a[u].load(r.p + i);
-        load_q(r, i, q[u]);
+        if (i < r.qn) {
+          if (r.qvec)
+            b[u].load(r.q + i);
+          else
+            b[u].load_elements(r.q + i);
+        }
       }
     }
 #pragma unroll
-    for (int u = 0; u < kUnroll; ++u) {
-      const int64_t vv = v + 32 * u;
-      float hi, lo;
+    for (int u = 0; u < U; ++u) {
+      const int vv = v + u * step, i = vv * VE - r.mis;
       if (in[u]) {
-        float p[VE];
+        float p[VE], q[VE];
         a[u].get(p);
+        if (i < r.qn) {
+          b[u].get(q);
 #pragma unroll
-        for (int j = 0; j < VE; ++j) {
-          weight(p[j], q[u][j], hi, lo, bad);
-          sum.add(hi, lo);
+          for (int j = 0; j < VE; ++j) {
+            float hi, lo;
+            weight(p[j], q[j], hi, lo, bad);
+            sum[j & 1].add(hi, lo);
+          }
+        } else {
+#pragma unroll
+          for (int j = 0; j < VE; ++j) {
+            const bool fin = fabsf(p[j]) < __int_as_float(0x7F800000);
+            bad = bad || !fin;
+            sum[j & 1].add(fin ? fmaxf(p[j], 0.0f) : 0.0f, 0.0f);
+          }
         }
-      } else if (vv < v1) {
+      } else if (vv < end) {
 #pragma unroll 1
         for (int j = 0; j < VE; ++j) {
-          edge_weight(r, vv * VE - r.mis + j, hi, lo, bad);
-          sum.add(hi, lo);
+          float hi, lo;
+          edge_weight(r, i + j, hi, lo, bad);
+          sum[0].add(hi, lo);
         }
       }
     }
   }
-  return warp_sum(sum);
+  sum[0].add(sum[1].s, sum[1].c);
+  return sum[0];
 }
 
-// One warp: the first index among vectors [v0, v1) (at most 32) whose running sum
-// from base exceeds t; the last one with a weight where rounding leaves none.
+// The part (lane c < N holding part c's sum) that t falls into: the first whose
+// prefix upto exceeds t, or the last with any mass; -1 without mass.
+__device__ __forceinline__ int pick(double mine, double upto, double t) {
+  const unsigned over = __ballot_sync(0xFFFFFFFFu, mine > 0.0 && upto > t);
+  const unsigned any = __ballot_sync(0xFFFFFFFFu, mine > 0.0);
+  return over != 0u ? __ffs(over) - 1 : 31 - __clz(any);  // (31 - clz(0) = -1)
+}
+// The prefix before part `who`.
+__device__ __forceinline__ double before(double upto, int who, double base) {
+  const double v = __shfl_sync(0xFFFFFFFFu, upto, who > 0 ? who - 1 : 0);
+  return who > 0 ? v : base;
+}
+
+// One warp: the first index among vectors [v0, v1) whose running sum from base
+// exceeds t; the last one with a weight where rounding leaves none.  First over
+// lanes with equal contiguous shares, then over the elements of one share.
+constexpr int kFindElements = 64;  // most elements of a lane's share
 template <typename T>
-__device__ int64_t find_index(const Rows<T>& r, int64_t v0, int64_t v1, double base, double t,
+__device__ int find_index(const Rows<T>& r, int v0, int v1, double base, double t,
                               int lane) {
   constexpr int VE = Vec<T>::VE;
-  float hi[VE], lo[VE];
-  Sum sum{0.0f, 0.0f};
-  int last = -1;
+  const int share = (v1 - v0 + 31) / 32;
   bool bad = false;
-#pragma unroll
-  for (int j = 0; j < VE; ++j) {
-    hi[j] = lo[j] = 0.0f;
-    if (v0 + lane < v1) edge_weight(r, (v0 + lane) * VE - r.mis + j, hi[j], lo[j], bad);
-    sum.add(hi[j], lo[j]);
-    if (hi[j] > 0.0f) last = j;
+  const int mv = min(v1, v0 + lane * share);
+  const double mine = lane_sum(r, mv, min(v1, mv + share), 1, bad).value();
+  const double upto = base + prefix<32>(mine, lane);
+  const int who = pick(mine, upto, t);
+  if (who < 0) return 0;
+  base = before(upto, who, base);
+  const int e0 = (v0 + who * share) * VE - r.mis, e1 = min(v1, v0 + (who + 1) * share) * VE - r.mis;
+  int last = 0;
+  for (int e = e0; e < e1; e += 32) {
+    float hi = 0.0f, lo = 0.0f;
+    if (e + lane < e1) edge_weight(r, e + lane, hi, lo, bad);
+    const double w = (double)hi + (double)lo;
+    const double run = base + prefix<32>(w, lane);
+    const int at = pick(w, run, t);
+    if (at >= 0) last = e + at;
+    base = __shfl_sync(0xFFFFFFFFu, run, 31);
+    if (__any_sync(0xFFFFFFFFu, w > 0.0 && run > t)) break;
   }
-  const double mine = sum.value();
-  const double upto = base + warp_prefix(mine, lane);
-  const unsigned over = __ballot_sync(0xFFFFFFFFu, last >= 0 && upto > t);
-  const unsigned any = __ballot_sync(0xFFFFFFFFu, last >= 0);
-  if (any == 0u) return 0;
-  const int who = over != 0u ? __ffs(over) - 1 : 31 - __clz(any);
-  int at = last;
-  if (lane == who) {
-    double run = upto - mine;
-    bool found = false;
-#pragma unroll
-    for (int j = 0; j < VE; ++j) {
-      run += (double)hi[j] + (double)lo[j];
-      if (!found && hi[j] > 0.0f && run > t) {
-        found = true;
-        at = j;
-      }
-    }
-  }
-  return (v0 + who) * VE - r.mis + __shfl_sync(0xFFFFFFFFu, at, who);
-}
-
-// The part (of n <= 32, lane c holding part c's sum) that t falls into, counting
-// from base: the first whose prefix exceeds t, or the last with any mass.  -1: no
-// mass.  start: the prefix before it.  The same answer in every lane.
-__device__ __forceinline__ int pick_part(double mine, int n, double base, double t, int lane,
-                                         double& start) {
-  const double upto = base + warp_prefix(lane < n ? mine : 0.0, lane);
-  const bool mass = lane < n && mine > 0.0;
-  const unsigned over = __ballot_sync(0xFFFFFFFFu, mass && upto > t);
-  const unsigned any = __ballot_sync(0xFFFFFFFFu, mass);
-  if (any == 0u) return -1;
-  const int who = over != 0u ? __ffs(over) - 1 : 31 - __clz(any);
-  const double before = __shfl_up_sync(0xFFFFFFFFu, upto, 1);
-  start = __shfl_sync(0xFFFFFFFFu, lane == 0 ? base : before, who);
-  return who;
+  return last;
 }
 
 template <typename T>
-__global__ void __launch_bounds__(kThreads) spec_verify_kernel(const __grid_constant__ VerifyParams p) {
+__global__ void __launch_bounds__(kThreads, 2) spec_verify_kernel(const __grid_constant__ VerifyParams p) {
   cg::cluster_group cluster = cg::this_cluster();
   const int rank = (int)cluster.block_rank(), ranks = (int)cluster.num_blocks();
   const int64_t seq = blockIdx.x / ranks;
@@ -305,21 +305,24 @@ __global__ void __launch_bounds__(kThreads) spec_verify_kernel(const __grid_cons
   }
   if (warp == 0) {  // the first refusal
     int a = num;
-    for (int i0 = 0; i0 < num; i0 += 32) {
+    for (int i0 = 0; i0 < p.g; i0 += 32) {
       const int i = i0 + lane;
       bool refuse = false;
-      if (i < num) {
+      if (i < p.g) {  // (loads before the comparison with num, which is on its way too)
         const int64_t d = __ldg(tokens + i);
-        refuse = true;
-        if (d >= 0 && d < p.vocab) {
-          const float pd = load_one(target + i * p.ld_tp + d);
-          const float qd = draft == nullptr    ? 1.0f
-                           : d < p.draft_vocab ? load_one(draft + i * p.ld_dp + d)
-                                               : 0.0f;
-          const float u = __ldg(p.accept_u + seq * p.ld_u + i);
-          refuse = !((double)u * (double)qd < (double)pd);  // 48 bits: the product is exact
-        } else if (rank == 0) {
-          nvfp4::report(p.dev_status, NVFP4_ERR_INDEX);
+        const float u = __ldg(p.accept_u + seq * p.ld_u + i);
+        const bool known = d >= 0 && d < p.vocab;
+        if (i < num) {
+          refuse = true;
+          if (known) {
+            const float pd = load_one(target + i * p.ld_tp + d);
+            const float qd = draft == nullptr    ? 1.0f
+                             : d < p.draft_vocab ? load_one(draft + i * p.ld_dp + d)
+                                                 : 0.0f;
+            refuse = !((double)u * (double)qd < (double)pd);  // 48 bits: the product is exact
+          } else if (rank == 0) {
+            nvfp4::report(p.dev_status, NVFP4_ERR_INDEX);
+          }
         }
       }
       const unsigned b = __ballot_sync(0xFFFFFFFFu, refuse);
@@ -327,6 +330,7 @@ __global__ void __launch_bounds__(kThreads) spec_verify_kernel(const __grid_cons
         a = i0 + __ffs(b) - 1;
         break;
       }
+      if (i0 + 32 >= num) break;
     }
     if (lane == 0) s_accepted = a;
     if (rank == 0) {  // everything but the sampled token
@@ -341,40 +345,49 @@ __global__ void __launch_bounds__(kThreads) spec_verify_kernel(const __grid_cons
 
   Rows<T> r;
   r.p = target + a * p.ld_tp;
-  r.vocab = p.vocab;
+  r.vocab = (int)p.vocab;
   r.q = refused && draft != nullptr ? draft + a * p.ld_dp : nullptr;
-  r.qn = r.q != nullptr ? p.draft_vocab : 0;
-  r.skip = refused && draft == nullptr ? (int64_t)__ldg(tokens + a) : -1;
+  r.qn = r.q != nullptr ? (int)p.draft_vocab : 0;
+  r.skip = refused && draft == nullptr ? __ldg(tokens + a) : -1;
   r.mis = (int)((reinterpret_cast<uintptr_t>(r.p) & 15u) / sizeof(T));
   r.qvec = ((reinterpret_cast<uintptr_t>(r.q) ^ reinterpret_cast<uintptr_t>(r.p)) & 15u) == 0;
 
   constexpr int VE = Vec<T>::VE;
-  const int64_t nvec = (r.vocab + r.mis + VE - 1) / VE;
-  const int64_t per_cta = (nvec + ranks - 1) / ranks;
-  int64_t v0 = min(nvec, rank * per_cta), v1 = min(nvec, v0 + per_cta);
+  const int nvec = (r.vocab + r.mis + VE - 1) / VE;
+  const int per_cta = (nvec + ranks - 1) / ranks;
+  int v0 = min(nvec, rank * per_cta), v1 = min(nvec, v0 + per_cta);
 
   bool bad = false;
-  double t = 0.0, base = 0.0;  // warp 0: r W, and the prefix before the share or segment at hand
-  int64_t per = (v1 - v0 + kWarps - 1) / kWarps;  // vectors of a warp's segment
+  double t = 0.0, base = 0.0;  // warp 0: r W, and the prefix before the part at hand
+  int per = (v1 - v0 + kWarps - 1) / kWarps;  // vectors of a warp's segment
   auto sum_parts = [&]() {
-    const int64_t w0 = min(v1, v0 + warp * per);
-    const Sum mine = segment_sum(r, w0, min(v1, w0 + per), lane, bad);
+    const int w0 = min(v1, v0 + warp * per);
+    const Sum mine = warp_sum(lane_sum(r, w0 + lane, min(v1, w0 + per), 32, bad));
     if (lane == 0) part[warp] = mine;
     __syncthreads();
   };
   for (int pass = 0; pass < 2; ++pass) {
     sum_parts();
+    double mine = 0.0, upto = 0.0;  // warp 0: of the CTA's parts
     if (warp == 0) {
-      Sum all = warp_sum(lane < kWarps ? part[lane] : Sum{0.0f, 0.0f});
-      if (lane == 0) cta_sum[pass] = all.value();
+      mine = lane < kWarps ? part[lane].value() : 0.0;
+      upto = prefix<kWarps>(mine, lane);
+      if (lane == kWarps - 1) cta_sum[pass] = upto;
     }
     cluster.sync();
-    if (warp == 0) {  // the CTA that t falls into; every CTA finds the same
-      const double mine = lane < ranks ? *cluster.map_shared_rank(&cta_sum[pass], lane) : 0.0;
-      const double all = __shfl_sync(0xFFFFFFFFu, warp_prefix(mine, lane), 31);
-      t = (double)__ldg(p.sample_u + seq) * all;
+    if (warp == 0) {  // the CTA that t falls into, the same in every CTA; there, the part
+      const double c = lane < ranks ? *cluster.map_shared_rank(&cta_sum[pass], lane) : 0.0;
+      const double cupto = prefix<kMaxCluster>(c, lane);
+      t = (double)__ldg(p.sample_u + seq) * __shfl_sync(0xFFFFFFFFu, cupto, ranks - 1);
       if (t < 0.0) t = 0.0;
-      const int owner = pick_part(mine, ranks, 0.0, t, lane, base);
+      const int owner = pick(c, cupto, t);
+      if (owner == rank) {
+        base = before(cupto, owner, 0.0);
+        upto += base;
+        const int w = max(pick(mine, upto, t), 0);
+        base = before(upto, w, base);
+        if (lane == 0) s_part = w;
+      }
       if (lane == 0) s_owner = owner;
     }
     __syncthreads();
@@ -387,23 +400,23 @@ __global__ void __launch_bounds__(kThreads) spec_verify_kernel(const __grid_cons
     if (rank == 0 && threadIdx.x == 0) p.out[seq * p.ld_out + a] = 0;
   } else if (rank == s_owner) {
     while (true) {  // narrow [v0, v1) to the segment that t falls into
+      v0 = min(v1, v0 + s_part * per);
+      v1 = min(v1, v0 + per);
+      if (v1 - v0 <= 32 * (kFindElements / VE)) break;
+      per = (v1 - v0 + kWarps - 1) / kWarps;
+      sum_parts();
       if (warp == 0) {
-        double start = base;
-        const int w = pick_part(lane < kWarps ? part[lane].value() : 0.0, kWarps, base, t, lane, start);
-        base = start;
+        const double mine = lane < kWarps ? part[lane].value() : 0.0;
+        const double upto = base + prefix<kWarps>(mine, lane);
+        const int w = max(pick(mine, upto, t), 0);
+        base = before(upto, w, base);
         if (lane == 0) s_part = w;
       }
       __syncthreads();
-      const int w = max(s_part, 0);
-      v0 = min(v1, v0 + w * per);
-      v1 = min(v1, v0 + per);
-      if (v1 - v0 <= 32) break;
-      per = (v1 - v0 + kWarps - 1) / kWarps;
-      sum_parts();
     }
     if (warp == 0) {
-      const int64_t j = find_index(r, v0, v1, base, t, lane);
-      if (lane == 0) p.out[seq * p.ld_out + a] = (int32_t)j;
+      const int j = find_index(r, v0, v1, base, t, lane);
+      if (lane == 0) p.out[seq * p.ld_out + a] = j;
     }
   }
   if (bad) nvfp4::report(p.dev_status, NVFP4_ERR_NONFINITE);

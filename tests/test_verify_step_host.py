@@ -87,7 +87,7 @@ def verify_input(**kw):
     (dict(target=None), P, 3, P, 1), (dict(tokens=None), P, 3, P, 1), (dict(accept_u=None), P, 3, P, 1),
     (dict(sample_u=None), P, 3, P, 1), ({}, None, 3, P, 1), ({}, P, 3, None, 1),
     (dict(batch=0), P, 3, P, 2), (dict(g=-1), P, 3, P, 2), (dict(g=1025), P, 1026, P, 2), (dict(vocab=0), P, 3, P, 2),
-    (dict(vocab=2 ** 31), P, 3, P, 2), (dict(draft_vocab=11), P, 3, P, 2), (dict(draft_vocab=0), P, 3, P, 2),
+    (dict(vocab=2 ** 30 + 1), P, 3, P, 2), (dict(draft_vocab=11), P, 3, P, 2), (dict(draft_vocab=0), P, 3, P, 2),
     (dict(ld_tokens=1), P, 3, P, 2), (dict(ld_accept_u=1), P, 3, P, 2), ({}, P, 2, P, 2),
     (dict(target=P + 2), P, 3, P, 3), (dict(target=P + 1, dtype=1), P, 3, P, 3), (dict(draft=P + 2), P, 3, P, 3),
     (dict(tokens=P + 1), P, 3, P, 3), (dict(num_draft=P + 1), P, 3, P, 3), ({}, P + 2, 3, P, 3), ({}, P, 3, P + 2, 3),
