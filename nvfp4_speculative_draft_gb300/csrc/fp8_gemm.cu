@@ -1,24 +1,27 @@
 // fp8_gemm.cu -- block-scaled FP8 (W8A8) product on the 5th-generation tensor
-// cores (sm_103a), one kernel from one token to prefill sizes.
+// cores (sm_103a), from one token to prefill sizes.
 //
-//   C[m, n] = sum_b sa[b][m] sw[n/128][b] D_b[n, m],  D_b = sum_{i in block b} w[n, i] a[m, i]
+//   C[m, n] = sum_b sa[b][m] sw[n/128][b] D_b[m, n],  D_b = sum_{i in block b} a[m, i] w[n, i]
 //
-// The weights are the MMA's M operand (128 rows: one scale block, so the weight
-// scale is one number per K block of a tile) and TN tokens its N operand, TN from
-// 16 to 256 chosen per call.  D_b is formed by four kind::f8f6f4 MMAs (K = 32 each)
-// into one of a ring of TMEM buffers; the epilogue warps take every D_b out of
-// TMEM and add it, times its scales, to FP32 accumulators in registers (one packed
-// FMA per two elements), while the tensor core forms the next.
-//   warp 0   TMA producer: per K block 128 x 128 weight codes and TN x 128
-//            activation codes (128-byte swizzle; past n, m and k read as 0);
+// D_b is formed by four kind::f8f6f4 MMAs (K = 32 each) into one of a ring of TMEM
+// buffers; the epilogue warps take every D_b out of TMEM and add it, times its
+// scales, to FP32 accumulators in registers (one packed FMA per two elements) while
+// the tensor core forms the next.  Two forms of one kernel:
+//   FEW   the 128 rows of the MMA are weights (one scale block), its N columns
+//         tokens, N = 16, 32 or 64: no tensor work is spent on absent tokens, and the
+//         weight stream, which bounds these sizes, is the same for all;
+//   MANY  the 128 rows are tokens, the N = 128 or 256 columns weights: a thread's
+//         accumulators share one token and one weight block, so one scale per K block.
+//   warp 0   TMA producer: per K block 128 rows of one operand and N of the other,
+//            128 codes each (128-byte swizzle; past n, m and k read as 0);
 //   warp 1   allocates TMEM; one thread issues the MMAs, committing each stage to
 //            its "empty" barrier and each D_b to its "full" barrier;
-//   warp 2   forms the TN products sa sw of each K block in shared memory, loads
+//   warp 2   FEW: forms the N products sa sw of each K block in shared memory, loads
 //            four K blocks ahead in registers;
-//   warps 4..  epilogue: lane = weight row (TMEM lane), columns = tokens.
-// Few output tiles: a cluster of S CTAs splits K, each CTA leaves its partial tile
-// in shared memory and adds a share of the columns over the S partials in rank
-// order (distributed shared memory), so results do not depend on timing.
+//   warps 4..  epilogue, a TMEM lane per thread and up to 128 columns.
+// Few output tiles: a cluster of S CTAs splits K, each CTA leaves its partial tile in
+// shared memory and adds and stores a share of it over the S partials in rank order
+// (distributed shared memory), so results do not depend on timing.
 // Every wait is bounded (2 s of globaltimer): one that runs out records
 // NVFP4_ERR_TIMEOUT in the caller's status word and the CTA unwinds.
 #include <cooperative_groups.h>
@@ -31,29 +34,29 @@ namespace {
 using namespace nvfp4::tc;
 namespace cg = cooperative_groups;
 
-constexpr int kRows = 128;               // weight rows of a tile = rows of a scale block
-constexpr int kK = 128;                  // K block: one swizzled 128-byte row of codes
-constexpr int kWBytes = kRows * kK;      // 16 KB
-constexpr int kSmemRing = 196 * 1024;    // ring of stages, with room for what follows it
-constexpr int kScalePrefetch = 4;        // K blocks of activation scales in flight
+constexpr int kM = 128;                // MMA rows
+constexpr int kK = 128;                // K block: one swizzled 128-byte row of codes
+constexpr int kRing = 196 * 1024;      // most bytes of the ring of stages
+constexpr int kScalePrefetch = 4;      // K blocks of scales in flight
 
-template <int TN>
+template <bool FEW, int N>
 struct Tile {
-  static constexpr int kEpiWarps = TN > 128 ? 8 : 4;
+  static constexpr int kEpiWarps = N > 128 ? 8 : 4;
   static constexpr int kThreads = 128 + 32 * kEpiWarps;
-  static constexpr int kCols = TN / (kEpiWarps / 4);  // columns of one epilogue warp
-  static constexpr int kStageBytes = kWBytes + TN * kK;
-  static constexpr int kStages = kSmemRing / kStageBytes < 10 ? kSmemRing / kStageBytes : 10;
-  static constexpr int kBufs = TN >= 256 ? 2 : TN >= 64 ? 4 : 8;  // TMEM ring
-  static constexpr int kTmemCols = TN * kBufs;
-  static constexpr int kScaleBytes = kBufs * TN * 4;
-  static constexpr bool kSplit = TN <= 64;  // K may be split over a cluster
+  static constexpr int kCols = N > 128 ? N / 2 : N;  // columns of one epilogue warp
+  static constexpr int kTokens = FEW ? N : kM, kOut = FEW ? kM : N;  // of an output tile
+  static constexpr int kABytes = kM * kK, kStageBytes = kABytes + N * kK;
+  static constexpr int kStages = kRing / kStageBytes < 10 ? kRing / kStageBytes : 10;
+  static constexpr int kBufs = N >= 256 ? 2 : N >= 64 ? 4 : 8;  // TMEM ring
+  static constexpr int kTmemCols = N * kBufs;
+  static constexpr bool kSplit = N <= 128;  // K may be split over a cluster
+  static constexpr int kScaleBytes = FEW ? kBufs * N * 4 : 0;
   static constexpr int kBars = 2 * kStages + 3 * kBufs + 1;
   static constexpr size_t kSmemBytes =
       1024 + (size_t)kStages * kStageBytes + kScaleBytes + 8 * kBars + 16;
   static_assert(kTmemCols >= 32 && kTmemCols <= 512 && (kTmemCols & (kTmemCols - 1)) == 0, "TMEM");
   static_assert(kStageBytes % 1024 == 0, "swizzled tiles start on 1 KB");
-  static_assert(TN * 512 <= kStages * kStageBytes, "the partial tile reuses the ring");
+  static_assert(!kSplit || kM * N * 4 <= kStages * kStageBytes, "the partial tile reuses the ring");
   static_assert(kSmemBytes <= 227 * 1024, "shared memory");
 };
 
@@ -64,7 +67,8 @@ struct Params {
   void* c;
   int64_t ldc;
   int64_t m, n;
-  int kblocks, mtiles, items;
+  int kblocks, wblocks, mtiles, items;
+  bool vector_store;  // C is 16-byte aligned, and so are its rows
   int32_t* dev_status;
 };
 
@@ -83,13 +87,83 @@ __device__ __forceinline__ Out* next_token(Out* p, int64_t ld) {
   return p;
 }
 
-template <int TN, typename Out>
-__global__ void __launch_bounds__(Tile<TN>::kThreads, 1)
-fp8b_gemm_kernel(const __grid_constant__ CUtensorMap tmap_w, const __grid_constant__ CUtensorMap tmap_a,
+// FEW: a thread's accumulators are one output column of `left` tokens; a warp's store
+// covers 32 neighbouring outputs of a token.
+template <int N, typename Out>
+__device__ __forceinline__ void store_tokens(const uint64_t (&acc)[N / 2], Out* dst, int64_t ldc, int left) {
+#pragma unroll
+  for (int i = 0; i < N / 2; ++i) {
+    float x0, x1;
+    unpack2(acc[i], x0, x1);
+    if (2 * i < left) *dst = cast<Out>(x0);
+    dst = next_token(dst, ldc);
+    if (2 * i + 1 < left) *dst = cast<Out>(x1);
+    dst = next_token(dst, ldc);
+  }
+}
+
+// MANY: a thread's accumulators are C consecutive outputs of one token.  128 bytes of
+// each row at a time are transposed in 16-byte pieces within groups of eight lanes,
+// so that a store covers four rows x 128 contiguous bytes.
+template <int C, typename Out>
+__device__ __forceinline__ void store_row(const uint64_t (&acc)[C / 2], const Params& p, int64_t row0, int64_t n0,
+                                          int lane) {
+  constexpr int kPiece = 16 / sizeof(Out);  // outputs of a piece
+#pragma unroll
+  for (int g = 0; g < C / (8 * kPiece); ++g) {
+    uint4 P[8];
+#pragma unroll
+    for (int i = 0; i < 8; ++i) {
+      uint32_t w[4];
+#pragma unroll
+      for (int e = 0; e < 4; ++e) {
+        const int at = (g * 8 + i) * kPiece / 2;  // first pair of the piece
+        if constexpr (sizeof(Out) == 4) {
+          float x[2];
+          unpack2(acc[at + e / 2], x[0], x[1]);
+          w[e] = __float_as_uint(x[e & 1]);
+        } else {
+          float x0, x1;
+          unpack2(acc[at + e], x0, x1);
+          const __nv_bfloat162 b = __floats2bfloat162_rn(x0, x1);
+          w[e] = *reinterpret_cast<const uint32_t*>(&b);
+        }
+      }
+      P[i] = make_uint4(w[0], w[1], w[2], w[3]);
+    }
+    transpose_pieces<8>(P, lane);
+    const int64_t col = n0 + (g * 8 + (lane & 7)) * kPiece;
+#pragma unroll
+    for (int i = 0; i < 8; ++i) {
+      const int64_t row = row0 + (lane & ~7) + i;
+      if (row < p.m && col < p.n) {
+        Out* dst = reinterpret_cast<Out*>(p.c) + row * p.ldc + col;
+        if (p.vector_store && col + kPiece <= p.n) {
+          *reinterpret_cast<uint4*>(dst) = P[i];
+        } else {
+          const uint32_t w[4] = {P[i].x, P[i].y, P[i].z, P[i].w};
+#pragma unroll
+          for (int e = 0; e < kPiece; ++e) {
+            if (col + e < p.n) {
+              if constexpr (sizeof(Out) == 4)
+                dst[e] = __uint_as_float(w[e]);
+              else
+                dst[e] = __ushort_as_bfloat16((unsigned short)(w[e / 2] >> (16 * (e & 1))));
+            }
+          }
+        }
+      }
+    }
+  }
+}
+
+template <bool FEW, int N, typename Out>
+__global__ void __launch_bounds__(Tile<FEW, N>::kThreads, 1)
+fp8b_gemm_kernel(const __grid_constant__ CUtensorMap tmap_a, const __grid_constant__ CUtensorMap tmap_b,
                  const __grid_constant__ Params p) {
-  using L = Tile<TN>;
-  constexpr int kStages = L::kStages, kBufs = L::kBufs;
-  constexpr uint32_t kIdesc = idesc_e4m3(kRows, TN);
+  using L = Tile<FEW, N>;
+  constexpr int kStages = L::kStages, kBufs = L::kBufs, kCols = L::kCols;
+  constexpr uint32_t kIdesc = idesc_e4m3(kM, N);
   extern __shared__ unsigned char smem_raw[];
   const uint32_t raw = smem_u32(smem_raw);
   const uint32_t ring = (raw + 1023u) & ~1023u;
@@ -107,11 +181,15 @@ fp8b_gemm_kernel(const __grid_constant__ CUtensorMap tmap_w, const __grid_consta
   volatile uint32_t* abort = tmem_slot + 1;
 
   cg::cluster_group cluster = cg::this_cluster();
-  const int rank = (int)cluster.block_rank(), ranks = (int)cluster.num_blocks();
+  const int rank = L::kSplit ? (int)cluster.block_rank() : 0;
+  const int ranks = L::kSplit ? (int)cluster.num_blocks() : 1;
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
-  // items of this cluster: first, first + step, ... (one only where K is split)
+  // output tiles of this cluster: first, first + step, ... (one only where K is split);
+  // neighbours share their weights
   const int first = (int)blockIdx.x / ranks, step = (int)gridDim.x / ranks;
   const int my_items = first < p.items ? (p.items - 1 - first) / step + 1 : 0;
+  auto token0 = [&](int it) { return (first + it * step) % p.mtiles * L::kTokens; };
+  auto out0 = [&](int it) { return (first + it * step) / p.mtiles * L::kOut; };
   const int kb0 = (int)((int64_t)p.kblocks * rank / ranks);
   const int nk = (int)((int64_t)p.kblocks * (rank + 1) / ranks) - kb0;
   const int total = my_items * nk;  // K blocks streamed through the ring
@@ -144,165 +222,214 @@ fp8b_gemm_kernel(const __grid_constant__ CUtensorMap tmap_w, const __grid_consta
   int issued = 0;  // stages filled (TMA producer)
 
   if (warp < 4) {
-  // TN = 256: the epilogue's two warpgroups take registers that the first has no
-  // use for (128 x 88 + 256 x 208 = 384 x 168, what the block was launched with).
-  if constexpr (L::kEpiWarps == 8) asm volatile("setmaxnreg.dec.sync.aligned.u32 88;");
-  if (warp == 0) {
-    // ---------------------------------------------------------- TMA producer
-    if (lane == 0) {
-      int g = 0;
+    // N = 256: the epilogue's two warpgroups take registers that the first has no
+    // use for (128 x 56 + 256 x 224 = 384 x 168, what the block was launched with).
+    if constexpr (L::kEpiWarps == 8) asm volatile("setmaxnreg.dec.sync.aligned.u32 56;");
+    if (warp == 0) {
+      // -------------------------------------------------------- TMA producer
+      if (lane == 0) {
+        int g = 0;
+        bool ok = true;
+        for (int it = 0; it < my_items && ok; ++it) {
+          const int a0 = FEW ? out0(it) : token0(it), b0 = FEW ? token0(it) : out0(it);
+          for (int kb = 0; kb < nk; ++kb, ++g) {
+            const int s = g % kStages, r = g / kStages;
+            if (r > 0 && !mbar_wait(empty(s), (r - 1) & 1, abort, p.dev_status)) {
+              ok = false;
+              break;
+            }
+            issued = g + 1;
+            if (nvfp4::kWithhold && blockIdx.x == 0 && g == 0) continue;  // test build: never issued
+            const uint32_t dst = ring + (uint32_t)(s * L::kStageBytes);
+            mbar_arrive_expect_tx(full(s), L::kStageBytes);
+            tma_load_2d(dst, &tmap_a, (kb0 + kb) * kK, a0, full(s));
+            tma_load_2d(dst + L::kABytes, &tmap_b, (kb0 + kb) * kK, b0, full(s));
+          }
+        }
+      }
+    } else if (warp == 1) {
+      // ---------------------------------------------------------- MMA issuer
+      if (lane == 0) {
+        for (int g = 0; g < total; ++g) {
+          const int s = g % kStages, b = g % kBufs;
+          if (g >= kBufs && !mbar_wait(tmem_empty(b), (g / kBufs - 1) & 1, abort, p.dev_status)) break;
+          if (!mbar_wait(full(s), (g / kStages) & 1, abort, p.dev_status)) break;
+          tc_fence_after();
+          const uint32_t src = ring + (uint32_t)(s * L::kStageBytes);
+          const uint64_t ad = smem_desc(src), bd = smem_desc(src + L::kABytes);
+          const uint32_t d = tmem + (uint32_t)(b * N);
+#pragma unroll
+          for (int kk = 0; kk < kK / 32; ++kk)
+            mma_f8(d, ad + 2 * kk, bd + 2 * kk, kIdesc, kk > 0 ? 1u : 0u);
+          mma_commit(empty(s));
+          mma_commit(tmem_full(b));
+        }
+      }
+    } else if (FEW && warp == 2) {
+      // -------------------------------------------------------------- scales
+      constexpr int kPer = N >= 32 ? N / 32 : 1;
+      float sa[kScalePrefetch][kPer], sw[kScalePrefetch];
+      int lit = 0, lkb = 0, left = 0;  // load cursor, tokens of its tile
+      const float *pa = nullptr, *pw = nullptr;
+      auto load = [&](int i) {
+        if (lkb == 0) {
+          const int m0 = token0(lit);
+          left = (int)(p.m - m0 < N ? p.m - m0 : N) - lane;
+          pa = p.sa + kb0 * p.lds + m0 + lane;
+          pw = p.sw + (int64_t)(out0(lit) / kK) * p.kblocks + kb0;
+        }
+        sw[i] = __ldg(pw);
+#pragma unroll
+        for (int j = 0; j < kPer; ++j) sa[i][j] = 32 * j < left ? __ldg(pa + 32 * j) : 0.0f;
+        pa += p.lds;
+        ++pw;
+        if (++lkb == nk) {
+          lkb = 0;
+          ++lit;
+        }
+      };
+#pragma unroll
+      for (int i = 0; i < kScalePrefetch; ++i)
+        if (i < total) load(i);
       bool ok = true;
-      for (int it = 0; it < my_items && ok; ++it) {
-        const int item = first + it * step;
-        const int m0 = item % p.mtiles * TN, n0 = item / p.mtiles * kRows;
-        for (int kb = 0; kb < nk; ++kb, ++g) {
-          const int s = g % kStages, r = g / kStages;
-          if (r > 0 && !mbar_wait(empty(s), (r - 1) & 1, abort, p.dev_status)) {
-            ok = false;
-            break;
-          }
-          issued = g + 1;
-          if (nvfp4::kWithhold && blockIdx.x == 0 && g == 0) continue;  // test build: never issued
-          const uint32_t dst = ring + (uint32_t)(s * L::kStageBytes);
-          mbar_arrive_expect_tx(full(s), L::kStageBytes);
-          tma_load_2d(dst, &tmap_w, (kb0 + kb) * kK, n0, full(s));
-          tma_load_2d(dst + kWBytes, &tmap_a, (kb0 + kb) * kK, m0, full(s));
-        }
-      }
-    }
-  } else if (warp == 1) {
-    // ------------------------------------------------------------ MMA issuer
-    if (lane == 0) {
-      for (int g = 0; g < total; ++g) {
-        const int s = g % kStages, b = g % kBufs;
-        if (g >= kBufs && !mbar_wait(tmem_empty(b), (g / kBufs - 1) & 1, abort, p.dev_status)) break;
-        if (!mbar_wait(full(s), (g / kStages) & 1, abort, p.dev_status)) break;
-        tc_fence_after();
-        const uint32_t src = ring + (uint32_t)(s * L::kStageBytes);
-        const uint64_t wd = smem_desc(src), ad = smem_desc(src + kWBytes);
-        const uint32_t d = tmem + (uint32_t)(b * TN);
+      for (int g0 = 0; g0 < total && ok; g0 += kScalePrefetch) {
 #pragma unroll
-        for (int kk = 0; kk < kK / 32; ++kk)
-          mma_f8(d, wd + 2 * kk, ad + 2 * kk, kIdesc, kk > 0 ? 1u : 0u);
-        mma_commit(empty(s));
-        mma_commit(tmem_full(b));
-      }
-    }
-  } else if (warp == 2) {
-    // ---------------------------------------------------------------- scales
-    constexpr int kPer = TN >= 32 ? TN / 32 : 1;
-    float sa[kScalePrefetch][kPer], sw[kScalePrefetch];
-    int lit = 0, lkb = 0;  // load cursor
-    auto load = [&](int i) {
-      const int item = first + lit * step;
-      const int64_t m0 = (int64_t)(item % p.mtiles) * TN;
-      const int64_t kb = kb0 + lkb;
-      sw[i] = __ldg(p.sw + (int64_t)(item / p.mtiles) * p.kblocks + kb);
+        for (int i = 0; i < kScalePrefetch; ++i) {
+          const int g = g0 + i;
+          if (g < total && ok) {
+            const int b = g % kBufs;
+            float v[kPer];
 #pragma unroll
-      for (int j = 0; j < kPer; ++j) {
-        const int64_t t = m0 + 32 * j + lane;
-        sa[i][j] = t < p.m ? __ldg(p.sa + kb * p.lds + t) : 0.0f;
-      }
-      if (++lkb == nk) {
-        lkb = 0;
-        ++lit;
-      }
-    };
+            for (int j = 0; j < kPer; ++j) v[j] = sa[i][j] * sw[i];
+            if (g + kScalePrefetch < total) load(i);
+            ok = g < kBufs || mbar_wait(tmem_empty(b), (g / kBufs - 1) & 1, abort, p.dev_status);
+            if (ok) {
 #pragma unroll
-    for (int i = 0; i < kScalePrefetch; ++i)
-      if (i < total) load(i);
-    bool ok = true;
-    for (int g0 = 0; g0 < total && ok; g0 += kScalePrefetch) {
-#pragma unroll
-      for (int i = 0; i < kScalePrefetch; ++i) {
-        const int g = g0 + i;
-        if (g < total && ok) {
-          const int b = g % kBufs;
-          float v[kPer];
-#pragma unroll
-          for (int j = 0; j < kPer; ++j) v[j] = sa[i][j] * sw[i];
-          if (g + kScalePrefetch < total) load(i);
-          ok = g < kBufs || mbar_wait(tmem_empty(b), (g / kBufs - 1) & 1, abort, p.dev_status);
-          if (ok) {
-#pragma unroll
-            for (int j = 0; j < kPer; ++j)
-              if (TN >= 32 || lane < TN) scale_buf[b * TN + 32 * j + lane] = v[j];
-            __syncwarp();
-            if (lane == 0) mbar_arrive(scale_full(b));
+              for (int j = 0; j < kPer; ++j)
+                if (N >= 32 || lane < N) scale_buf[b * N + 32 * j + lane] = v[j];
+              __syncwarp();
+              if (lane == 0) mbar_arrive(scale_full(b));
+            }
           }
         }
       }
     }
-  }
   } else {
-    if constexpr (L::kEpiWarps == 8) asm volatile("setmaxnreg.inc.sync.aligned.u32 208;");
     // -------------------------------------------------------------- epilogue
-    constexpr int kChunk = L::kCols < 32 || L::kCols > 64 ? 16 : 32;
-    constexpr int kChunks = L::kCols / kChunk;
-    const int q = warp & 3, c0 = (warp - 4) / 4 * L::kCols;
+    if constexpr (L::kEpiWarps == 8) asm volatile("setmaxnreg.inc.sync.aligned.u32 224;");
+    constexpr int kChunk = kCols < 32 || kCols > 64 ? 16 : 32;
+    constexpr int kChunks = kCols / kChunk;
+    constexpr int kUnroll = FEW ? 1 : kScalePrefetch;
+    const int q = warp & 3, c0 = (warp - 4) / 4 * kCols;
     const uint32_t tq = tmem + ((uint32_t)(32 * q) << 16) + (uint32_t)c0;
     int g = 0;
     bool ok = true;
+    // MANY: the thread's token scale and its weight block's of the next K blocks
+    float sa[kScalePrefetch], sw[kScalePrefetch];
+    int lit = 0, lkb = 0;  // load cursor, with its pointers (advanced, not recomputed:
+    const float *pa = nullptr, *pw = nullptr;  // a tile's take two divisions)
+    auto set_tile = [&]() {
+      const int64_t t = (int64_t)token0(lit) + 32 * q + lane;
+      const int wb = (out0(lit) + c0) / kK;
+      pa = p.sa + kb0 * p.lds + (t < p.m ? t : 0);  // (past m and n: values that nothing stores)
+      pw = p.sw + (int64_t)(wb < p.wblocks ? wb : 0) * p.kblocks + kb0;
+    };
+    auto load = [&](int i) {
+      if (lkb < nk) {
+        sa[i] = __ldg(pa);
+        sw[i] = __ldg(pw);
+        pa += p.lds;
+        ++pw;
+      }
+      if (++lkb >= nk && lkb % kUnroll == 0) {  // a tile's first block is always in slot 0
+        lkb = 0;
+        if (++lit < my_items)
+          set_tile();
+        else
+          lkb = nk;  // the last tile: nothing more is loaded
+      }
+    };
+    if constexpr (!FEW) {
+      if (my_items > 0)
+        set_tile();
+      else
+        lkb = nk;
+#pragma unroll
+      for (int i = 0; i < kScalePrefetch; ++i) {
+        sa[i] = sw[i] = 0.0f;
+        load(i);
+      }
+    }
     for (int it = 0; it < my_items && ok; ++it) {
-      uint64_t acc[L::kCols / 2];  // FP32 pairs of neighbouring tokens
+      uint64_t acc[kCols / 2];  // FP32 pairs of neighbouring columns
 #pragma unroll
-      for (int i = 0; i < L::kCols / 2; ++i) acc[i] = 0ull;
+      for (int i = 0; i < kCols / 2; ++i) acc[i] = 0ull;
+      // unrolled by the prefetch depth: a scale's register is named by its K block, so
+      // that nothing waits for a load before its K block comes
 #pragma unroll 1
-      for (int kb = 0; kb < nk; ++kb, ++g) {
-        const int b = g % kBufs;
-        const uint32_t parity = (g / kBufs) & 1;
-        ok = mbar_wait(tmem_full(b), parity, abort, p.dev_status) &&
-             mbar_wait(scale_full(b), parity, abort, p.dev_status);
-        if (!__all_sync(0xFFFFFFFFu, ok)) {
-          ok = false;
-          break;
-        }
-        tc_fence_after();
-        const ulonglong2* sc = reinterpret_cast<const ulonglong2*>(scale_buf + b * TN + c0);
-        uint32_t v[2][kChunk];
-        tmem_issue(tq + (uint32_t)(b * TN), v[0]);
+      for (int kb = 0; kb < nk && ok; kb += kUnroll) {
 #pragma unroll
-        for (int ch = 0; ch < kChunks; ++ch) {
-          tmem_wait(v[ch & 1]);
-          if (ch + 1 < kChunks) {
-            tmem_issue(tq + (uint32_t)(b * TN + (ch + 1) * kChunk), v[(ch + 1) & 1]);
+        for (int u = 0; u < kUnroll; ++u) {
+          uint64_t s1 = 0ull;
+          if constexpr (!FEW) {
+            const float s = sa[u] * sw[u];
+            s1 = pack2(__float_as_uint(s), __float_as_uint(s));
+            load(u);
           }
+          if (kb + u < nk && ok) {
+            const int b = g % kBufs;
+            const uint32_t parity = (g / kBufs) & 1;
+            ++g;
+            ok = mbar_wait(tmem_full(b), parity, abort, p.dev_status) &&
+                 (!FEW || mbar_wait(scale_full(b), parity, abort, p.dev_status));
+            ok = __all_sync(0xFFFFFFFFu, ok);
+            if (ok) {
+              tc_fence_after();
+              const ulonglong2* sc = reinterpret_cast<const ulonglong2*>(scale_buf + b * N);
+              uint32_t v[2][kChunk];
+              tmem_issue(tq + (uint32_t)(b * N), v[0]);
 #pragma unroll
-          for (int i = 0; i < kChunk / 4; ++i) {
-            const ulonglong2 s2 = sc[ch * (kChunk / 4) + i];
-            const uint32_t* d = &v[ch & 1][4 * i];
-            uint64_t* a = &acc[ch * (kChunk / 2) + 2 * i];
-            fma_f32x2(a[0], pack2(d[0], d[1]), s2.x);
-            fma_f32x2(a[1], pack2(d[2], d[3]), s2.y);
+              for (int ch = 0; ch < kChunks; ++ch) {
+                tmem_wait(v[ch & 1]);
+                if (ch + 1 < kChunks) {
+                  tmem_issue(tq + (uint32_t)(b * N + (ch + 1) * kChunk), v[(ch + 1) & 1]);
+                } else if constexpr (!FEW) {  // all of D_b is in registers
+                  tc_fence_before();
+                  __syncwarp();
+                  if (lane == 0) mbar_arrive(tmem_empty(b));
+                }
+#pragma unroll
+                for (int i = 0; i < kChunk / 4; ++i) {
+                  ulonglong2 s2 = make_ulonglong2(s1, s1);
+                  if constexpr (FEW) s2 = sc[ch * (kChunk / 4) + i];
+                  const uint32_t* d = &v[ch & 1][4 * i];
+                  uint64_t* a = &acc[ch * (kChunk / 2) + 2 * i];
+                  fma_f32x2(a[0], pack2(d[0], d[1]), s2.x);
+                  fma_f32x2(a[1], pack2(d[2], d[3]), s2.y);
+                }
+              }
+              if constexpr (FEW) {  // its scales have been read too
+                tc_fence_before();
+                __syncwarp();
+                if (lane == 0) mbar_arrive(tmem_empty(b));
+              }
+            }
           }
         }
-        tc_fence_before();
-        __syncwarp();
-        if (lane == 0) mbar_arrive(tmem_empty(b));
       }
       if (!ok) break;
-      // lane = weight row: a warp's store covers 32 neighbouring outputs of a token
-      const int item = first + it * step;
       if (L::kSplit && ranks > 1) {
-        // the ring's memory: every load and MMA has left it (all D_b were waited for)
-        float* part = reinterpret_cast<float*>(smem) + c0 * kRows + 32 * q + lane;
+        // the ring's memory: every load and MMA has left it (all D_b were waited for);
+        // [column][MMA row], so that neighbouring lanes write neighbouring words
+        float* part = reinterpret_cast<float*>(smem) + c0 * kM + 32 * q + lane;
 #pragma unroll
-        for (int i = 0; i < L::kCols / 2; ++i)
-          unpack2(acc[i], part[2 * i * kRows], part[(2 * i + 1) * kRows]);
+        for (int i = 0; i < kCols / 2; ++i) unpack2(acc[i], part[2 * i * kM], part[(2 * i + 1) * kM]);
+      } else if constexpr (FEW) {
+        const int64_t t0 = token0(it), nn = (int64_t)out0(it) + 32 * q + lane;
+        const int left = nn < p.n ? (int)(p.m - t0 < N ? p.m - t0 : N) : 0;
+        store_tokens<kCols>(acc, reinterpret_cast<Out*>(p.c) + t0 * p.ldc + nn, p.ldc, left);
       } else {
-        const int64_t t0 = (int64_t)(item % p.mtiles) * TN + c0;
-        const int64_t nn = (int64_t)(item / p.mtiles) * kRows + 32 * q + lane;
-        const int left = nn < p.n ? (int)(p.m - t0 < L::kCols ? p.m - t0 : L::kCols) : 0;
-        Out* dst = reinterpret_cast<Out*>(p.c) + t0 * p.ldc + nn;
-#pragma unroll
-        for (int i = 0; i < L::kCols / 2; ++i) {
-          float x0, x1;
-          unpack2(acc[i], x0, x1);
-          if (2 * i < left) *dst = cast<Out>(x0);
-          dst = next_token(dst, p.ldc);
-          if (2 * i + 1 < left) *dst = cast<Out>(x1);
-          dst = next_token(dst, p.ldc);
-        }
+        store_row<kCols, Out>(acc, p, (int64_t)token0(it) + 32 * q, (int64_t)out0(it) + c0, lane);
       }
     }
   }
@@ -326,36 +453,50 @@ fp8b_gemm_kernel(const __grid_constant__ CUtensorMap tmap_w, const __grid_consta
                  : "memory");
   }
   if (L::kSplit && ranks > 1) {
-    // partial tiles [token][weight row]: each CTA adds and stores every ranks-th token
+    // each CTA adds and stores a share of the partial tiles: FEW every ranks-th token,
+    // 32 outputs of it a warp; MANY every ranks-th group of tokens likewise
     cluster.sync();
-    float* partial = reinterpret_cast<float*>(smem);
-    const int64_t m0 = (int64_t)(first % p.mtiles) * TN;
-    const int64_t n0 = (int64_t)(first / p.mtiles) * kRows;
-    for (int i = threadIdx.x; i < TN / ranks * kRows; i += L::kThreads) {
-      const int c = i / kRows * ranks + rank, row = i % kRows;
-      if (m0 + c < p.m && n0 + row < p.n) {
+    const float* partial = reinterpret_cast<const float*>(smem);
+    const int64_t m0 = token0(0), n0 = out0(0);
+    for (int i = rank * L::kThreads + threadIdx.x; i < N * kM; i += ranks * L::kThreads) {
+      // FEW: neighbouring threads take neighbouring MMA rows, which are outputs.  MANY:
+      // the columns are the outputs; eight tokens x four columns a warp share the words
+      // of a column and the bytes of a row between them.
+      int row, col;
+      if constexpr (FEW) {
+        row = i % kM;
+        col = i / kM;
+      } else {
+        const int t = i / 32, l = i % 32;
+        row = t % (kM / 8) * 8 + l % 8;
+        col = t / (kM / 8) * 4 + l / 8;
+      }
+      const int64_t token = m0 + (FEW ? col : row), out = n0 + (FEW ? row : col);
+      if (token < p.m && out < p.n) {
         float x = 0.0f;
-        for (int o = 0; o < ranks; ++o) x += cluster.map_shared_rank(partial, o)[c * kRows + row];
-        reinterpret_cast<Out*>(p.c)[(m0 + c) * p.ldc + n0 + row] = cast<Out>(x);
+        for (int o = 0; o < ranks; ++o)
+          x += *cluster.map_shared_rank(const_cast<float*>(partial) + col * kM + row, o);
+        reinterpret_cast<Out*>(p.c)[token * p.ldc + out] = cast<Out>(x);
       }
     }
     cluster.sync();  // no CTA leaves while another reads its partial tile
   }
 }
 
-template <int TN>
-int launch(const CUtensorMap& tw, const CUtensorMap& ta, Params p, int split, bool f32,
+template <bool FEW, int N>
+int launch(const CUtensorMap& ta, const CUtensorMap& tb, const Params& p, int split, bool f32,
            cudaStream_t stream) {
-  const void* kern = f32 ? (const void*)fp8b_gemm_kernel<TN, float>
-                         : (const void*)fp8b_gemm_kernel<TN, __nv_bfloat16>;
-  if (nvfp4::occupancy(kern, Tile<TN>::kThreads, Tile<TN>::kSmemBytes) < 1) return NVFP4_ERR_CUDA;
+  using L = Tile<FEW, N>;
+  const void* kern = f32 ? (const void*)fp8b_gemm_kernel<FEW, N, float>
+                         : (const void*)fp8b_gemm_kernel<FEW, N, __nv_bfloat16>;
+  if (nvfp4::occupancy(kern, L::kThreads, L::kSmemBytes) < 1) return NVFP4_ERR_CUDA;
   const int sms = nvfp4::sm_count();
   const int64_t grid = split > 1 ? (int64_t)p.items * split : (p.items < sms ? p.items : sms);
   if (grid > 0x7FFFFFFF) return NVFP4_ERR_SHAPE;
   cudaLaunchConfig_t cfg = {};
   cfg.gridDim = dim3((unsigned)grid);
-  cfg.blockDim = dim3(Tile<TN>::kThreads);
-  cfg.dynamicSmemBytes = Tile<TN>::kSmemBytes;
+  cfg.blockDim = dim3(L::kThreads);
+  cfg.dynamicSmemBytes = L::kSmemBytes;
   cfg.stream = stream;
   cudaLaunchAttribute attr[1];
   attr[0].id = cudaLaunchAttributeClusterDimension;
@@ -363,9 +504,18 @@ int launch(const CUtensorMap& tw, const CUtensorMap& ta, Params p, int split, bo
   attr[0].val.clusterDim.y = 1;
   attr[0].val.clusterDim.z = 1;
   cfg.attrs = attr;
-  cfg.numAttrs = 1;
-  void* args[] = {const_cast<CUtensorMap*>(&tw), const_cast<CUtensorMap*>(&ta), &p};
+  cfg.numAttrs = split > 1 ? 1 : 0;
+  void* args[] = {const_cast<CUtensorMap*>(&ta), const_cast<CUtensorMap*>(&tb), const_cast<Params*>(&p)};
   return cudaLaunchKernelExC(&cfg, kern, args) == cudaSuccess ? NVFP4_OK : NVFP4_ERR_CUDA;
+}
+
+bool encode(CUtensorMap* map, const uint8_t* codes, int64_t rows, int64_t k, int64_t ld, int box_rows) {
+  const cuuint64_t dims[2] = {(cuuint64_t)k, (cuuint64_t)rows};
+  const cuuint64_t strides[1] = {(cuuint64_t)ld};
+  const cuuint32_t box[2] = {kK, (cuuint32_t)box_rows};
+  const cuuint32_t estr[2] = {1, 1};
+  return nvfp4::encode_tiled(map, CU_TENSOR_MAP_DATA_TYPE_UINT8, 2, const_cast<uint8_t*>(codes), dims, strides,
+                             box, estr, CU_TENSOR_MAP_SWIZZLE_128B);
 }
 
 }  // namespace
@@ -373,33 +523,20 @@ int launch(const CUtensorMap& tw, const CUtensorMap& ta, Params p, int split, bo
 int launch_fp8b_gemm(const fp8b_act* a, const fp8b_weight* w, void* c, int c_dtype, int64_t ldc,
                      int32_t* dev_status, cudaStream_t stream) {
   const int64_t m = a->m, n = w->n, k = w->k;
-  const int64_t ntiles = nvfp4::cdiv(n, kRows), kblocks = nvfp4::cdiv(k, kK);
-  // Token tile: the smallest that holds all tokens, 256 beyond that.
-  const int tn = m <= 16 ? 16 : m <= 32 ? 32 : m <= 64 ? 64 : m <= 128 ? 128 : 256;
-  const int64_t mtiles = nvfp4::cdiv(m, tn), items = ntiles * mtiles;
-  if (items > 0x7FFFFFFF) return NVFP4_ERR_SHAPE;
+  const int64_t kblocks = nvfp4::cdiv(k, kK);
+  const int sms = nvfp4::sm_count();
+  // FEW with the smallest tile that holds all tokens; MANY beyond 64.
+  const bool few = m <= 64;
+  const int tile = m <= 16 ? 16 : m <= 32 ? 32 : m <= 64 ? 64 : 256;
+  const int64_t mtiles = nvfp4::cdiv(m, few ? tile : kM), ntiles = nvfp4::cdiv(n, few ? kM : tile);
+  const int64_t items = mtiles * ntiles;
+  if (items > 0x7FFFFFFF - 1024) return NVFP4_ERR_SHAPE;
   // K is split while that still finds idle SMs and leaves four blocks to each CTA.
   int split = 1;
-  while (tn <= 64 && split < 8 && items * split * 2 <= nvfp4::sm_count() && kblocks / (split * 2) >= 4)
-    split *= 2;
+  while (tile <= 128 && split < 8 && items * split * 2 <= sms && kblocks / (split * 2) >= 4) split *= 2;
   CUtensorMap tw, ta;
-  const cuuint32_t estr[2] = {1, 1};
-  {
-    const cuuint64_t dims[2] = {(cuuint64_t)k, (cuuint64_t)n};
-    const cuuint64_t strides[1] = {(cuuint64_t)k};
-    const cuuint32_t box[2] = {kK, kRows};
-    if (!nvfp4::encode_tiled(&tw, CU_TENSOR_MAP_DATA_TYPE_UINT8, 2, const_cast<uint8_t*>(w->codes), dims,
-                             strides, box, estr, CU_TENSOR_MAP_SWIZZLE_128B))
-      return NVFP4_ERR_CUDA;
-  }
-  {
-    const cuuint64_t dims[2] = {(cuuint64_t)k, (cuuint64_t)m};
-    const cuuint64_t strides[1] = {(cuuint64_t)a->ld};
-    const cuuint32_t box[2] = {kK, (cuuint32_t)tn};
-    if (!nvfp4::encode_tiled(&ta, CU_TENSOR_MAP_DATA_TYPE_UINT8, 2, a->codes, dims, strides, box, estr,
-                             CU_TENSOR_MAP_SWIZZLE_128B))
-      return NVFP4_ERR_CUDA;
-  }
+  if (!encode(&tw, w->codes, n, k, k, few ? kM : tile) || !encode(&ta, a->codes, m, k, a->ld, few ? tile : kM))
+    return NVFP4_ERR_CUDA;
   Params p;
   p.sa = a->scales;
   p.lds = a->ld_scales;
@@ -409,15 +546,17 @@ int launch_fp8b_gemm(const fp8b_act* a, const fp8b_weight* w, void* c, int c_dty
   p.m = m;
   p.n = n;
   p.kblocks = (int)kblocks;
+  p.wblocks = (int)nvfp4::cdiv(n, kK);
   p.mtiles = (int)mtiles;
   p.items = (int)items;
-  p.dev_status = dev_status;
   const bool f32 = c_dtype == NVFP4_DTYPE_F32;
-  switch (tn) {
-    case 16: return launch<16>(tw, ta, p, split, f32, stream);
-    case 32: return launch<32>(tw, ta, p, split, f32, stream);
-    case 64: return launch<64>(tw, ta, p, split, f32, stream);
-    case 128: return launch<128>(tw, ta, p, split, f32, stream);
-    default: return launch<256>(tw, ta, p, split, f32, stream);
+  p.vector_store = nvfp4::aligned16(c) && ldc % (f32 ? 4 : 8) == 0;
+  p.dev_status = dev_status;
+  switch (tile) {
+    case 16: return launch<true, 16>(tw, ta, p, split, f32, stream);
+    case 32: return launch<true, 32>(tw, ta, p, split, f32, stream);
+    case 64: return launch<true, 64>(tw, ta, p, split, f32, stream);
+    case 128: return launch<false, 128>(ta, tw, p, split, f32, stream);
+    default: return launch<false, 256>(ta, tw, p, split, f32, stream);
   }
 }

@@ -98,34 +98,6 @@ __device__ __forceinline__ void mma_f16kind(uint32_t tmem_d, uint64_t adesc, uin
       "l"(adesc), "l"(bdesc), "r"(idesc), "r"(accumulate)
       : "memory");
 }
-// Transpose of 16-byte pieces within each group of G lanes (G = 4 or 8): on
-// entry lane gG + a holds pieces b = 0..G-1 (8 consecutive BF16 each) of its
-// own row a; on exit lane gG + b holds piece b of rows a = 0..G-1 in slot a.
-// Rounds m = 1, 2 (, 4) swap, between lanes l and l ^ m, the pieces whose
-// (lane ^ slot) bit m is set.
-template <int G>
-__device__ __forceinline__ void transpose_pieces(uint4 (&P)[G], int lane) {
-#pragma unroll
-  for (int m = 1; m < G; m <<= 1) {
-    const bool hi = (lane & m) != 0;
-#pragma unroll
-    for (int s0 = 0; s0 < G; ++s0) {
-      if (s0 & m) continue;
-      const int s1 = s0 | m;
-      const uint4 snd = hi ? P[s0] : P[s1];
-      uint4 rcv;
-      rcv.x = __shfl_xor_sync(0xFFFFFFFFu, snd.x, m);
-      rcv.y = __shfl_xor_sync(0xFFFFFFFFu, snd.y, m);
-      rcv.z = __shfl_xor_sync(0xFFFFFFFFu, snd.z, m);
-      rcv.w = __shfl_xor_sync(0xFFFFFFFFu, snd.w, m);
-      if (hi)
-        P[s0] = rcv;
-      else
-        P[s1] = rcv;
-    }
-  }
-}
-
 __device__ __forceinline__ uint4 ld_nc_u4(const void* p) {
   uint4 v;
   asm volatile("ld.global.nc.L1::no_allocate.v4.u32 {%0,%1,%2,%3}, [%4];"
