@@ -16,8 +16,8 @@
 //            128 codes each (128-byte swizzle; past n, m and k read as 0);
 //   warp 1   allocates TMEM; one thread issues the MMAs, committing each stage to
 //            its "empty" barrier and each D_b to its "full" barrier;
-//   warp 2   FEW: forms the N products sa sw of each K block in shared memory, loads
-//            four K blocks ahead in registers;
+//   warp 2   forms the products sa sw of each K block in shared memory, loads four K
+//            blocks ahead in registers;
 //   warps 4..  epilogue, a TMEM lane per thread and up to 128 columns.
 // Few output tiles: a cluster of S CTAs splits K, each CTA leaves its partial tile in
 // shared memory and adds and stores a share of it over the S partials in rank order
@@ -50,7 +50,8 @@ struct Tile {
   static constexpr int kBufs = N >= 256 ? 2 : N >= 64 ? 4 : 8;  // TMEM ring
   static constexpr int kTmemCols = N * kBufs;
   static constexpr bool kSplit = N <= 128;  // K may be split over a cluster
-  static constexpr int kScaleBytes = FEW ? kBufs * N * 4 : 0;
+  static constexpr int kWBlocks = FEW || N < 128 ? 1 : N / 128;  // weight blocks of an output tile
+  static constexpr int kScales = kTokens * kWBlocks, kScaleBytes = kBufs * kScales * 4;
   static constexpr int kBars = 2 * kStages + 3 * kBufs + 1;
   static constexpr size_t kSmemBytes =
       1024 + (size_t)kStages * kStageBytes + kScaleBytes + 8 * kBars + 16;
@@ -223,8 +224,8 @@ fp8b_gemm_kernel(const __grid_constant__ CUtensorMap tmap_a, const __grid_consta
 
   if (warp < 4) {
     // N = 256: the epilogue's two warpgroups take registers that the first has no
-    // use for (128 x 56 + 256 x 224 = 384 x 168, what the block was launched with).
-    if constexpr (L::kEpiWarps == 8) asm volatile("setmaxnreg.dec.sync.aligned.u32 56;");
+    // use for (128 x 88 + 256 x 208 = 384 x 168, what the block was launched with).
+    if constexpr (L::kEpiWarps == 8) asm volatile("setmaxnreg.dec.sync.aligned.u32 88;");
     if (warp == 0) {
       // -------------------------------------------------------- TMA producer
       if (lane == 0) {
@@ -249,40 +250,52 @@ fp8b_gemm_kernel(const __grid_constant__ CUtensorMap tmap_a, const __grid_consta
       }
     } else if (warp == 1) {
       // ---------------------------------------------------------- MMA issuer
-      if (lane == 0) {
-        for (int g = 0; g < total; ++g) {
-          const int s = g % kStages, b = g % kBufs;
-          if (g >= kBufs && !mbar_wait(tmem_empty(b), (g / kBufs - 1) & 1, abort, p.dev_status)) break;
-          if (!mbar_wait(full(s), (g / kStages) & 1, abort, p.dev_status)) break;
+      // The warp stays together and one elected lane issues: descriptors and addresses
+      // are then uniform values (a lone thread's instructions cost 600 cycles a K block).
+      bool ok = true;
+      for (int g = 0; g < total && ok; ++g) {
+        const int s = g % kStages, b = g % kBufs;
+        ok = g < kBufs ? mbar_wait(full(s), (g / kStages) & 1, abort, p.dev_status)
+                       : mbar_wait_both(tmem_empty(b), (g / kBufs - 1) & 1, full(s), (g / kStages) & 1, abort,
+                                        p.dev_status);
+        ok = __all_sync(0xFFFFFFFFu, ok);
+        if (ok) {
           tc_fence_after();
           const uint32_t src = ring + (uint32_t)(s * L::kStageBytes);
           const uint64_t ad = smem_desc(src), bd = smem_desc(src + L::kABytes);
           const uint32_t d = tmem + (uint32_t)(b * N);
+          if (elect_one()) {
 #pragma unroll
-          for (int kk = 0; kk < kK / 32; ++kk)
-            mma_f8(d, ad + 2 * kk, bd + 2 * kk, kIdesc, kk > 0 ? 1u : 0u);
-          mma_commit(empty(s));
-          mma_commit(tmem_full(b));
+            for (int kk = 0; kk < kK / 32; ++kk)
+              mma_f8(d, ad + 2 * kk, bd + 2 * kk, kIdesc, kk > 0 ? 1u : 0u);
+            mma_commit(empty(s));
+            mma_commit(tmem_full(b));
+          }
+          __syncwarp();
         }
       }
-    } else if (FEW && warp == 2) {
+    } else if (warp == 2) {
       // -------------------------------------------------------------- scales
-      constexpr int kPer = N >= 32 ? N / 32 : 1;
-      float sa[kScalePrefetch][kPer], sw[kScalePrefetch];
-      int lit = 0, lkb = 0, left = 0;  // load cursor, tokens of its tile
-      const float *pa = nullptr, *pw = nullptr;
+      // the products sa sw of each K block: FEW of N tokens and one weight block, MANY of
+      // 128 tokens and N / 128 weight blocks
+      constexpr int kTok = L::kTokens >= 32 ? L::kTokens / 32 : 1, kW = L::kWBlocks;
+      float sa[kScalePrefetch][kTok], sw[kScalePrefetch][kW];
+      int lit = 0, lkb = 0, left = 0;  // load cursor, tokens of its tile from this lane on
+      const float *pa = nullptr, *pw[kW];
       auto load = [&](int i) {
         if (lkb == 0) {
-          const int m0 = token0(lit);
-          left = (int)(p.m - m0 < N ? p.m - m0 : N) - lane;
+          const int m0 = token0(lit), wb = out0(lit) / kK;
+          left = (int)(p.m - m0 < L::kTokens ? p.m - m0 : L::kTokens) - lane;
           pa = p.sa + kb0 * p.lds + m0 + lane;
-          pw = p.sw + (int64_t)(out0(lit) / kK) * p.kblocks + kb0;
-        }
-        sw[i] = __ldg(pw);
 #pragma unroll
-        for (int j = 0; j < kPer; ++j) sa[i][j] = 32 * j < left ? __ldg(pa + 32 * j) : 0.0f;
+          for (int j = 0; j < kW; ++j)  // (past n: values that nothing stores)
+            pw[j] = p.sw + (int64_t)(wb + j < p.wblocks ? wb + j : wb) * p.kblocks + kb0;
+        }
+#pragma unroll
+        for (int j = 0; j < kW; ++j) sw[i][j] = __ldg(pw[j]++);
+#pragma unroll
+        for (int j = 0; j < kTok; ++j) sa[i][j] = 32 * j < left ? __ldg(pa + 32 * j) : 0.0f;
         pa += p.lds;
-        ++pw;
         if (++lkb == nk) {
           lkb = 0;
           ++lit;
@@ -298,15 +311,21 @@ fp8b_gemm_kernel(const __grid_constant__ CUtensorMap tmap_a, const __grid_consta
           const int g = g0 + i;
           if (g < total && ok) {
             const int b = g % kBufs;
-            float v[kPer];
+            float v[kW][kTok];
 #pragma unroll
-            for (int j = 0; j < kPer; ++j) v[j] = sa[i][j] * sw[i];
+            for (int w = 0; w < kW; ++w)
+#pragma unroll
+              for (int j = 0; j < kTok; ++j) v[w][j] = sa[i][j] * sw[i][w];
             if (g + kScalePrefetch < total) load(i);
             ok = g < kBufs || mbar_wait(tmem_empty(b), (g / kBufs - 1) & 1, abort, p.dev_status);
+            ok = __all_sync(0xFFFFFFFFu, ok);
             if (ok) {
 #pragma unroll
-              for (int j = 0; j < kPer; ++j)
-                if (N >= 32 || lane < N) scale_buf[b * N + 32 * j + lane] = v[j];
+              for (int w = 0; w < kW; ++w)
+#pragma unroll
+                for (int j = 0; j < kTok; ++j)
+                  if (L::kTokens >= 32 || lane < L::kTokens)
+                    scale_buf[b * L::kScales + w * L::kTokens + 32 * j + lane] = v[w][j];
               __syncwarp();
               if (lane == 0) mbar_arrive(scale_full(b));
             }
@@ -316,104 +335,50 @@ fp8b_gemm_kernel(const __grid_constant__ CUtensorMap tmap_a, const __grid_consta
     }
   } else {
     // -------------------------------------------------------------- epilogue
-    if constexpr (L::kEpiWarps == 8) asm volatile("setmaxnreg.inc.sync.aligned.u32 224;");
+    if constexpr (L::kEpiWarps == 8) asm volatile("setmaxnreg.inc.sync.aligned.u32 208;");
     constexpr int kChunk = kCols < 32 || kCols > 64 ? 16 : 32;
     constexpr int kChunks = kCols / kChunk;
-    constexpr int kUnroll = FEW ? 1 : kScalePrefetch;
     const int q = warp & 3, c0 = (warp - 4) / 4 * kCols;
     const uint32_t tq = tmem + ((uint32_t)(32 * q) << 16) + (uint32_t)c0;
     int g = 0;
     bool ok = true;
-    // MANY: the thread's token scale and its weight block's of the next K blocks
-    float sa[kScalePrefetch], sw[kScalePrefetch];
-    int lit = 0, lkb = 0;  // load cursor, with its pointers (advanced, not recomputed:
-    const float *pa = nullptr, *pw = nullptr;  // a tile's take two divisions)
-    auto set_tile = [&]() {
-      const int64_t t = (int64_t)token0(lit) + 32 * q + lane;
-      const int wb = (out0(lit) + c0) / kK;
-      pa = p.sa + kb0 * p.lds + (t < p.m ? t : 0);  // (past m and n: values that nothing stores)
-      pw = p.sw + (int64_t)(wb < p.wblocks ? wb : 0) * p.kblocks + kb0;
-    };
-    auto load = [&](int i) {
-      if (lkb < nk) {
-        sa[i] = __ldg(pa);
-        sw[i] = __ldg(pw);
-        pa += p.lds;
-        ++pw;
-      }
-      if (++lkb >= nk && lkb % kUnroll == 0) {  // a tile's first block is always in slot 0
-        lkb = 0;
-        if (++lit < my_items)
-          set_tile();
-        else
-          lkb = nk;  // the last tile: nothing more is loaded
-      }
-    };
-    if constexpr (!FEW) {
-      if (my_items > 0)
-        set_tile();
-      else
-        lkb = nk;
-#pragma unroll
-      for (int i = 0; i < kScalePrefetch; ++i) {
-        sa[i] = sw[i] = 0.0f;
-        load(i);
-      }
-    }
     for (int it = 0; it < my_items && ok; ++it) {
       uint64_t acc[kCols / 2];  // FP32 pairs of neighbouring columns
 #pragma unroll
       for (int i = 0; i < kCols / 2; ++i) acc[i] = 0ull;
-      // unrolled by the prefetch depth: a scale's register is named by its K block, so
-      // that nothing waits for a load before its K block comes
 #pragma unroll 1
-      for (int kb = 0; kb < nk && ok; kb += kUnroll) {
+      for (int kb = 0; kb < nk; ++kb, ++g) {
+        const int b = g % kBufs;
+        const uint32_t parity = (g / kBufs) & 1;
+        ok = mbar_wait_both(tmem_full(b), parity, scale_full(b), parity, abort, p.dev_status);
+        ok = __all_sync(0xFFFFFFFFu, ok);
+        if (!ok) break;
+        tc_fence_after();
+        const float* scales = scale_buf + b * L::kScales;
+        const float s = FEW ? 0.0f : scales[c0 / kK * kM + 32 * q + lane];
+        const uint64_t s1 = pack2(__float_as_uint(s), __float_as_uint(s));
+        uint32_t v[kChunk];
 #pragma unroll
-        for (int u = 0; u < kUnroll; ++u) {
-          uint64_t s1 = 0ull;
-          if constexpr (!FEW) {
-            const float s = sa[u] * sw[u];
-            s1 = pack2(__float_as_uint(s), __float_as_uint(s));
-            load(u);
+        for (int ch = 0; ch < kChunks; ++ch) {
+          tmem_issue(tq + (uint32_t)(b * N + ch * kChunk), v);
+          ulonglong2 s2[kChunk / 4];
+#pragma unroll
+          for (int i = 0; i < kChunk / 4; ++i) {
+            s2[i] = make_ulonglong2(s1, s1);
+            if constexpr (FEW) s2[i] = reinterpret_cast<const ulonglong2*>(scales)[ch * (kChunk / 4) + i];
           }
-          if (kb + u < nk && ok) {
-            const int b = g % kBufs;
-            const uint32_t parity = (g / kBufs) & 1;
-            ++g;
-            ok = mbar_wait(tmem_full(b), parity, abort, p.dev_status) &&
-                 (!FEW || mbar_wait(scale_full(b), parity, abort, p.dev_status));
-            ok = __all_sync(0xFFFFFFFFu, ok);
-            if (ok) {
-              tc_fence_after();
-              const ulonglong2* sc = reinterpret_cast<const ulonglong2*>(scale_buf + b * N);
-              uint32_t v[2][kChunk];
-              tmem_issue(tq + (uint32_t)(b * N), v[0]);
+          tmem_wait(v);
+          if (ch + 1 == kChunks) {  // D_b and its scales are in registers
+            tc_fence_before();
+            __syncwarp();
+            if (lane == 0) mbar_arrive(tmem_empty(b));
+          }
 #pragma unroll
-              for (int ch = 0; ch < kChunks; ++ch) {
-                tmem_wait(v[ch & 1]);
-                if (ch + 1 < kChunks) {
-                  tmem_issue(tq + (uint32_t)(b * N + (ch + 1) * kChunk), v[(ch + 1) & 1]);
-                } else if constexpr (!FEW) {  // all of D_b is in registers
-                  tc_fence_before();
-                  __syncwarp();
-                  if (lane == 0) mbar_arrive(tmem_empty(b));
-                }
-#pragma unroll
-                for (int i = 0; i < kChunk / 4; ++i) {
-                  ulonglong2 s2 = make_ulonglong2(s1, s1);
-                  if constexpr (FEW) s2 = sc[ch * (kChunk / 4) + i];
-                  const uint32_t* d = &v[ch & 1][4 * i];
-                  uint64_t* a = &acc[ch * (kChunk / 2) + 2 * i];
-                  fma_f32x2(a[0], pack2(d[0], d[1]), s2.x);
-                  fma_f32x2(a[1], pack2(d[2], d[3]), s2.y);
-                }
-              }
-              if constexpr (FEW) {  // its scales have been read too
-                tc_fence_before();
-                __syncwarp();
-                if (lane == 0) mbar_arrive(tmem_empty(b));
-              }
-            }
+          for (int i = 0; i < kChunk / 4; ++i) {
+            const uint32_t* d = &v[4 * i];
+            uint64_t* a = &acc[ch * (kChunk / 2) + 2 * i];
+            fma_f32x2(a[0], pack2(d[0], d[1]), s2[i].x);
+            fma_f32x2(a[1], pack2(d[2], d[3]), s2[i].y);
           }
         }
       }
@@ -441,9 +406,11 @@ fp8b_gemm_kernel(const __grid_constant__ CUtensorMap tmap_a, const __grid_consta
     if (warp == 0 && lane == 0)
       for (int g = issued > kStages ? issued - kStages : 0; g < issued; ++g)
         mbar_drain(full(g % kStages), (uint32_t)(g / kStages) & 1u, p.dev_status);
-    if (warp == 1 && lane == 0) {
-      mma_commit(drain_bar);
-      mbar_drain(drain_bar, 0u, p.dev_status);
+    if (warp == 1) {  // (by the lane that issued them: elect picks the same one)
+      if (elect_one()) {
+        mma_commit(drain_bar);
+        mbar_drain(drain_bar, 0u, p.dev_status);
+      }
     }
   }
   if (warp == 1) {

@@ -64,6 +64,22 @@ __device__ __forceinline__ bool mbar_wait(uint32_t bar, uint32_t parity, volatil
     }
   }
 }
+// The same for two barriers, tested together: the common case, both complete, takes
+// one round trip instead of two.
+__device__ __forceinline__ bool mbar_wait_both(uint32_t bar0, uint32_t parity0, uint32_t bar1,
+                                               uint32_t parity1, volatile uint32_t* abort,
+                                               int32_t* dev_status) {
+  const bool r0 = mbar_try_wait(bar0, parity0), r1 = mbar_try_wait(bar1, parity1);
+  return (r0 || mbar_wait(bar0, parity0, abort, dev_status)) &&
+         (r1 || mbar_wait(bar1, parity1, abort, dev_status));
+}
+// One lane of a converged warp; the compiler then knows that what it executes is uniform.
+__device__ __forceinline__ bool elect_one() {
+  uint32_t p;
+  asm volatile(
+      "{\n .reg .pred p;\n elect.sync _|p, 0xFFFFFFFF;\n selp.u32 %0, 1, 0, p;\n}" : "=r"(p));
+  return p != 0;
+}
 // Bounded by time only: after an abort, lets work already in flight land.
 __device__ __forceinline__ bool mbar_drain(uint32_t bar, uint32_t parity, int32_t* dev_status) {
   const unsigned long long t0 = globaltimer();
