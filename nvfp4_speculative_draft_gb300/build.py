@@ -4,12 +4,15 @@ Each ``csrc/*.cu`` is compiled in parallel with
 ``nvcc -gencode arch=compute_103a,code=sm_103a -O3 -lineinfo`` and linked into
 ``_build/libnvfp4draft.so`` (CUDA runtime linked statically, so the library
 is self-contained; it shares the process's primary CUDA context).
+``csrc/binding.cpp``, the native argument marshalling of the verify step's
+calls, is compiled beside them with g++ against PyTorch's headers.
 """
 import concurrent.futures as cf
 import glob
 import os
 import subprocess
 import sys
+import sysconfig
 
 PKG = os.path.dirname(os.path.abspath(__file__))
 ROOT = os.path.dirname(PKG)
@@ -44,13 +47,45 @@ def _stale(srcs, target):
     return any(os.path.getmtime(d) > t for d in deps)
 
 
+def binding_path():
+    """The binding's file: one per PyTorch and Python version, whose headers it is built with."""
+    import torch
+    tag = f"torch{torch.__version__}_py{sys.version_info[0]}{sys.version_info[1]}".replace("+", "_")
+    return os.path.join(OUT, f"_binding_{tag}.so")
+
+
+def build_binding(force=False):
+    import torch
+    src, target = os.path.join(CSRC, "binding.cpp"), binding_path()
+    os.makedirs(OUT, exist_ok=True)
+    if not force and not _stale([src], target):
+        return target
+    home = os.path.dirname(torch.__file__)
+    cuda = os.path.dirname(os.path.dirname(_nvcc())) or "/usr/local/cuda"
+    tmp = target + f".tmp{os.getpid()}"
+    cmd = ["g++", "-O2", "-std=c++17", "-fPIC", "-shared", "-I", INCLUDE,
+           "-I", os.path.join(home, "include"),
+           "-I", os.path.join(home, "include", "torch", "csrc", "api", "include"),
+           "-I", sysconfig.get_paths()["include"], "-I", os.path.join(cuda, "include"),
+           f"-D_GLIBCXX_USE_CXX11_ABI={int(torch._C._GLIBCXX_USE_CXX11_ABI)}", src, "-o", tmp,
+           "-L", os.path.join(home, "lib"), "-ltorch_python", "-ltorch_cpu", "-ltorch", "-lc10",
+           "-lc10_cuda"]
+    r = subprocess.run(cmd, capture_output=True, text=True)
+    if r.returncode != 0:
+        raise RuntimeError(f"g++ failed on {src}:\n{r.stdout}\n{r.stderr}")
+    os.replace(tmp, target)
+    return target
+
+
 def build(force=False, verbose=False, extra=(), debug=False, withhold=False):
     if not debug and not withhold:
-        # the library and its timeout-test variant, side by side
-        with cf.ThreadPoolExecutor(2) as ex:
+        # the library, its timeout-test variant and the binding, side by side
+        with cf.ThreadPoolExecutor(3) as ex:
             fw = ex.submit(build, force, verbose, extra, False, True)
+            fb = ex.submit(build_binding, force)
             lib = _build_one(force, verbose, extra, False, False)
             fw.result()
+            fb.result()
         return lib
     return _build_one(force, verbose, extra, debug, withhold)
 

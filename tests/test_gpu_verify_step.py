@@ -530,3 +530,57 @@ def test_on_another_stream(dev):
     tokens, accepted = m.spec_verify(want[3], drafted, u, r, num_draft=num, stream=s)
     s.synchronize()
     assert torch.equal(logits, want[2]) and torch.equal(tokens, want[4]) and torch.equal(accepted, want[5])
+
+
+def test_refusals_leave_outputs_alone(dev):
+    """Tensors of the wrong shape, type, stride or device are refused before anything is launched."""
+    m = nd()
+    bf, i32 = torch.bfloat16, torch.int32
+    x = torch.ones((4, 256), dtype=bf, device=dev)
+    g = torch.ones(256, dtype=bf, device=dev)
+    bad_norm = [dict(x=x.float()), dict(x=x.t()), dict(x=x[0]), dict(gamma=g[:128]), dict(gamma=g.float()), dict(gamma=torch.ones(512, dtype=bf, device=dev)[::2]),
+                dict(residual=x[:3]), dict(residual=x.cpu()), dict(residual=x, residual_out=x[:, :128]), dict(dev_status=torch.zeros(1, device=dev)),
+                dict(gamma=torch.ones(256, dtype=bf))]
+    for kw in bad_norm:
+        args = dict(x=x, gamma=g)
+        args.update(kw)
+        with pytest.raises(ValueError):
+            m.fp8b_rmsnorm(args.pop("x"), args.pop("gamma"), 1e-6, **args)
+    acts, _ = m.fp8b_rmsnorm(x, g)
+    w = m.fp8b_quantize(torch.ones((64, 256), dtype=bf, device=dev))
+    out = torch.full((4, 64), 7.0, device=dev)
+    for a in (m.Fp8BlockActs(acts.codes, acts.scales, 3, 256), m.Fp8BlockActs(acts.codes, acts.scales[:1], 4, 256),
+              m.Fp8BlockActs(acts.codes[:, :128], acts.scales[:1], 4, 128), m.Fp8BlockActs(acts.codes.float(), acts.scales, 4, 256),
+              m.Fp8BlockActs(acts.codes.cpu(), acts.scales.cpu(), 4, 256)):
+        with pytest.raises(ValueError):
+            m.fp8b_gemm(a, w, out=out)
+    for bad in (m.Fp8BlockWeight(w.codes, w.scales[:, :1], 64, 256), m.Fp8BlockWeight(w.codes.t(), w.scales, 256, 64),
+                m.Fp8BlockWeight(w.codes, w.scales.double(), 64, 256)):
+        with pytest.raises(ValueError):
+            m.fp8b_gemm(acts, bad, out=out)
+    for o in (out[:3], out.half(), torch.full((4, 128), 7.0, device=dev)[:, ::2]):
+        with pytest.raises(ValueError):
+            m.fp8b_gemm(acts, w, out=o)
+    with pytest.raises(ValueError):
+        m.fp8b_gemm(acts, w, out_dtype=torch.float16)
+    with pytest.raises(m.Nvfp4Error):  # k not a multiple of 16: the library's own check
+        m.fp8b_quantize(torch.ones((4, 24), dtype=bf, device=dev))
+    with pytest.raises(m.Nvfp4Error):
+        m.fp8b_rmsnorm(torch.ones((0, 256), dtype=bf, device=dev), g)
+    assert (out == 7).all()
+    t = torch.full((2, 3, 10), 0.1, device=dev)
+    q = t[:, :2].contiguous()
+    tok, u, r = torch.zeros((2, 2), dtype=i32, device=dev), torch.zeros((2, 2), device=dev), torch.zeros(2, device=dev)
+    res = torch.full((2, 3), 9, dtype=i32, device=dev)
+    good = dict(target=t, tok=tok, u=u, r=r, draft_probs=q, out_tokens=res)
+    bad = [dict(target=t.double()), dict(target=t.transpose(1, 2)), dict(target=t[0]), dict(tok=tok.long()), dict(tok=tok[:, :1]), dict(u=u[:1]),
+           dict(r=r[:1]), dict(r=r.double()), dict(draft_probs=q.bfloat16()), dict(draft_probs=q[:, :1]), dict(draft_probs=torch.zeros((2, 2, 11), device=dev)),
+           dict(num_draft=torch.zeros(3, dtype=i32, device=dev)), dict(out_tokens=res[:, :2]), dict(out_accepted=torch.zeros(1, dtype=i32, device=dev)),
+           dict(tok=tok.cpu())]
+    for kw in bad:
+        a = dict(good)
+        a.update(kw)
+        with pytest.raises(ValueError):
+            m.spec_verify(a.pop("target"), a.pop("tok"), a.pop("u"), a.pop("r"), **a)
+    torch.cuda.synchronize()
+    assert (res == 9).all()

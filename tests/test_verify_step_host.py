@@ -101,7 +101,7 @@ def bf16(*shape):
     return torch.zeros(shape, dtype=torch.bfloat16)
 
 
-def test_binding_refuses_host_tensors():
+def test_binding_refuses_host_tensors(L):
     w = nd.Fp8BlockWeight(torch.zeros((8, 64), dtype=torch.uint8), torch.zeros((1, 1)), 8, 64)
     a = nd.Fp8BlockActs(torch.zeros((2, 64), dtype=torch.uint8), torch.zeros((1, 2)), 2, 64)
     f = torch.zeros((1, 2, 8))
@@ -112,29 +112,25 @@ def test_binding_refuses_host_tensors():
             call()
 
 
-def test_row_strides():
-    cpu = torch.device("cpu")
-
-    def rows(t):
-        return nd._is_rows(t, torch.float32, cpu, t.shape)
-
-    assert rows(torch.zeros(4, 8)) and rows(torch.zeros(4, 16)[:, :8]) and rows(torch.zeros(1, 8)) and rows(torch.zeros(0, 8))
-    assert not rows(torch.zeros(8, 4).t()) and not rows(torch.zeros(16).as_strided((4, 8), (2, 1)))
-    assert not nd._is_rows(torch.zeros(4, 8), torch.float32, cpu, (4, 7)) and not nd._is_rows(None, torch.float32, cpu, (4, 8))
-    assert not nd._is_rows(torch.zeros(4, 8), torch.bfloat16, cpu, (4, 8))
-    assert nd._ld(torch.zeros(4, 16)[:, :8]) == 16 and nd._ld(torch.zeros(1, 5)) == 16
+def test_binding_refuses_other_objects(L):
+    a = nd.Fp8BlockActs(torch.zeros((2, 64), dtype=torch.uint8), torch.zeros((1, 2)), 2, 64)
+    for call in (lambda: nd.fp8b_quantize(None), lambda: nd.fp8b_rmsnorm("x", None), lambda: nd.fp8b_rmsnorm([1.0], None),
+                 lambda: nd.spec_verify(3, None, None, None)):
+        with pytest.raises(ValueError, match="CUDA"):
+            call()
+    with pytest.raises(AttributeError):
+        nd.fp8b_gemm(torch.zeros(2, 64), a)
 
 
-def test_packed_structs_have_the_layout_of_the_c_ones():
-    import struct
-    for fmt, s in ((nd._PACK_EXEC, nd._Exec), (nd._PACK_NORM, nd._NormInput), (nd._PACK_ACTS, nd._Fp8BlockActs),
-                   (nd._PACK_WEIGHT, nd._Fp8BlockWeight), (nd._PACK_VERIFY, nd._VerifyInput)):
-        fields = s._fields_
-        values = [0.5 if t is ctypes.c_float else i + 1 for i, (_, t) in enumerate(fields)]
-        raw = fmt(*values)
-        assert len(raw) == ctypes.sizeof(s)
-        got = s.from_buffer_copy(raw)
-        assert [getattr(got, n) for n, _ in fields] == values
+def test_binding_needs_the_library_first():
+    """The native module refuses calls before bind(), and bad arguments of bind()."""
+    native = nd._load_binding()
+    with pytest.raises(TypeError):
+        native.bind(1, 2)
+    with pytest.raises((TypeError, ValueError)):
+        native.bind(0, 0, 0, 0, nd.Nvfp4Error)
+    with pytest.raises(TypeError):
+        native.quantize(None)
 
 
 # ---------------------------------------- the plain implementations themselves
