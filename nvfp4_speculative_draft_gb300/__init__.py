@@ -632,7 +632,7 @@ def _raw(stream):
 @dataclass
 class Fp8BlockWeight:
     """Device tensors of one block-scaled FP8 (E4M3) weight."""
-    codes: torch.Tensor   # uint8 [n, k]
+    codes: torch.Tensor   # float8_e4m3fn [n, k] (or the same bytes as uint8)
     scales: torch.Tensor  # float32 [ceil(n/128), ceil(k/128)]
     n: int
     k: int
@@ -642,7 +642,7 @@ class Fp8BlockWeight:
 class Fp8BlockActs:
     """Device tensors of block-scaled FP8 (E4M3) activations.  The scales are
     stored by column block, so that a tile's tokens lie side by side."""
-    codes: torch.Tensor   # uint8 [m, k], rows may be padded
+    codes: torch.Tensor   # float8_e4m3fn [m, k] (or uint8), rows may be padded
     scales: torch.Tensor  # float32 [ceil(k/128), m], rows may be padded
     m: int
     k: int

@@ -61,7 +61,7 @@ const char* dtype_text(at::ScalarType t) {
     case at::kBFloat16: return "torch.bfloat16";
     case at::kFloat: return "torch.float32";
     case at::kInt: return "torch.int32";
-    case at::kByte: return "torch.uint8";
+    case at::kFloat8_e4m3fn: return "torch.float8_e4m3fn (or torch.uint8)";
     default: return "another type";
   }
 }
@@ -101,6 +101,13 @@ constexpr const char* kRowsText = " with unit column stride and rows that do not
 const Tensor& need_rows(PyObject* o, const char* name, at::ScalarType type, at::Device dev, at::IntArrayRef shape) {
   const Tensor* t = tensor_of(o);
   if (!is(t, type, dev, shape) || !rows_ok(*t)) refuse(name, t, type, shape, kRowsText);
+  return *t;
+}
+// E4M3 codes: torch's own type, or the same bytes as uint8
+const Tensor& need_codes(PyObject* o, const char* name, at::Device dev, at::IntArrayRef shape) {
+  const Tensor* t = tensor_of(o);
+  if (!(is(t, at::kFloat8_e4m3fn, dev, shape) || is(t, at::kByte, dev, shape)) || !rows_ok(*t))
+    refuse(name, t, at::kFloat8_e4m3fn, shape, kRowsText);
   return *t;
 }
 const Tensor& need_vector(PyObject* o, const char* name, at::ScalarType type, at::Device dev, int64_t n) {
@@ -190,9 +197,9 @@ struct Acts {
   explicit Acts(PyObject* o) : codes(o, s_codes), scales(o, s_scales), dev(device_of(codes.o, "acts.codes")) {
     a.m = integer(o, s_m);
     a.k = integer(o, s_k);
-    const Tensor& c = need_rows(codes.o, "acts.codes", at::kByte, dev, {a.m, a.k});
+    const Tensor& c = need_codes(codes.o, "acts.codes", dev, {a.m, a.k});
     const Tensor& s = need_rows(scales.o, "acts.scales", at::kFloat, dev, {blocks(a.k), a.m});
-    a.codes = c.data_ptr<uint8_t>();
+    a.codes = static_cast<uint8_t*>(c.data_ptr());
     a.ld = ld(c);
     a.scales = s.data_ptr<float>();
     a.ld_scales = s.size(0) > 1 ? s.stride(0) : a.m;
@@ -209,15 +216,15 @@ PyObject* quantize(PyObject*, PyObject* const* a, Py_ssize_t nargs) {
   const int64_t n = w.size(0), k = w.size(1);
   Tensor codes, scales;
   if (a[1] != Py_None) {
-    codes = need_rows(a[1], "out.codes", at::kByte, dev, {n, k});
+    codes = need_codes(a[1], "out.codes", dev, {n, k});
     scales = need_rows(a[2], "out.scales", at::kFloat, dev, {blocks(n), blocks(k)});
     if (!codes.is_contiguous() || !scales.is_contiguous()) throw Refusal("out must be contiguous");
   } else {
-    codes = make({n, k}, at::kByte, dev);
+    codes = make({n, k}, at::kFloat8_e4m3fn, dev);
     scales = make({blocks(n), blocks(k)}, at::kFloat, dev);
   }
   Call call(dev, a[3], a[4]);
-  const int rc = lib.quantize(w.data_ptr(), n, k, ld(w), codes.data_ptr<uint8_t>(), scales.data_ptr<float>(), &call.ex);
+  const int rc = lib.quantize(w.data_ptr(), n, k, ld(w), static_cast<uint8_t*>(codes.data_ptr()), scales.data_ptr<float>(), &call.ex);
   if (rc != NVFP4_OK) return fail("fp8b_quantize", rc);
   return Py_BuildValue("(NN)", wrap(codes), wrap(scales));
   CALL_END
@@ -259,9 +266,9 @@ PyObject* rmsnorm(PyObject*, PyObject* const* a, Py_ssize_t nargs) {
       throw Refusal("out must be activations of the shape and device of x");
     out = given.a;
   } else {
-    codes = make({m, k}, at::kByte, dev);
+    codes = make({m, k}, at::kFloat8_e4m3fn, dev);
     scales = make({blocks(k), m}, at::kFloat, dev);
-    out = fp8b_act{codes.data_ptr<uint8_t>(), ld(codes), scales.data_ptr<float>(), m, m, k};
+    out = fp8b_act{static_cast<uint8_t*>(codes.data_ptr()), ld(codes), scales.data_ptr<float>(), m, m, k};
   }
   Call call(dev, a[6], a[7]);
   const int rc = lib.rmsnorm(&in, &out, &call.ex);
@@ -281,11 +288,11 @@ PyObject* gemm(PyObject*, PyObject* const* a, Py_ssize_t nargs) {
   w.n = integer(a[1], s_n);
   w.k = integer(a[1], s_k);
   const at::Device dev = device_of(wc.o, "weight.codes");
-  const Tensor& codes = need_rows(wc.o, "weight.codes", at::kByte, dev, {w.n, w.k});
+  const Tensor& codes = need_codes(wc.o, "weight.codes", dev, {w.n, w.k});
   const Tensor& scales = need_rows(ws.o, "weight.scales", at::kFloat, dev, {blocks(w.n), blocks(w.k)});
   if (!codes.is_contiguous() || !scales.is_contiguous())
     throw Refusal("weight.codes and weight.scales must be contiguous");
-  w.codes = codes.data_ptr<uint8_t>();
+  w.codes = static_cast<uint8_t*>(codes.data_ptr());
   w.scales = scales.data_ptr<float>();
   if (acts.dev != dev) throw Refusal("acts must be on the weight's device");
   if (acts.a.k != w.k) throw Refusal("acts must have k = " + std::to_string(w.k) + " columns, got " + std::to_string(acts.a.k));

@@ -36,7 +36,7 @@ namespace cg = cooperative_groups;
 
 constexpr int kM = 128;                // MMA rows
 constexpr int kK = 128;                // K block: one swizzled 128-byte row of codes
-constexpr int kRing = 196 * 1024;      // most bytes of the ring of stages
+constexpr int kRing = 196 * 1024;      // bytes of the rings of an SM's CTAs, at most
 constexpr int kScalePrefetch = 4;      // K blocks of scales in flight
 
 template <bool FEW, int N>
@@ -46,19 +46,24 @@ struct Tile {
   static constexpr int kCols = N > 128 ? N / 2 : N;  // columns of one epilogue warp
   static constexpr int kTokens = FEW ? N : kM, kOut = FEW ? kM : N;  // of an output tile
   static constexpr int kABytes = kM * kK, kStageBytes = kABytes + N * kK;
-  static constexpr int kStages = kRing / kStageBytes < 10 ? kRing / kStageBytes : 10;
+  // Two CTAs an SM where registers allow: a K block of few tokens takes less time than
+  // its handovers between producer, MMAs and epilogue, and two such chains overlap.
+  static constexpr int kCtas = N <= 32 ? 2 : 1;
+  static constexpr int kStages = kRing / kCtas / kStageBytes;
   static constexpr int kBufs = N >= 256 ? 2 : N >= 64 ? 4 : 8;  // TMEM ring
   static constexpr int kTmemCols = N * kBufs;
   static constexpr bool kSplit = N <= 128;  // K may be split over a cluster
   static constexpr int kWBlocks = FEW || N < 128 ? 1 : N / 128;  // weight blocks of an output tile
   static constexpr int kScales = kTokens * kWBlocks, kScaleBytes = kBufs * kScales * 4;
   static constexpr int kBars = 2 * kStages + 3 * kBufs + 1;
+  static constexpr int kStoreBytes = FEW ? 0 : kEpiWarps * 2048;
   static constexpr size_t kSmemBytes =
-      1024 + (size_t)kStages * kStageBytes + kScaleBytes + 8 * kBars + 16;
+      1024 + (size_t)kStages * kStageBytes + kScaleBytes + kStoreBytes + 8 * kBars + 16;
   static_assert(kTmemCols >= 32 && kTmemCols <= 512 && (kTmemCols & (kTmemCols - 1)) == 0, "TMEM");
   static_assert(kStageBytes % 1024 == 0, "swizzled tiles start on 1 KB");
   static_assert(!kSplit || kM * N * 4 <= kStages * kStageBytes, "the partial tile reuses the ring");
-  static_assert(kSmemBytes <= 227 * 1024, "shared memory");
+  static_assert(kCtas * (kSmemBytes + 1024) <= 228 * 1024, "shared memory");
+  static_assert(kCtas * kTmemCols <= 512, "TMEM");
 };
 
 struct Params {
@@ -103,22 +108,22 @@ __device__ __forceinline__ void store_tokens(const uint64_t (&acc)[N / 2], Out* 
   }
 }
 
-// MANY: a thread's accumulators are C consecutive outputs of one token.  128 bytes of
-// each row at a time are transposed in 16-byte pieces within groups of eight lanes,
-// so that a store covers four rows x 128 contiguous bytes.
+// MANY: a thread's accumulators are C consecutive outputs of one token (a lane's row).
+// 64 bytes of each row at a time go through 2 KB of the warp's own shared memory, so
+// that a store covers eight rows x 64 contiguous bytes rather than 32 rows x 16.  The
+// 16-byte pieces of row r lie at piece ^ (r / 2 % 4): neither side meets bank conflicts.
 template <int C, typename Out>
 __device__ __forceinline__ void store_row(const uint64_t (&acc)[C / 2], const Params& p, int64_t row0, int64_t n0,
-                                          int lane) {
+                                          int lane, uint4* stage) {
   constexpr int kPiece = 16 / sizeof(Out);  // outputs of a piece
 #pragma unroll
-  for (int g = 0; g < C / (8 * kPiece); ++g) {
-    uint4 P[8];
+  for (int g = 0; g < C / (4 * kPiece); ++g) {
 #pragma unroll
-    for (int i = 0; i < 8; ++i) {
+    for (int i = 0; i < 4; ++i) {
       uint32_t w[4];
 #pragma unroll
       for (int e = 0; e < 4; ++e) {
-        const int at = (g * 8 + i) * kPiece / 2;  // first pair of the piece
+        const int at = (g * 4 + i) * kPiece / 2;  // first pair of the piece
         if constexpr (sizeof(Out) == 4) {
           float x[2];
           unpack2(acc[at + e / 2], x[0], x[1]);
@@ -130,19 +135,21 @@ __device__ __forceinline__ void store_row(const uint64_t (&acc)[C / 2], const Pa
           w[e] = *reinterpret_cast<const uint32_t*>(&b);
         }
       }
-      P[i] = make_uint4(w[0], w[1], w[2], w[3]);
+      stage[lane * 4 + (i ^ (lane / 2 % 4))] = make_uint4(w[0], w[1], w[2], w[3]);
     }
-    transpose_pieces<8>(P, lane);
-    const int64_t col = n0 + (g * 8 + (lane & 7)) * kPiece;
+    __syncwarp();
+    const int64_t col = n0 + (g * 4 + lane % 4) * kPiece;
 #pragma unroll
-    for (int i = 0; i < 8; ++i) {
-      const int64_t row = row0 + (lane & ~7) + i;
+    for (int i = 0; i < 4; ++i) {
+      const int r = 8 * i + lane / 4;
+      const uint4 v = stage[r * 4 + (lane % 4 ^ (r / 2 % 4))];
+      const int64_t row = row0 + r;
       if (row < p.m && col < p.n) {
         Out* dst = reinterpret_cast<Out*>(p.c) + row * p.ldc + col;
         if (p.vector_store && col + kPiece <= p.n) {
-          *reinterpret_cast<uint4*>(dst) = P[i];
+          *reinterpret_cast<uint4*>(dst) = v;
         } else {
-          const uint32_t w[4] = {P[i].x, P[i].y, P[i].z, P[i].w};
+          const uint32_t w[4] = {v.x, v.y, v.z, v.w};
 #pragma unroll
           for (int e = 0; e < kPiece; ++e) {
             if (col + e < p.n) {
@@ -155,11 +162,12 @@ __device__ __forceinline__ void store_row(const uint64_t (&acc)[C / 2], const Pa
         }
       }
     }
+    __syncwarp();
   }
 }
 
 template <bool FEW, int N, typename Out>
-__global__ void __launch_bounds__(Tile<FEW, N>::kThreads, 1)
+__global__ void __launch_bounds__(Tile<FEW, N>::kThreads, Tile<FEW, N>::kCtas)
 fp8b_gemm_kernel(const __grid_constant__ CUtensorMap tmap_a, const __grid_constant__ CUtensorMap tmap_b,
                  const __grid_constant__ Params p) {
   using L = Tile<FEW, N>;
@@ -170,15 +178,16 @@ fp8b_gemm_kernel(const __grid_constant__ CUtensorMap tmap_a, const __grid_consta
   const uint32_t ring = (raw + 1023u) & ~1023u;
   unsigned char* const smem = smem_raw + (ring - raw);
   float* const scale_buf = reinterpret_cast<float*>(smem + kStages * L::kStageBytes);
-  const uint32_t bars = ring + kStages * L::kStageBytes + L::kScaleBytes;
+  uint4* const store_buf = reinterpret_cast<uint4*>(smem + kStages * L::kStageBytes + L::kScaleBytes);
+  constexpr int kBarsAt = kStages * L::kStageBytes + L::kScaleBytes + L::kStoreBytes;
+  const uint32_t bars = ring + kBarsAt;
   auto full = [&](int s) { return bars + 8u * s; };
   auto empty = [&](int s) { return bars + 8u * (kStages + s); };
   auto tmem_full = [&](int b) { return bars + 8u * (2 * kStages + b); };
   auto tmem_empty = [&](int b) { return bars + 8u * (2 * kStages + kBufs + b); };
   auto scale_full = [&](int b) { return bars + 8u * (2 * kStages + 2 * kBufs + b); };
   const uint32_t drain_bar = bars + 8u * (L::kBars - 1);
-  uint32_t* tmem_slot =
-      reinterpret_cast<uint32_t*>(smem + kStages * L::kStageBytes + L::kScaleBytes + 8 * L::kBars);
+  uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(smem + kBarsAt + 8 * L::kBars);
   volatile uint32_t* abort = tmem_slot + 1;
 
   cg::cluster_group cluster = cg::this_cluster();
@@ -394,7 +403,8 @@ fp8b_gemm_kernel(const __grid_constant__ CUtensorMap tmap_a, const __grid_consta
         const int left = nn < p.n ? (int)(p.m - t0 < N ? p.m - t0 : N) : 0;
         store_tokens<kCols>(acc, reinterpret_cast<Out*>(p.c) + t0 * p.ldc + nn, p.ldc, left);
       } else {
-        store_row<kCols, Out>(acc, p, (int64_t)token0(it) + 32 * q, (int64_t)out0(it) + c0, lane);
+        store_row<kCols, Out>(acc, p, (int64_t)token0(it) + 32 * q, (int64_t)out0(it) + c0, lane,
+                              store_buf + (warp - 4) * 128);
       }
     }
   }
@@ -458,7 +468,8 @@ int launch(const CUtensorMap& ta, const CUtensorMap& tb, const Params& p, int sp
                          : (const void*)fp8b_gemm_kernel<FEW, N, __nv_bfloat16>;
   if (nvfp4::occupancy(kern, L::kThreads, L::kSmemBytes) < 1) return NVFP4_ERR_CUDA;
   const int sms = nvfp4::sm_count();
-  const int64_t grid = split > 1 ? (int64_t)p.items * split : (p.items < sms ? p.items : sms);
+  const int64_t slots = (int64_t)sms * L::kCtas;
+  const int64_t grid = split > 1 ? (int64_t)p.items * split : (p.items < slots ? p.items : slots);
   if (grid > 0x7FFFFFFF) return NVFP4_ERR_SHAPE;
   cudaLaunchConfig_t cfg = {};
   cfg.gridDim = dim3((unsigned)grid);
@@ -492,15 +503,26 @@ int launch_fp8b_gemm(const fp8b_act* a, const fp8b_weight* w, void* c, int c_dty
   const int64_t m = a->m, n = w->n, k = w->k;
   const int64_t kblocks = nvfp4::cdiv(k, kK);
   const int sms = nvfp4::sm_count();
-  // FEW with the smallest tile that holds all tokens; MANY beyond 64.
+  // Form and tile: FEW with the smallest that holds all tokens, MANY beyond 64 with the
+  // tile whose whole waves take less time (a K block of 128 columns takes about 650
+  // cycles, of 256 about 750: the handovers weigh on the smaller).
   const bool few = m <= 64;
-  const int tile = m <= 16 ? 16 : m <= 32 ? 32 : m <= 64 ? 64 : 256;
+  int tile = m <= 16 ? 16 : m <= 32 ? 32 : 64;
+  if (!few) {
+    const int64_t mt = nvfp4::cdiv(m, kM);
+    const int64_t w128 = nvfp4::cdiv(mt * nvfp4::cdiv(n, 128), sms), w256 = nvfp4::cdiv(mt * nvfp4::cdiv(n, 256), sms);
+    tile = w128 * 650 <= w256 * 750 ? 128 : 256;
+  }
   const int64_t mtiles = nvfp4::cdiv(m, few ? tile : kM), ntiles = nvfp4::cdiv(n, few ? kM : tile);
   const int64_t items = mtiles * ntiles;
   if (items > 0x7FFFFFFF - 1024) return NVFP4_ERR_SHAPE;
-  // K is split while that still finds idle SMs and leaves four blocks to each CTA.
+  // K is split while that finds idle SMs and leaves eight blocks to each CTA.  Where two
+  // CTAs share an SM, clusters (which stay within a group of SMs) fill about 8/5 of the
+  // SMs' number: 5120 x 10240, one token: 6 parts 12.4 us, 7 parts 17.4, 3 parts 13.0, 1
+  // part 21.9.
+  const int64_t slots = tile <= 32 ? (int64_t)sms * 8 / 5 : sms;
   int split = 1;
-  while (tile <= 128 && split < 8 && items * split * 2 <= sms && kblocks / (split * 2) >= 4) split *= 2;
+  while (tile <= 128 && split < 6 && items * (split + 1) <= slots && kblocks / (split + 1) >= 8) ++split;
   CUtensorMap tw, ta;
   if (!encode(&tw, w->codes, n, k, k, few ? kM : tile) || !encode(&ta, a->codes, m, k, a->ld, few ? tile : kM))
     return NVFP4_ERR_CUDA;

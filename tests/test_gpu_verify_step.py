@@ -39,6 +39,10 @@ def randn(dev, seed, *shape):
     return torch.randn(shape, generator=gen(dev, seed), device=dev)
 
 
+def u8(codes):
+    return codes.view(torch.uint8)
+
+
 # ------------------------------------------------------------------ quantiser
 
 def check_quantize(w, q):
@@ -67,7 +71,8 @@ def test_quantize_special_blocks(dev):
     w[256, 128] = 448.0
     q = nd().fp8b_quantize(w)
     check_quantize(w, q)
-    assert (q.codes[:128, :128] == 0).all() and (q.scales[0, 0] == 0).item()
+    assert q.codes.dtype == torch.float8_e4m3fn
+    assert (u8(q.codes)[:128, :128] == 0).all() and (q.scales[0, 0] == 0).item()
 
 
 def test_quantize_padded_rows_and_guards(dev):
@@ -93,7 +98,7 @@ def test_quantize_reports_nonfinite(dev):
     w[200, 10] = float("nan")
     bad = m.fp8b_quantize(w, dev_status=status)
     assert status.item() == 7
-    assert torch.equal(bad.codes[:128], good.codes[:128]) and torch.equal(bad.codes[128:, 128:], good.codes[128:, 128:])
+    assert torch.equal(u8(bad.codes)[:128], u8(good.codes)[:128]) and torch.equal(u8(bad.codes)[128:, 128:], u8(good.codes)[128:, 128:])
 
 
 # ----------------------------------------------------------------------- norm
@@ -136,8 +141,8 @@ def test_norm_zero_rows_and_eps(dev):
     for eps in (0.0, 1e-6, 1.0):
         acts, _ = nd().fp8b_rmsnorm(x, g, eps)
         check_norm(acts, None, x, None, g, eps)
-        assert (acts.codes[1] == 0).all() and (acts.scales[:, 1] == 0).all()
-        assert (acts.codes[2, 128:] == 0).all() and acts.scales[1, 2].item() == 0
+        assert (u8(acts.codes)[1] == 0).all() and (acts.scales[:, 1] == 0).all()
+        assert (u8(acts.codes)[2, 128:] == 0).all() and acts.scales[1, 2].item() == 0
 
 
 @pytest.mark.parametrize("alias", ["residual", "x"])
@@ -152,7 +157,7 @@ def test_norm_in_place(dev, alias, k):
     target = r2 if alias == "residual" else x2
     got, h2 = m.fp8b_rmsnorm(x2, g, residual=r2, residual_out=target)
     assert h2 is target and torch.equal(target, h)
-    assert torch.equal(got.codes, want.codes) and torch.equal(got.scales, want.scales)
+    assert torch.equal(u8(got.codes), u8(want.codes)) and torch.equal(got.scales, want.scales)
 
 
 def test_norm_strides_and_guards(dev):
@@ -184,7 +189,7 @@ def test_norm_reports_nonfinite(dev):
             acts, _ = m.fp8b_rmsnorm(x, gamma, dev_status=status)
             want, _ = m.fp8b_rmsnorm(good, gamma)
             assert status.item() == (7 if gamma is not None or value != 3e38 else 0)
-            assert torch.equal(acts.codes[[0, 1, 3]], want.codes[[0, 1, 3]])
+            assert torch.equal(u8(acts.codes)[[0, 1, 3]], u8(want.codes)[[0, 1, 3]])
 
 
 # ----------------------------------------------------------------------- gemm
@@ -499,7 +504,7 @@ def test_verify_step_captured_and_replayed(dev):
             again = chain(m, *fresh[0])
     torch.cuda.synchronize()
     for got, want in [(outs[0], eager[0]), (outs[1], eager[1]), (again, eager[0])]:
-        assert torch.equal(got[0].codes, want[0].codes)
+        assert torch.equal(u8(got[0].codes), u8(want[0].codes))
         for i in (1, 2, 4, 5):
             assert torch.equal(got[i], want[i])
 
