@@ -43,6 +43,32 @@ constexpr unsigned long long kWaitLimit = 2000000000ull;
 constexpr bool kWithhold = false;
 #endif
 
+// Loads through the read-only path that stay behind wait_for_previous_kernel(): __ldg
+// promises the compiler that the value never changes, and may be moved before it.
+__device__ __forceinline__ float ld_ro(const float* p) {
+  float v;
+  asm volatile("ld.global.nc.f32 %0, [%1];" : "=f"(v) : "l"(p));
+  return v;
+}
+__device__ __forceinline__ int32_t ld_ro(const int32_t* p) {
+  int32_t v;
+  asm volatile("ld.global.nc.s32 %0, [%1];" : "=r"(v) : "l"(p));
+  return v;
+}
+__device__ __forceinline__ uint32_t ld_ro(const unsigned short* p) {
+  unsigned short v;
+  asm volatile("ld.global.nc.u16 %0, [%1];" : "=h"(v) : "l"(p));
+  return v;
+}
+
+// Programmatic dependent launch, as the verify step's kernels use it: a kernel may start
+// while the one before it on the stream finishes, but touches no global memory before
+// this wait; its own dependents may start once all its CTAs have passed it.
+__device__ __forceinline__ void wait_for_previous_kernel() {
+  asm volatile("griddepcontrol.wait;" ::: "memory");
+  asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
+}
+
 __host__ __device__ __forceinline__ int64_t cdiv(int64_t a, int64_t b) { return (a + b - 1) / b; }
 
 inline bool aligned16(const void* p) { return (reinterpret_cast<uintptr_t>(p) & 15u) == 0; }
@@ -65,6 +91,27 @@ int occupancy(const void* func, int threads, size_t smem);
 bool encode_tiled(CUtensorMap* map, CUtensorMapDataType type, cuuint32_t rank, void* addr,
                   const cuuint64_t* dims, const cuuint64_t* strides, const cuuint32_t* box,
                   const cuuint32_t* elem_strides, CUtensorMapSwizzle swizzle);
+
+// Launch with programmatic stream serialisation (the kernel calls
+// wait_for_previous_kernel), as clusters of `cluster` CTAs along x.
+inline cudaError_t launch_dependent(const void* func, dim3 grid, dim3 block, size_t smem, cudaStream_t stream,
+                                    unsigned cluster, void** args) {
+  cudaLaunchAttribute attr[2];
+  attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+  attr[0].val.programmaticStreamSerializationAllowed = 1;
+  attr[1].id = cudaLaunchAttributeClusterDimension;
+  attr[1].val.clusterDim.x = cluster;
+  attr[1].val.clusterDim.y = 1;
+  attr[1].val.clusterDim.z = 1;
+  cudaLaunchConfig_t cfg = {};
+  cfg.gridDim = grid;
+  cfg.blockDim = block;
+  cfg.dynamicSmemBytes = smem;
+  cfg.stream = stream;
+  cfg.attrs = attr;
+  cfg.numAttrs = cluster > 1 ? 2 : 1;
+  return cudaLaunchKernelExC(&cfg, func, args);
+}
 
 // Host-side argument checks shared by the entry points (status codes of
 // nvfp4draft.h).

@@ -40,6 +40,7 @@ fp8b_quantize_kernel(const uint4* __restrict__ w, int64_t n, int64_t k, int64_t 
   const bool colok = col < k / 8;
   uint4 v[kQVecs];
   uint32_t m2 = 0u;
+  nvfp4::wait_for_previous_kernel();
 #pragma unroll
   for (int i = 0; i < kQVecs; ++i) {
     const int64_t r = row0 + (kQThreads / 16) * i;
@@ -118,6 +119,7 @@ fp8b_rmsnorm_kernel(const __grid_constant__ NormParams p) {
   const int64_t row = (int64_t)blockIdx.x * blockDim.y + threadIdx.y;
   const bool live = row < p.m;
   uint4 h[V];
+  nvfp4::wait_for_previous_kernel();
 #pragma unroll
   for (int i = 0; i < V; ++i) {
     const int c = c0 + i * T;
@@ -206,8 +208,11 @@ int launch_norm(const NormParams& p, int T, cudaStream_t stream) {
   const int rows = T >= 256 ? 1 : 256 / T;  // of a CTA
   const int64_t grid = nvfp4::cdiv(p.m, rows);
   const unsigned cols = p.gamma != nullptr ? 1u : (unsigned)nvfp4::cdiv(p.nvec, V * T);
-  fp8b_rmsnorm_kernel<V, MAXT><<<dim3((unsigned)grid, cols), dim3(T, rows), 0, stream>>>(p);
-  return cudaGetLastError() == cudaSuccess ? NVFP4_OK : NVFP4_ERR_CUDA;
+  void* args[] = {const_cast<NormParams*>(&p)};
+  return nvfp4::launch_dependent((const void*)fp8b_rmsnorm_kernel<V, MAXT>, dim3((unsigned)grid, cols), dim3(T, rows), 0,
+                                 stream, 1, args) == cudaSuccess
+             ? NVFP4_OK
+             : NVFP4_ERR_CUDA;
 }
 
 }  // namespace
@@ -216,10 +221,14 @@ int launch_fp8b_quantize(const void* w, int64_t n, int64_t k, int64_t ld, uint8_
                          float* scales, int32_t* dev_status, cudaStream_t stream) {
   const int64_t kb = nvfp4::cdiv(k, kBlock), blocks = nvfp4::cdiv(n, kBlock) * kb;
   if (blocks > 0x7FFFFFFF) return NVFP4_ERR_SHAPE;
-  fp8b_quantize_kernel<<<(unsigned)blocks, kQThreads, 0, stream>>>(
-      reinterpret_cast<const uint4*>(w), n, k, ld / 8, reinterpret_cast<uint2*>(codes), scales, kb,
-      dev_status);
-  return cudaGetLastError() == cudaSuccess ? NVFP4_OK : NVFP4_ERR_CUDA;
+  const uint4* wv = reinterpret_cast<const uint4*>(w);
+  uint2* cv = reinterpret_cast<uint2*>(codes);
+  int64_t ldv = ld / 8, kbv = kb;
+  void* args[] = {&wv, &n, &k, &ldv, &cv, &scales, &kbv, &dev_status};
+  return nvfp4::launch_dependent((const void*)fp8b_quantize_kernel, dim3((unsigned)blocks), dim3(kQThreads), 0, stream, 1,
+                                 args) == cudaSuccess
+             ? NVFP4_OK
+             : NVFP4_ERR_CUDA;
 }
 
 int launch_fp8b_rmsnorm(const fp8b_norm_input* in, const fp8b_act* out, int32_t* dev_status,

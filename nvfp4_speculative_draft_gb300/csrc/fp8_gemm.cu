@@ -204,6 +204,10 @@ fp8b_gemm_kernel(const __grid_constant__ CUtensorMap tmap_a, const __grid_consta
   const int nk = (int)((int64_t)p.kblocks * (rank + 1) / ranks) - kb0;
   const int total = my_items * nk;  // K blocks streamed through the ring
 
+  if (threadIdx.x == 32) {
+    asm volatile("prefetch.tensormap [%0];" ::"l"(reinterpret_cast<uint64_t>(&tmap_a)) : "memory");
+    asm volatile("prefetch.tensormap [%0];" ::"l"(reinterpret_cast<uint64_t>(&tmap_b)) : "memory");
+  }
   if (threadIdx.x == 0) {
     for (int s = 0; s < kStages; ++s) {
       mbar_init(full(s), 1);
@@ -229,6 +233,7 @@ fp8b_gemm_kernel(const __grid_constant__ CUtensorMap tmap_a, const __grid_consta
   __syncthreads();
   tc_fence_after();
   const uint32_t tmem = *tmem_slot;
+  nvfp4::wait_for_previous_kernel();
   int issued = 0;  // stages filled (TMA producer)
 
   if (warp < 4) {
@@ -301,9 +306,9 @@ fp8b_gemm_kernel(const __grid_constant__ CUtensorMap tmap_a, const __grid_consta
             pw[j] = p.sw + (int64_t)(wb + j < p.wblocks ? wb + j : wb) * p.kblocks + kb0;
         }
 #pragma unroll
-        for (int j = 0; j < kW; ++j) sw[i][j] = __ldg(pw[j]++);
+        for (int j = 0; j < kW; ++j) sw[i][j] = nvfp4::ld_ro(pw[j]++);
 #pragma unroll
-        for (int j = 0; j < kTok; ++j) sa[i][j] = 32 * j < left ? __ldg(pa + 32 * j) : 0.0f;
+        for (int j = 0; j < kTok; ++j) sa[i][j] = 32 * j < left ? nvfp4::ld_ro(pa + 32 * j) : 0.0f;
         pa += p.lds;
         if (++lkb == nk) {
           lkb = 0;
@@ -471,20 +476,11 @@ int launch(const CUtensorMap& ta, const CUtensorMap& tb, const Params& p, int sp
   const int64_t slots = (int64_t)sms * L::kCtas;
   const int64_t grid = split > 1 ? (int64_t)p.items * split : (p.items < slots ? p.items : slots);
   if (grid > 0x7FFFFFFF) return NVFP4_ERR_SHAPE;
-  cudaLaunchConfig_t cfg = {};
-  cfg.gridDim = dim3((unsigned)grid);
-  cfg.blockDim = dim3(L::kThreads);
-  cfg.dynamicSmemBytes = L::kSmemBytes;
-  cfg.stream = stream;
-  cudaLaunchAttribute attr[1];
-  attr[0].id = cudaLaunchAttributeClusterDimension;
-  attr[0].val.clusterDim.x = (unsigned)split;
-  attr[0].val.clusterDim.y = 1;
-  attr[0].val.clusterDim.z = 1;
-  cfg.attrs = attr;
-  cfg.numAttrs = split > 1 ? 1 : 0;
   void* args[] = {const_cast<CUtensorMap*>(&ta), const_cast<CUtensorMap*>(&tb), const_cast<Params*>(&p)};
-  return cudaLaunchKernelExC(&cfg, kern, args) == cudaSuccess ? NVFP4_OK : NVFP4_ERR_CUDA;
+  return nvfp4::launch_dependent(kern, dim3((unsigned)grid), dim3(L::kThreads), L::kSmemBytes, stream,
+                                 (unsigned)split, args) == cudaSuccess
+             ? NVFP4_OK
+             : NVFP4_ERR_CUDA;
 }
 
 bool encode(CUtensorMap* map, const uint8_t* codes, int64_t rows, int64_t k, int64_t ld, int box_rows) {

@@ -54,8 +54,12 @@ struct VerifyParams {
   int g, log_ranks;
 };
 
-__device__ __forceinline__ float load_one(const float* p) { return __ldg(p); }
-__device__ __forceinline__ float load_one(const __nv_bfloat16* p) { return __bfloat162float(*p); }
+using nvfp4::ld_ro;
+
+__device__ __forceinline__ float load_one(const float* p) { return ld_ro(p); }
+__device__ __forceinline__ float load_one(const __nv_bfloat16* p) {
+  return __uint_as_float(ld_ro(reinterpret_cast<const unsigned short*>(p)) << 16);
+}
 
 // Packed binary32 pairs.
 __device__ __forceinline__ uint64_t pair(uint32_t lo, uint32_t hi) {
@@ -100,8 +104,8 @@ struct Vec<float> {
                  : "l"(p));
   }
   __device__ __forceinline__ void load_elements(const float* p) {
-    raw = make_uint4(__float_as_uint(__ldg(p)), __float_as_uint(__ldg(p + 1)),
-                     __float_as_uint(__ldg(p + 2)), __float_as_uint(__ldg(p + 3)));
+    raw = make_uint4(__float_as_uint(ld_ro(p)), __float_as_uint(ld_ro(p + 1)),
+                     __float_as_uint(ld_ro(p + 2)), __float_as_uint(ld_ro(p + 3)));
   }
   __device__ __forceinline__ void get(uint64_t (&f)[2]) const {
     f[0] = pair(raw.x, raw.y);
@@ -121,7 +125,7 @@ struct Vec<__nv_bfloat16> {
     const unsigned short* u = reinterpret_cast<const unsigned short*>(p);
     uint32_t w[4];
 #pragma unroll
-    for (int j = 0; j < 4; ++j) w[j] = (uint32_t)__ldg(u + 2 * j) | (uint32_t)__ldg(u + 2 * j + 1) << 16;
+    for (int j = 0; j < 4; ++j) w[j] = ld_ro(u + 2 * j) | ld_ro(u + 2 * j + 1) << 16;
     raw = make_uint4(w[0], w[1], w[2], w[3]);
   }
   __device__ __forceinline__ void get(uint64_t (&f)[4]) const {
@@ -388,9 +392,10 @@ __global__ void __launch_bounds__(kThreads, 4) spec_verify_kernel(const __grid_c
   const T* target = reinterpret_cast<const T*>(p.target) + seq * p.ld_ts;
   const T* draft = p.draft != nullptr ? reinterpret_cast<const T*>(p.draft) + seq * p.ld_ds : nullptr;
   const int32_t* tokens = p.tokens + seq * p.ld_tok;
+  nvfp4::wait_for_previous_kernel();
   int num = p.g;
   if (p.num_draft != nullptr) {
-    num = __ldg(p.num_draft + seq);
+    num = ld_ro(p.num_draft + seq);
     if (num < 0) return;  // absent: the same in every CTA of the cluster
     if (num > p.g) {
       num = p.g;
@@ -403,8 +408,8 @@ __global__ void __launch_bounds__(kThreads, 4) spec_verify_kernel(const __grid_c
       const int i = i0 + lane;
       bool refuse = false;
       if (i < num) {
-        d = __ldg(tokens + i);
-        const float u = __ldg(p.accept_u + seq * p.ld_u + i);
+        d = ld_ro(tokens + i);
+        const float u = ld_ro(p.accept_u + seq * p.ld_u + i);
         refuse = true;
         if (d >= 0 && d < p.vocab) {
           const float pd = load_one(target + i * p.ld_tp + d);
@@ -459,7 +464,7 @@ __global__ void __launch_bounds__(kThreads, 4) spec_verify_kernel(const __grid_c
     if (lane == 0) warp_part[pass][warp] = sum;
     if (pass == 0 && rank == 0 && warp == 0) {  // the outputs but for the sampled token
       for (int i = lane; i <= p.g; i += 32)
-        if (i != a) p.out[seq * p.ld_out + i] = i < a ? __ldg(tokens + i) : -1;
+        if (i != a) p.out[seq * p.ld_out + i] = i < a ? ld_ro(tokens + i) : -1;
       if (lane == 0) p.accepted[seq] = a;
     }
     if (ranks > 1)
@@ -480,7 +485,7 @@ __global__ void __launch_bounds__(kThreads, 4) spec_verify_kernel(const __grid_c
 #pragma unroll
       for (int i = 0; i < kLaneParts; ++i) mine.add(parts[i]);
       const Sum upto = prefix(mine, lane), all = shuffle(upto, 31).normal();
-      const float u = __ldg(p.sample_u + seq), h = u * all.s;
+      const float u = ld_ro(p.sample_u + seq), h = u * all.s;
       Sum t = Sum{h, fmaf(u, all.s, -h) + u * all.c}.normal();
       if (t.s < 0.0f) t = Sum{0.0f, 0.0f};
       const int who = pick(mine, upto, t);
@@ -593,19 +598,11 @@ int launch_spec_verify(const spec_verify_input* in, int32_t* out_tokens, int64_t
   const int ranks = 1 << log_ranks;
   if (in->batch > 0x7FFFFFFF / ranks) return NVFP4_ERR_SHAPE;
   p.log_ranks = log_ranks;
-  cudaLaunchConfig_t cfg = {};
-  cfg.gridDim = dim3((unsigned)(in->batch * ranks));
-  cfg.blockDim = dim3(kThreads);
-  cfg.stream = stream;
-  cudaLaunchAttribute attr[1];
-  attr[0].id = cudaLaunchAttributeClusterDimension;
-  attr[0].val.clusterDim.x = (unsigned)ranks;
-  attr[0].val.clusterDim.y = 1;
-  attr[0].val.clusterDim.z = 1;
-  cfg.attrs = attr;
-  cfg.numAttrs = ranks > 1 ? 1 : 0;
-  const cudaError_t e = in->dtype == NVFP4_DTYPE_F32
-                            ? cudaLaunchKernelEx(&cfg, spec_verify_kernel<float>, p)
-                            : cudaLaunchKernelEx(&cfg, spec_verify_kernel<__nv_bfloat16>, p);
-  return e == cudaSuccess ? NVFP4_OK : NVFP4_ERR_CUDA;
+  const void* kern = in->dtype == NVFP4_DTYPE_F32 ? (const void*)spec_verify_kernel<float>
+                                                  : (const void*)spec_verify_kernel<__nv_bfloat16>;
+  void* args[] = {&p};
+  return nvfp4::launch_dependent(kern, dim3((unsigned)(in->batch * ranks)), dim3(kThreads), 0, stream,
+                                 (unsigned)ranks, args) == cudaSuccess
+             ? NVFP4_OK
+             : NVFP4_ERR_CUDA;
 }
