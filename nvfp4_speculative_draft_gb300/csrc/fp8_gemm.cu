@@ -14,8 +14,9 @@
 //         accumulators share one token and one weight block, so one scale per K block.
 //   warp 0   TMA producer: per K block 128 rows of one operand and N of the other,
 //            128 codes each (128-byte swizzle; past n, m and k read as 0);
-//   warp 1   allocates TMEM; one thread issues the MMAs, committing each stage to
-//            its "empty" barrier and each D_b to its "full" barrier;
+//   warp 1   allocates TMEM and issues the MMAs, committing each stage to its "empty"
+//            barrier and each D_b to its "full" barrier (N = 64, 128: warps 1 and 3, K
+//            blocks in turn);
 //   warp 2   forms the products sa sw of each K block in shared memory, loads four K
 //            blocks ahead in registers;
 //   warps 4..  epilogue, a TMEM lane per thread and up to 128 columns.
@@ -41,15 +42,19 @@ constexpr int kScalePrefetch = 4;      // K blocks of scales in flight
 
 template <bool FEW, int N>
 struct Tile {
-  static constexpr int kEpiWarps = N > 128 ? 8 : 4;
+  static constexpr int kEpiWarps = N >= 64 ? 8 : 4;
   static constexpr int kThreads = 128 + 32 * kEpiWarps;
-  static constexpr int kCols = N > 128 ? N / 2 : N;  // columns of one epilogue warp
+  static constexpr int kCols = N / (kEpiWarps / 4);  // columns of one epilogue warp
   static constexpr int kTokens = FEW ? N : kM, kOut = FEW ? kM : N;  // of an output tile
   static constexpr int kABytes = kM * kK, kStageBytes = kABytes + N * kK;
   // Two CTAs an SM where registers allow: a K block of few tokens takes less time than
   // its handovers between producer, MMAs and epilogue, and two such chains overlap.
   static constexpr int kCtas = N <= 32 ? 2 : 1;
-  static constexpr int kStages = kRing / kCtas / kStageBytes;
+  // Issuing a K block's MMAs takes a warp about 500 cycles: where that is what a tile
+  // waits for, two warps take K blocks in turn (128 x 5120 x 5120: 17.0 -> 14.6 us; with
+  // two CTAs an SM, 11.5 -> 12.7 for one token, or N = 256, 132 -> 137 for prefill, not).
+  static constexpr int kIssuers = N == 64 || N == 128 ? 2 : 1;
+  static constexpr int kStages = kRing / kCtas / kStageBytes / kIssuers * kIssuers;
   static constexpr int kBufs = N >= 256 ? 2 : N >= 64 ? 4 : 8;  // TMEM ring
   static constexpr int kTmemCols = N * kBufs;
   static constexpr bool kSplit = N <= 128;  // K may be split over a cluster
@@ -61,6 +66,10 @@ struct Tile {
       1024 + (size_t)kStages * kStageBytes + kScaleBytes + kStoreBytes + 8 * kBars + 16;
   static_assert(kTmemCols >= 32 && kTmemCols <= 512 && (kTmemCols & (kTmemCols - 1)) == 0, "TMEM");
   static_assert(kStageBytes % 1024 == 0, "swizzled tiles start on 1 KB");
+  // With rings that are multiples of the issuers a stage and a buffer always serve the same
+  // warp, which so waits for every phase of their barriers.  (A warp that skipped one would
+  // take the parity of the phase before for the one it waits for.)
+  static_assert(kStages % kIssuers == 0 && kBufs % kIssuers == 0, "rings");
   static_assert(!kSplit || kM * N * 4 <= kStages * kStageBytes, "the partial tile reuses the ring");
   static_assert(kCtas * (kSmemBytes + 1024) <= 228 * 1024, "shared memory");
   static_assert(kCtas * kTmemCols <= 512, "TMEM");
@@ -218,7 +227,7 @@ fp8b_gemm_kernel(const __grid_constant__ CUtensorMap tmap_a, const __grid_consta
       mbar_init(tmem_empty(b), L::kEpiWarps);
       mbar_init(scale_full(b), 1);
     }
-    mbar_init(drain_bar, 1);
+    mbar_init(drain_bar, L::kIssuers);
     *abort = 0u;
     asm volatile("fence.mbarrier_init.release.cluster;" ::: "memory");
   }
@@ -239,7 +248,7 @@ fp8b_gemm_kernel(const __grid_constant__ CUtensorMap tmap_a, const __grid_consta
   if (warp < 4) {
     // N = 256: the epilogue's two warpgroups take registers that the first has no
     // use for (128 x 88 + 256 x 208 = 384 x 168, what the block was launched with).
-    if constexpr (L::kEpiWarps == 8) asm volatile("setmaxnreg.dec.sync.aligned.u32 88;");
+    if constexpr (N == 256) asm volatile("setmaxnreg.dec.sync.aligned.u32 88;");
     if (warp == 0) {
       // -------------------------------------------------------- TMA producer
       if (lane == 0) {
@@ -262,12 +271,13 @@ fp8b_gemm_kernel(const __grid_constant__ CUtensorMap tmap_a, const __grid_consta
           }
         }
       }
-    } else if (warp == 1) {
-      // ---------------------------------------------------------- MMA issuer
-      // The warp stays together and one elected lane issues: descriptors and addresses
+    } else if (warp == 1 || (warp == 3 && L::kIssuers == 2)) {
+      // --------------------------------------------------------- MMA issuers
+      // Each warp stays together and one elected lane issues: descriptors and addresses
       // are then uniform values (a lone thread's instructions cost 600 cycles a K block).
+      // Every D_b has a buffer of its own, so issuers need not wait for one another.
       bool ok = true;
-      for (int g = 0; g < total && ok; ++g) {
+      for (int g = warp >> 1; g < total && ok; g += L::kIssuers) {
         const int s = g % kStages, b = g % kBufs;
         ok = g < kBufs ? mbar_wait(full(s), (g / kStages) & 1, abort, p.dev_status)
                        : mbar_wait_both(tmem_empty(b), (g / kBufs - 1) & 1, full(s), (g / kStages) & 1, abort,
@@ -349,7 +359,7 @@ fp8b_gemm_kernel(const __grid_constant__ CUtensorMap tmap_a, const __grid_consta
     }
   } else {
     // -------------------------------------------------------------- epilogue
-    if constexpr (L::kEpiWarps == 8) asm volatile("setmaxnreg.inc.sync.aligned.u32 208;");
+    if constexpr (N == 256) asm volatile("setmaxnreg.inc.sync.aligned.u32 208;");
     constexpr int kChunk = kCols < 32 || kCols > 64 ? 16 : 32;
     constexpr int kChunks = kCols / kChunk;
     const int q = warp & 3, c0 = (warp - 4) / 4 * kCols;
@@ -379,7 +389,7 @@ fp8b_gemm_kernel(const __grid_constant__ CUtensorMap tmap_a, const __grid_consta
 #pragma unroll
           for (int i = 0; i < kChunk / 4; ++i) {
             s2[i] = make_ulonglong2(s1, s1);
-            if constexpr (FEW) s2[i] = reinterpret_cast<const ulonglong2*>(scales)[ch * (kChunk / 4) + i];
+            if constexpr (FEW) s2[i] = reinterpret_cast<const ulonglong2*>(scales + c0)[ch * (kChunk / 4) + i];
           }
           tmem_wait(v);
           if (ch + 1 == kChunks) {  // D_b and its scales are in registers
@@ -404,8 +414,8 @@ fp8b_gemm_kernel(const __grid_constant__ CUtensorMap tmap_a, const __grid_consta
 #pragma unroll
         for (int i = 0; i < kCols / 2; ++i) unpack2(acc[i], part[2 * i * kM], part[(2 * i + 1) * kM]);
       } else if constexpr (FEW) {
-        const int64_t t0 = token0(it), nn = (int64_t)out0(it) + 32 * q + lane;
-        const int left = nn < p.n ? (int)(p.m - t0 < N ? p.m - t0 : N) : 0;
+        const int64_t t0 = token0(it) + c0, nn = (int64_t)out0(it) + 32 * q + lane;
+        const int left = nn < p.n ? (int)(p.m - t0 < kCols ? p.m - t0 : kCols) : 0;
         store_tokens<kCols>(acc, reinterpret_cast<Out*>(p.c) + t0 * p.ldc + nn, p.ldc, left);
       } else {
         store_row<kCols, Out>(acc, p, (int64_t)token0(it) + 32 * q, (int64_t)out0(it) + c0, lane,
@@ -421,12 +431,13 @@ fp8b_gemm_kernel(const __grid_constant__ CUtensorMap tmap_a, const __grid_consta
     if (warp == 0 && lane == 0)
       for (int g = issued > kStages ? issued - kStages : 0; g < issued; ++g)
         mbar_drain(full(g % kStages), (uint32_t)(g / kStages) & 1u, p.dev_status);
-    if (warp == 1) {  // (by the lane that issued them: elect picks the same one)
+    if (warp == 1 || (warp == 3 && L::kIssuers == 2)) {  // (by the lane that issued them: elect picks the same one)
       if (elect_one()) {
         mma_commit(drain_bar);
         mbar_drain(drain_bar, 0u, p.dev_status);
       }
     }
+    __syncthreads();
   }
   if (warp == 1) {
     __syncwarp();
