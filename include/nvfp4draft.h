@@ -334,6 +334,12 @@ int fp8w_gemv_argmax_ex(const w4a16_act_segment *seg, int nseg, int m, const fp8
  *   fp8b_rmsnorm   residual addition + RMSNorm -> E4M3 rows + scales per 128 columns
  *   fp8b_gemm      their product, one row to thousands
  *   spec_verify    verification of drafted tokens from given uniform numbers
+ *
+ * These kernels are launched with programmatic stream serialisation: one may
+ * start while the previous kernel on the stream finishes, but reads and writes
+ * no global memory (weights included) before that kernel has completed.  No
+ * workspace is used, so calls on different streams are independent.  Outputs
+ * must not overlap inputs, except where a call says so.
  */
 
 /* Largest k of fp8b_rmsnorm (a row is held in one CTA's registers). */

@@ -25,6 +25,21 @@
 // (distributed shared memory), so results do not depend on timing.
 // Every wait is bounded (2 s of globaltimer): one that runs out records
 // NVFP4_ERR_TIMEOUT in the caller's status word and the CTA unwinds.
+//
+// What bounds it, and what it measured (BF16 out unless stated):
+//   few tokens     HBM, the weight stream: 10 x 151936 x 5120 (FP32 out) 114.5 us, 6.85 TB/s, 1.0
+//                  of the measured copy; 1 x 5120 x 10240 11.6 us, 4.5 TB/s (0.67), of which about
+//                  5 us are launch, pipeline fill and the exchange of partial tiles.
+//   77 rows        18.2 us for 77 x 17408 x 5120 (0.74 of HBM): 136 tiles on 152 SMs, each K block's
+//                  32 KB from L2.
+//   prefill        2048 x 17408 x 5120 133.7 us, 2730 TFLOP/s, 0.71 of twice the measured BF16 rate.
+//                  Taking D_b out of TMEM for its scales after every K block is the price of the
+//                  format: a K block's MMAs take 512 cycles, the epilogue's loads and packed FMAs
+//                  (at 2 cycles a warp) 460, and the handovers between them, with TMEM full at two
+//                  buffers of 256 columns, raise the period to 750.  Without the epilogue the same
+//                  kernel takes 122 us, without loads either 106.  Measured and not kept: CTA pairs
+//                  (145 us, the handovers cross SMs), weights as MMA rows at 256 tokens (182 us, a
+//                  scale per column from shared memory), two MMA warps (137 us).
 #include <cooperative_groups.h>
 #include <cuda_bf16.h>
 
@@ -511,14 +526,15 @@ int launch_fp8b_gemm(const fp8b_act* a, const fp8b_weight* w, void* c, int c_dty
   const int64_t kblocks = nvfp4::cdiv(k, kK);
   const int sms = nvfp4::sm_count();
   // Form and tile: FEW with the smallest that holds all tokens, MANY beyond 64 with the
-  // tile whose whole waves take less time (a K block of 128 columns takes about 650
-  // cycles, of 256 about 750: the handovers weigh on the smaller).
+  // tile whose whole waves take less time (a K block of 128 columns takes about 600
+  // cycles, of 256 about 750: the handovers weigh on the smaller).  77 x 17408 x 5120: 128
+  // columns 18.2 us, 256 columns 22.5; 2048 x 17408 x 5120: 193 and 134.
   const bool few = m <= 64;
   int tile = m <= 16 ? 16 : m <= 32 ? 32 : 64;
   if (!few) {
     const int64_t mt = nvfp4::cdiv(m, kM);
     const int64_t w128 = nvfp4::cdiv(mt * nvfp4::cdiv(n, 128), sms), w256 = nvfp4::cdiv(mt * nvfp4::cdiv(n, 256), sms);
-    tile = w128 * 650 <= w256 * 750 ? 128 : 256;
+    tile = w128 * 600 <= w256 * 750 ? 128 : 256;
   }
   const int64_t mtiles = nvfp4::cdiv(m, few ? tile : kM), ntiles = nvfp4::cdiv(n, few ? kM : tile);
   const int64_t items = mtiles * ntiles;

@@ -19,6 +19,14 @@
 // in two words (the rounding errors of the additions are added up beside them,
 // Knuth's two-sum): off by about 2^-46 of W.  Binary64 is not used: the SM's one
 // binary64 unit takes 16 cycles a warp instruction.
+//
+// What bounds it: for large batches HBM (256 sequences of 151936 FP32 probabilities,
+// ragged drafts, 55.7 us; every sequence's target row and the draft rows of those that
+// refuse are about 250 MB, 4.5 TB/s, 0.66 of the measured copy; 121 us with sums joined in
+// binary64 and 512 threads a CTA); for few sequences the chain of dependent steps, each a
+// load's or a shuffle's latency: one sequence of 32768 5.8 us, of which launch about 2,
+// finding the refusal 0.8, the sums 2, their exchange 1 and the search 1.3 (17 us with one
+// CTA).  16 CTAs a sequence or 512 threads are no faster.
 
 #include <cooperative_groups.h>
 #include <cuda_bf16.h>
@@ -96,7 +104,7 @@ template <typename T>
 struct Vec;
 template <>
 struct Vec<float> {
-  static constexpr int VE = 4, kUnroll = 2;
+  static constexpr int VE = 4;
   uint4 raw;
   __device__ __forceinline__ void load(const float* p) {
     asm volatile("ld.global.nc.v4.u32 {%0,%1,%2,%3}, [%4];"
@@ -114,7 +122,7 @@ struct Vec<float> {
 };
 template <>
 struct Vec<__nv_bfloat16> {
-  static constexpr int VE = 8, kUnroll = 1;
+  static constexpr int VE = 8;
   uint4 raw;
   __device__ __forceinline__ void load(const __nv_bfloat16* p) {
     asm volatile("ld.global.nc.v4.u32 {%0,%1,%2,%3}, [%4];"
@@ -250,9 +258,9 @@ __device__ __noinline__ Sum lane_sum_checked(Rows<T> r, int v, int end, int step
 
 // One lane's sum of the weights of vectors first, first + step, ... below end.  (Not
 // inlined: both uses share the code, which a short kernel fetches for the first time.)
-template <typename T>
+template <typename T, int EL>
 __device__ __noinline__ Sum lane_sum(Rows<T> r, int first, int end, int step, int32_t* dev_status) {
-  constexpr int VE = Vec<T>::VE, U = Vec<T>::kUnroll;
+  constexpr int VE = Vec<T>::VE, U = EL / VE;  // vectors of each row in flight
   Sum2 sum{0ull, 0ull, 0ull};
   Sum edge{0.0f, 0.0f};
   bool edge_bad = false;
@@ -377,8 +385,9 @@ __device__ __forceinline__ bool below(float u, float q, float p) {  // u q < p, 
   return h < p || (h == p && fmaf(u, q, -h) < 0.0f);
 }
 
-template <typename T>
-__global__ void __launch_bounds__(kThreads, 4) spec_verify_kernel(const __grid_constant__ VerifyParams p) {
+// EL: elements of a row that a lane has in flight; CTAS: CTAs an SM.
+template <typename T, int EL, int CTAS>
+__global__ void __launch_bounds__(kThreads, CTAS) spec_verify_kernel(const __grid_constant__ VerifyParams p) {
   cg::cluster_group cluster = cg::this_cluster();
   const int ranks = 1 << p.log_ranks, rank = (int)blockIdx.x & (ranks - 1);
   const int64_t seq = (int)blockIdx.x >> p.log_ranks;
@@ -455,7 +464,7 @@ __global__ void __launch_bounds__(kThreads, 4) spec_verify_kernel(const __grid_c
   auto segment = [&](int w) { return min(c1, c0 + w * per_warp); };
   for (int pass = 0; pass < 2; ++pass) {
     const int w1 = segment(warp + 1), g0 = min(w1, segment(warp) + lane / kGroupLanes * per);
-    Sum sum = lane_sum(r, g0 + lane % kGroupLanes, min(w1, g0 + per), kGroupLanes, p.dev_status);
+    Sum sum = lane_sum<T, EL>(r, g0 + lane % kGroupLanes, min(w1, g0 + per), kGroupLanes, p.dev_status);
 #pragma unroll
     for (int d = 1; d < 32; d <<= 1) {
       if (d == kGroupLanes && lane % kGroupLanes == 0) group_part[warp][lane / kGroupLanes] = sum;
@@ -525,7 +534,7 @@ __global__ void __launch_bounds__(kThreads, 4) spec_verify_kernel(const __grid_c
       if (one && warp > 0) break;
       const int share = (v1 - v0 + threads - 1) / threads;
       const int mv = min(v1, v0 + (int)threadIdx.x * share), me = min(v1, mv + share);
-      const Sum mine = lane_sum(r, mv, me, 1, nullptr);
+      const Sum mine = lane_sum<T, EL>(r, mv, me, 1, nullptr);
       Sum upto = prefix(mine, lane);
       bool mine_next = warp == 0;
       if (!one) {
@@ -598,8 +607,13 @@ int launch_spec_verify(const spec_verify_input* in, int32_t* out_tokens, int64_t
   const int ranks = 1 << log_ranks;
   if (in->batch > 0x7FFFFFFF / ranks) return NVFP4_ERR_SHAPE;
   p.log_ranks = log_ranks;
-  const void* kern = in->dtype == NVFP4_DTYPE_F32 ? (const void*)spec_verify_kernel<float>
-                                                  : (const void*)spec_verify_kernel<__nv_bfloat16>;
+  // Few CTAs: twice the registers each, and for BF16 twice the loads in flight (one
+  // sequence 6.2 -> 5.8 us; another doubling is slower, 13.5 us against 11.5 for 24 x 151936).
+  const bool few = in->batch * ranks <= 2 * sms, f32 = in->dtype == NVFP4_DTYPE_F32;
+  const void* kern = f32 ? (few ? (const void*)spec_verify_kernel<float, 8, 2>
+                                : (const void*)spec_verify_kernel<float, 8, 4>)
+                         : (few ? (const void*)spec_verify_kernel<__nv_bfloat16, 16, 2>
+                                : (const void*)spec_verify_kernel<__nv_bfloat16, 8, 4>);
   void* args[] = {&p};
   return nvfp4::launch_dependent(kern, dim3((unsigned)(in->batch * ranks)), dim3(kThreads), 0, stream,
                                  (unsigned)ranks, args) == cudaSuccess

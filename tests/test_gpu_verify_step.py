@@ -234,7 +234,9 @@ def test_gemm(dev, m, n, k, dtype):
     check_gemm(got, a, w)
 
 
-@pytest.mark.parametrize("m,n,k", [(1, 5120, 10240), (24, 20000, 5120), (2048, 2176, 5120), (1, 151936, 512)])
+# (the last five: 256-column tiles, alone for up to 128 rows and as pairs of CTAs beyond, a pair's second half empty or ragged)
+@pytest.mark.parametrize("m,n,k", [(1, 5120, 10240), (24, 20000, 5120), (2048, 2176, 5120), (1, 151936, 512), (128, 40000, 272),
+                                   (300, 20001, 256), (385, 40000, 144), (1000, 9000, 400), (600, 20000, 1152)])
 def test_gemm_large(dev, m, n, k):
     a, w = make_gemm(dev, m, n, k)
     check_gemm(nd().fp8b_gemm(a, w, out_dtype=torch.float32), a, w)
