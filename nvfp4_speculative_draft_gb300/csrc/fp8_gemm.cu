@@ -136,6 +136,8 @@ __device__ __forceinline__ void store_tokens(const uint64_t (&acc)[N / 2], Out* 
 // 64 bytes of each row at a time go through 2 KB of the warp's own shared memory, so
 // that a store covers eight rows x 64 contiguous bytes rather than 32 rows x 16.  The
 // 16-byte pieces of row r lie at piece ^ (r / 2 % 4): neither side meets bank conflicts.
+// Rows that are not 16-byte aligned are stored by elements, neighbouring lanes
+// neighbouring outputs.
 template <int C, typename Out>
 __device__ __forceinline__ void store_row(const uint64_t (&acc)[C / 2], const Params& p, int64_t row0, int64_t n0,
                                           int lane, uint4* stage) {
@@ -162,28 +164,25 @@ __device__ __forceinline__ void store_row(const uint64_t (&acc)[C / 2], const Pa
       stage[lane * 4 + (i ^ (lane / 2 % 4))] = make_uint4(w[0], w[1], w[2], w[3]);
     }
     __syncwarp();
-    const int64_t col = n0 + (g * 4 + lane % 4) * kPiece;
+    const int64_t g0 = n0 + g * 4 * kPiece;
+    if (p.vector_store && g0 + 4 * kPiece <= p.n) {
+      const int64_t col = g0 + lane % 4 * kPiece;
 #pragma unroll
-    for (int i = 0; i < 4; ++i) {
-      const int r = 8 * i + lane / 4;
-      const uint4 v = stage[r * 4 + (lane % 4 ^ (r / 2 % 4))];
-      const int64_t row = row0 + r;
-      if (row < p.m && col < p.n) {
-        Out* dst = reinterpret_cast<Out*>(p.c) + row * p.ldc + col;
-        if (p.vector_store && col + kPiece <= p.n) {
-          *reinterpret_cast<uint4*>(dst) = v;
-        } else {
-          const uint32_t w[4] = {v.x, v.y, v.z, v.w};
-#pragma unroll
-          for (int e = 0; e < kPiece; ++e) {
-            if (col + e < p.n) {
-              if constexpr (sizeof(Out) == 4)
-                dst[e] = __uint_as_float(w[e]);
-              else
-                dst[e] = __ushort_as_bfloat16((unsigned short)(w[e / 2] >> (16 * (e & 1))));
-            }
-          }
-        }
+      for (int i = 0; i < 4; ++i) {
+        const int r = 8 * i + lane / 4;
+        const uint4 v = stage[r * 4 + (lane % 4 ^ (r / 2 % 4))];
+        const int64_t row = row0 + r;
+        if (row < p.m) *reinterpret_cast<uint4*>(reinterpret_cast<Out*>(p.c) + row * p.ldc + col) = v;
+      }
+    } else {
+      constexpr int kRow = 4 * kPiece;  // outputs of a row: 16 or 32 lanes
+      const int e = lane % kRow;
+#pragma unroll 4
+      for (int r0 = 0; r0 < 32; r0 += 32 / kRow) {
+        const int r = r0 + lane / kRow;
+        const Out* src = reinterpret_cast<const Out*>(stage + r * 4 + (e / kPiece ^ (r / 2 % 4))) + e % kPiece;
+        const int64_t row = row0 + r, col = g0 + e;
+        if (row < p.m && col < p.n) reinterpret_cast<Out*>(p.c)[row * p.ldc + col] = *src;
       }
     }
     __syncwarp();
