@@ -404,6 +404,30 @@ def test_verify_fine_borders(dev):
     assert np.array_equal(out[:, 0].cpu().numpy(), want)
 
 
+@pytest.mark.parametrize("v,dv,dtype", [(6000001, 0, torch.float32), (6000001, 6000001, torch.float32), (9000003, 2000001, torch.bfloat16)])
+def test_verify_very_wide_rows(dev, v, dv, dtype):
+    """Rows so wide that the search narrows in several steps."""
+    t, q, tok, u, r = make_wide(dev, v, dv)
+    t, q = t.to(dtype), None if q is None else q.to(dtype)
+    check_verify(t, q, tok, u, r)
+    check_verify(t, q, tok, u * 0 + 0.999, r)  # refused: the difference is sampled
+
+
+def make_wide(dev, v, dv):
+    g = gen(dev, v)
+    t = torch.softmax(torch.randn((2, 2, v), generator=g, device=dev) * 2, -1)
+    q = torch.softmax(torch.randn((2, 1, dv), generator=g, device=dev) * 2, -1) if dv else None
+    tok = torch.randint(0, v, (2, 1), generator=g, device=dev).int()
+    return t, q, tok, torch.rand((2, 1), generator=g, device=dev), torch.rand(2, generator=g, device=dev)
+
+
+def test_verify_most_drafts(dev):
+    t, q, tok, u, r = make_verify(dev, 3, 1024, 9, 9, torch.float32, 7)
+    out, acc = check_verify(t, q, tok, u * 1e-3, r)
+    check_verify(t, q, tok, u * 0, r, torch.tensor([1024, 1000, 31], dtype=torch.int32, device=dev))
+    assert acc.max().item() > 32
+
+
 @pytest.mark.parametrize("off_p,off_q", [(0, 1), (1, 1), (3, 2), (1, 0)])
 @pytest.mark.parametrize("dtype", [torch.float32, torch.bfloat16])
 def test_verify_strides(dev, off_p, off_q, dtype):
@@ -591,3 +615,38 @@ def test_refusals_leave_outputs_alone(dev):
             m.spec_verify(a.pop("target"), a.pop("tok"), a.pop("u"), a.pop("r"), **a)
     torch.cuda.synchronize()
     assert (res == 9).all()
+
+
+# ------------------------------------------------- offsets beyond 32 bits
+
+def test_offsets_pass_32_bits(dev):
+    """Tensors of more than 2^31 elements; the parts that lie beyond are checked."""
+    m = nd()
+    # quantiser: 2.2e9 elements, the last two blocks of rows
+    n, k = 131328, 16640
+    w = torch.empty((n, k), dtype=torch.bfloat16, device=dev)
+    for r in range(0, n, 16416):
+        w[r:r + 16416] = (randn(dev, r, 16416, k) * 0.02).to(torch.bfloat16)
+    q = m.fp8b_quantize(w)
+    values, scales = ref.quantize(w[-256:, :1024].contiguous())
+    assert torch.equal(q.scales[-2:, :8], scales) and torch.equal(ref.decode(q.codes[-256:, :1024]), values)
+    # norm: the same matrix as rows of activations
+    acts, h = m.fp8b_rmsnorm(w, torch.ones(k, dtype=torch.bfloat16, device=dev), 1e-6, residual=w)
+    tail = m.Fp8BlockActs(acts.codes[-3:], acts.scales[:, -3:], 3, k)
+    check_norm(tail, h[-3:], w[-3:], w[-3:], torch.ones(k, dtype=torch.bfloat16, device=dev), 1e-6)
+    del w, q, acts, h, tail
+    # product: 2.3e9 outputs
+    a, wt = make_gemm(dev, 15000, 151936, 32)
+    c = m.fp8b_gemm(a, wt)
+    last = m.Fp8BlockActs(a.codes[-70:], a.scales[:, -70:], 70, 32)
+    check_gemm(c[-70:], last, wt)
+    check_gemm(c[:70], m.Fp8BlockActs(a.codes[:70], a.scales[:, :70], 70, 32), wt)
+    del a, wt, c, last
+    # verification: 2.4e9 probabilities; sequences of one repeated set of rows
+    b, g, v = 4000, 3, 150001
+    t1, q1, tok1, u1, r1 = make_verify(dev, 4, g, v, v, torch.bfloat16, 3)
+    t = t1.repeat(b // 4, 1, 1)
+    out, acc = m.spec_verify(t, tok1.repeat(b // 4, 1), u1.repeat(b // 4, 1), r1.repeat(b // 4),
+                             draft_probs=q1.repeat(b // 4, 1, 1))
+    want, wacc = check_verify(t1, q1, tok1, u1, r1)
+    assert torch.equal(out, want.repeat(b // 4, 1)) and torch.equal(acc, wacc.repeat(b // 4))
