@@ -107,10 +107,13 @@ __device__ __forceinline__ uint2 codes_of(uint4 v, float s, bool fast, uint64_t 
 // (|q| >= 2^-10) leaves binary32's normal range; divisions otherwise.
 // (A rounding test with a division in doubt, as above, costs more here: up to a per
 // cent of the quotients of BF16 values by a BF16 maximum lie on a border exactly.)
+// The steps form -q, from -y: the remainder of x = +-0 is +0, and the last step's
+// (+0)(-y) + (-q0) is then -q0 for either sign, where (+0) y + q0 would lose the sign of
+// -0.  Conversion to E4M3 is symmetric, so a code's sign bit is flipped instead.
 struct Scale {
   float s;
   bool fast;
-  uint64_t y, neg;  // 1/s and -s, as pairs
+  uint64_t neg_y, pair;  // -1/s and s, as pairs
 };
 __device__ __forceinline__ Scale scale_of(float amax) {
   Scale o;
@@ -120,8 +123,8 @@ __device__ __forceinline__ Scale scale_of(float amax) {
   o.s = o.fast ? fmaf(fmaf(-448.0f, q, amax), c, q) : __fdiv_rn(amax, 448.0f);
   float y;
   asm("rcp.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"(o.s));
-  o.y = f32x2_splat(y);
-  o.neg = f32x2_splat(-o.s);
+  o.neg_y = f32x2_splat(-y);
+  o.pair = f32x2_splat(o.s);
   return o;
 }
 __device__ __forceinline__ uint64_t mul_f32x2(uint64_t a, uint64_t b) {
@@ -143,9 +146,10 @@ __device__ __forceinline__ uint2 codes_of(const uint64_t (&x)[4], const Scale& s
   if (sc.fast) {
 #pragma unroll
     for (int j = 0; j < 4; ++j) {
-      const uint64_t q = mul_f32x2(x[j], sc.y);
-      c[j] = e4m3_pair2(fma_f32x2(fma_f32x2(sc.neg, q, x[j]), sc.y, q));
+      const uint64_t nq = mul_f32x2(x[j], sc.neg_y);  // -q0
+      c[j] = e4m3_pair2(fma_f32x2(fma_f32x2(sc.pair, nq, x[j]), sc.neg_y, nq));
     }
+    return make_uint2((c[0] | c[1] << 16) ^ 0x80808080u, (c[2] | c[3] << 16) ^ 0x80808080u);
   } else if (sc.s == 0.0f) {
     return make_uint2(0u, 0u);
   } else {
