@@ -411,8 +411,9 @@ typedef struct fp8b_norm_input {
  * FP32 in a fixed order.  gamma as stored, as in w4a16_act_segment.
  *   out   codes and scales written for rows 0..out->m-1; out->m >= 1,
  *         out->k a multiple of 16, 16..FP8B_MAX_K.
- * A row with a non-finite value, or whose sum of squares leaves FP32's range:
- * that row's codes and scales undefined, NVFP4_ERR_NONFINITE to dev_status.
+ * A row with a non-finite value, or whose sum of squares exceeds FP32's range:
+ * that row's codes and scales undefined, NVFP4_ERR_NONFINITE to dev_status.  Rows
+ * of small values are normalised whatever their magnitude, also with eps = 0.
  * Workspace: none.
  */
 int fp8b_rmsnorm(const fp8b_norm_input *in, const fp8b_act *out, const nvfp4_exec *ex);

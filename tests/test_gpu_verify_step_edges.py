@@ -1,4 +1,4 @@
-"""Edges of the verify step's operators on the GPU: signs of zeros, code bytes.
+"""Edges of the verify step's operators on the GPU: signs of zeros, rows of tiny values.
 
 Codes are compared byte by byte, so that -0 (0x80) and +0 (0x00) differ: the
 contract gives every code the sign of its value, also where it rounds to zero.
@@ -7,7 +7,7 @@ import pytest
 import torch
 
 import verify_step_ref as ref
-from test_gpu_verify_step import nd, randn, u8
+from test_gpu_verify_step import check_norm, nd, randn, u8
 
 pytestmark = pytest.mark.gpu
 
@@ -62,3 +62,48 @@ def test_norm_sign_of_zero_with_gamma(dev, m, k, with_res):
     y = torch.signbit(x if r is None else h) ^ torch.signbit(g)[None]
     s = acts.scales.t().repeat_interleave(ref.BLOCK, 1)[:, :k]
     assert torch.equal((u8(acts.codes) >= 0x80)[s > 0], y[s > 0])
+
+
+# ------------------------------------------ rows whose squares leave binary32's range
+
+# magnitudes of a row; around 2^-50 the squares' mean passes from the plain sum to the scaled one
+TINY = [2.0 ** -e for e in (40, 48, 49, 50, 51, 52, 60, 63, 64, 70, 76, 100, 120, 126, 130)]
+
+
+@pytest.mark.parametrize("eps", [0.0, 2.0 ** -148, 1e-38, 2.0 ** -101, 2.0 ** -100, 1e-24])
+@pytest.mark.parametrize("k", [16, 128, 272, 2064, 5120, 17408])
+@pytest.mark.parametrize("with_res", [False, True])
+def test_norm_of_tiny_rows(dev, k, eps, with_res):
+    """Finite rows are normalised whatever their magnitude: the squares of values below 2^-63 are not
+    normal binary32 numbers, those below 2^-75 are zero.  (Tolerance: that of every other row; scaling a
+    row by a power of two rounds nothing.)"""
+    eps = torch.tensor(eps).item()  # as binary32
+    x = randn(dev, k, 3 * len(TINY) + 2, k)
+    x[0] = 0.0
+    x[1, k // 2:] = 0.0
+    for i, t in enumerate(TINY):
+        x[3 * i + 2] *= t          # between rows of other magnitudes, which share a CTA with it
+        x[3 * i + 3, : k // 2] *= t
+    x = x.to(torch.bfloat16)
+    x[4, 0] = 2.0 ** -133          # the smallest of all values, alone in its row
+    x[4, 1:] = 0.0
+    r = x.flip(0) * 2.0 ** -20 if with_res else None
+    g = (1 + 0.05 * randn(dev, k + 1, k)).to(torch.bfloat16)
+    status = torch.zeros(1, dtype=torch.int32, device=dev)
+    acts, h = nd().fp8b_rmsnorm(x, g, eps, residual=r, dev_status=status)
+    assert status.item() == 0
+    check_norm(acts, h, x, r, g, eps)
+
+
+def test_norm_of_tiny_rows_leaves_the_residual_stream(dev):
+    """h is written as it is, also in place, where the row is scaled to be summed."""
+    m = nd()
+    x = (randn(dev, 1, 8, 512) * 2.0 ** -80).to(torch.bfloat16)
+    r = (randn(dev, 2, 8, 512) * 2.0 ** -81).to(torch.bfloat16)
+    g = torch.ones(512, dtype=torch.bfloat16, device=dev)
+    want, h = m.fp8b_rmsnorm(x, g, 0.0, residual=r)
+    check_norm(want, h, x, r, g, 0.0)
+    target = r.clone()
+    got, _ = m.fp8b_rmsnorm(x, g, 0.0, residual=target, residual_out=target)
+    assert torch.equal(target, h)
+    assert torch.equal(u8(got.codes), u8(want.codes)) and torch.equal(got.scales, want.scales)
