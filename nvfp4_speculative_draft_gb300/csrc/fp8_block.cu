@@ -306,6 +306,7 @@ int launch_fp8b_rmsnorm(const fp8b_norm_input* in, const fp8b_act* out, int32_t*
   const int v = p.nvec > 2048 ? 4 : p.nvec > 1024 || (many && p.nvec > 256) ? 2 : 1;
   const int T = (int)nvfp4::cdiv(warps, v) * 32;
   if (v == 4) return launch_norm<4, 1024>(p, T, stream);
-  if (v == 2) return T <= 320 ? launch_norm<2, 320>(p, T, stream) : launch_norm<2, 1024>(p, T, stream);
+  if (v == 2) return launch_norm<2, 1024>(p, T, stream);
+  // (compiled for 256 threads: 100000 x 512 58.4 us against 59.9)
   return T <= 256 ? launch_norm<1, 256>(p, T, stream) : launch_norm<1, 1024>(p, T, stream);
 }
