@@ -141,18 +141,27 @@ struct Attribute {
   ~Attribute() { Py_DECREF(o); }
 };
 
-// Stream, status word and current device of one call.
+// Stream, status word and current device of one call.  While it lives, the call's stream
+// is the current one, so that outputs are allocated on it: memory that work queued on
+// another stream may still use is not handed to this call, nor this call's to others.
+// (So it is made before any output.)
 struct Call {
   c10::cuda::OptionalCUDAGuard guard;
+  c10::cuda::OptionalCUDAStreamGuard stream_guard;
   nvfp4_exec ex;
   Call(at::Device dev, PyObject* stream, PyObject* status) {
     if (c10::cuda::current_device() != dev.index()) guard.set_device(dev);
     ex = nvfp4_exec{};
+    const cudaStream_t current = c10::cuda::getCurrentCUDAStream(dev.index()).stream();
     if (stream == Py_None) {
-      ex.stream = c10::cuda::getCurrentCUDAStream(dev.index()).stream();
+      ex.stream = current;
     } else {
       ex.stream = PyLong_AsVoidPtr(stream);
       if (ex.stream == nullptr && PyErr_Occurred()) throw python_error();
+      // (the legacy default stream's handle is another name of PyTorch's default stream)
+      const cudaStream_t given =
+          ex.stream == cudaStreamLegacy ? nullptr : static_cast<cudaStream_t>(ex.stream);
+      if (given != current) stream_guard.reset_stream(c10::cuda::getStreamFromExternal(given, dev.index()));
     }
     if (status != Py_None) {
       const Tensor* t = tensor_of(status);
@@ -212,6 +221,7 @@ PyObject* quantize(PyObject*, PyObject* const* a, Py_ssize_t nargs) {
   const Tensor& w = *tensor_of(a[0]);
   if (w.dim() != 2 || w.scalar_type() != at::kBFloat16 || !rows_ok(w))
     refuse("w", &w, at::kBFloat16, {-1, -1}, kRowsText);
+  const Call call(dev, a[3], a[4]);
   const int64_t n = w.size(0), k = w.size(1);
   Tensor codes, scales;
   if (a[1] != Py_None) {
@@ -222,7 +232,6 @@ PyObject* quantize(PyObject*, PyObject* const* a, Py_ssize_t nargs) {
     codes = make({n, k}, at::kFloat8_e4m3fn, dev);
     scales = make({blocks(n), blocks(k)}, at::kFloat, dev);
   }
-  Call call(dev, a[3], a[4]);
   const int rc = lib.quantize(w.data_ptr(), n, k, ld(w), static_cast<uint8_t*>(codes.data_ptr()), scales.data_ptr<float>(), &call.ex);
   if (rc != NVFP4_OK) return fail("fp8b_quantize", rc);
   return Py_BuildValue("(NN)", wrap(codes), wrap(scales));
@@ -237,6 +246,7 @@ PyObject* rmsnorm(PyObject*, PyObject* const* a, Py_ssize_t nargs) {
   const Tensor& x = *tensor_of(a[0]);
   if (x.dim() != 2 || x.scalar_type() != at::kBFloat16 || !rows_ok(x))
     refuse("x", &x, at::kBFloat16, {-1, -1}, kRowsText);
+  const Call call(dev, a[6], a[7]);
   const int64_t m = x.size(0), k = x.size(1);
   fp8b_norm_input in{};
   in.x = x.data_ptr();
@@ -269,7 +279,6 @@ PyObject* rmsnorm(PyObject*, PyObject* const* a, Py_ssize_t nargs) {
     scales = make({blocks(k), m}, at::kFloat, dev);
     out = fp8b_act{static_cast<uint8_t*>(codes.data_ptr()), ld(codes), scales.data_ptr<float>(), m, m, k};
   }
-  Call call(dev, a[6], a[7]);
   const int rc = lib.rmsnorm(&in, &out, &call.ex);
   if (rc != NVFP4_OK) return fail("fp8b_rmsnorm", rc);
   PyObject* ho = a[4] != Py_None ? Py_NewRef(a[4]) : h.defined() ? wrap(h) : Py_NewRef(Py_None);
@@ -299,8 +308,8 @@ PyObject* gemm(PyObject*, PyObject* const* a, Py_ssize_t nargs) {
   if (given == nullptr && (a[3] != Py_None || !THPDtype_Check(a[2]))) throw Refusal("out must be a tensor and out_dtype a torch.dtype");
   const at::ScalarType type = given != nullptr ? given->scalar_type() : reinterpret_cast<THPDtype*>(a[2])->scalar_type;
   if (type != at::kFloat && type != at::kBFloat16) throw Refusal("out must be float32 or bfloat16");
+  const Call call(dev, a[4], a[5]);
   Tensor out = given != nullptr ? need_rows(a[3], "out", type, dev, {acts.a.m, w.n}) : make({acts.a.m, w.n}, type, dev);
-  Call call(dev, a[4], a[5]);
   const int rc = lib.gemm(&acts.a, &w, out.data_ptr(), type == at::kFloat ? NVFP4_DTYPE_F32 : NVFP4_DTYPE_BF16,
                           out.size(0) > 1 ? out.stride(0) : out.size(1), &call.ex);
   if (rc != NVFP4_OK) return fail("fp8b_gemm", rc);
@@ -350,6 +359,7 @@ PyObject* verify(PyObject*, PyObject* const* a, Py_ssize_t nargs) {
     }
   }
   if (a[5] != Py_None) in.num_draft = need_vector(a[5], "num_draft", at::kInt, dev, in.batch).data_ptr<int32_t>();
+  const Call call(dev, a[8], a[9]);
   Tensor out, accepted;
   if (a[6] != Py_None) {  // may be wider, or longer
     const Tensor* t = tensor_of(a[6]);
@@ -369,7 +379,6 @@ PyObject* verify(PyObject*, PyObject* const* a, Py_ssize_t nargs) {
   } else {
     accepted = make({in.batch}, at::kInt, dev);
   }
-  Call call(dev, a[8], a[9]);
   const int rc = lib.verify(&in, out.data_ptr<int32_t>(), out.size(0) > 1 ? out.stride(0) : out.size(1),
                             accepted.data_ptr<int32_t>(), &call.ex);
   if (rc != NVFP4_OK) return fail("spec_verify", rc);

@@ -1,4 +1,4 @@
-"""Edges of the verify step's operators on the GPU: signs of zeros, rows of tiny values.
+"""Edges of the verify step's operators on the GPU: signs of zeros, rows of tiny values, memory of other streams.
 
 Codes are compared byte by byte, so that -0 (0x80) and +0 (0x00) differ: the
 contract gives every code the sign of its value, also where it rounds to zero.
@@ -107,3 +107,58 @@ def test_norm_of_tiny_rows_leaves_the_residual_stream(dev):
     got, _ = m.fp8b_rmsnorm(x, g, 0.0, residual=target, residual_out=target)
     assert torch.equal(target, h)
     assert torch.equal(u8(got.codes), u8(want.codes)) and torch.equal(got.scales, want.scales)
+
+
+# --------------------------------------------------- outputs on the call's stream
+
+def segment_stream(t):
+    """The stream whose memory pool holds t."""
+    for s in torch.cuda.memory_snapshot():
+        if s["address"] <= t.data_ptr() < s["address"] + s["total_size"]:
+            return s["stream"]
+    raise AssertionError("not in the allocator's memory")
+
+
+@pytest.mark.parametrize("handle", [False, True])
+def test_outputs_are_allocated_on_the_calls_stream(dev, handle):
+    """With ``stream`` given: memory that the current stream's queued work may still use is not taken."""
+    m = nd()
+    s = torch.cuda.Stream()
+    stream = s.cuda_stream if handle else s
+    w = torch.ones((128, 256), dtype=torch.bfloat16, device=dev)
+    x = torch.ones((4, 256), dtype=torch.bfloat16, device=dev)
+    g = torch.ones(256, dtype=torch.bfloat16, device=dev)
+    p = torch.full((2, 3, 64), 1 / 64, device=dev)
+    tok, u, r = torch.zeros((2, 2), dtype=torch.int32, device=dev), torch.zeros((2, 2), device=dev), torch.zeros(2, device=dev)
+
+    def outputs(st):
+        q = m.fp8b_quantize(w, stream=st)
+        a, h = m.fp8b_rmsnorm(x, g, residual=x, stream=st)
+        c = m.fp8b_gemm(a, q, stream=st)
+        tokens, accepted = m.spec_verify(p, tok, u, r, stream=st)
+        return q.codes, q.scales, a.codes, a.scales, h, c, tokens, accepted
+
+    torch.cuda.synchronize()
+    current = torch.cuda.current_stream().cuda_stream
+    got = outputs(stream)
+    assert all(segment_stream(t) == s.cuda_stream for t in got)
+    assert torch.cuda.current_stream().cuda_stream == current  # restored
+    s.synchronize()
+    for st in (None, torch.cuda.current_stream(), current):
+        want = outputs(st)
+        assert all(segment_stream(t) == current for t in want)
+        torch.cuda.synchronize()
+        assert all(torch.equal(a.view(torch.uint8), b.view(torch.uint8)) for a, b in zip(got, want))
+    with torch.cuda.stream(s):  # the current stream's outputs while another one is current
+        want = outputs(current)
+    assert all(segment_stream(t) == current for t in want)
+    torch.cuda.synchronize()
+    for st in (1, 0):  # the default stream by its legacy handle, and by none
+        assert all(segment_stream(t) == 0 for t in outputs(st))
+    torch.cuda.synchronize()
+    bad = torch.zeros((3, 3), dtype=torch.int32, device=dev)
+    with pytest.raises(ValueError):  # a refusal restores it too
+        m.spec_verify(p, bad, u, r, stream=stream)
+    with pytest.raises(ValueError):
+        m.spec_verify(p, tok, u, r, out_accepted=bad, stream=stream)
+    assert torch.cuda.current_stream().cuda_stream == current
