@@ -183,7 +183,7 @@ _NATIVE = None
 
 def load(path: str = LIB_PATH):
     """Load the CUDA library (raises if it was not built)."""
-    global _LIB, _NATIVE
+    global _LIB
     if _LIB is not None:
         return _LIB
     if not os.path.exists(path):
@@ -212,10 +212,7 @@ def load(path: str = LIB_PATH):
     L.spec_verify.argtypes = [P(_VerifyInput), vp, i64, vp, P(_Exec)]
     for f in EXPORTED + ("w4a16_gemv_argmax_noalloc",):
         getattr(L, f).restype = ctypes.c_int
-    native = _load_binding()
-    native.bind(*(ctypes.cast(getattr(L, f), vp).value
-                  for f in ("fp8b_quantize", "fp8b_rmsnorm", "fp8b_gemm", "spec_verify")), Nvfp4Error)
-    _LIB, _NATIVE = L, native
+    _LIB = L
     return L
 
 
@@ -623,8 +620,14 @@ def fp8w_gemv_argmax_ex(segments: Sequence, weight: Fp8Weight, mask: Optional[to
 # one), as under ``torch.cuda.stream(stream)``.
 
 def _native():
+    """The native module, loaded on the first of these calls: it is built for one version of
+    PyTorch, which the other calls do not need."""
+    global _NATIVE
     if _NATIVE is None:
-        load()
+        L, native = load(), _load_binding()
+        native.bind(*(ctypes.cast(getattr(L, f), ctypes.c_void_p).value
+                      for f in ("fp8b_quantize", "fp8b_rmsnorm", "fp8b_gemm", "spec_verify")), Nvfp4Error)
+        _NATIVE = native
     return _NATIVE
 
 
