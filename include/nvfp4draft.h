@@ -425,6 +425,9 @@ int fp8b_rmsnorm(const fp8b_norm_input *in, const fp8b_act *out, const nvfp4_exe
  *   a      a->k == w->k; a->m >= 1 (one token to prefill sizes).
  *   c      device [m, ldc] of c_dtype (F32 or BF16), ldc >= n, aligned to its type.
  * Rows of C at or past m and columns past n are left as they were.
+ * sa * sw is formed first, in FP32.  Below 2^-126 it loses bits: less than 2^-125 of
+ * the result for each block.  Sums that are not finite, as where sa * sw overflows or
+ * an operand is not finite: NVFP4_ERR_NONFINITE to dev_status.
  * Workspace: none.  Waits inside the kernel are bounded; one that runs out
  * writes NVFP4_ERR_TIMEOUT to dev_status and leaves C incomplete.
  */

@@ -421,6 +421,15 @@ fp8b_gemm_kernel(const __grid_constant__ CUtensorMap tmap_a, const __grid_consta
         }
       }
       if (!ok) break;
+      // What is not finite is reported, such as a product of scales that overflowed: 0 times
+      // it is NaN.  (Here, once a tile, that costs at most 1 %; by warp 2, whose products each
+      // K block waits for, it took 77 x 17408 x 5120 from 18.1 to 23.2 us.)
+      uint64_t zero = 0ull;
+#pragma unroll
+      for (int i = 0; i < kCols / 2; ++i) fma_f32x2(zero, acc[i], 0ull);
+      float z0, z1;
+      unpack2(zero, z0, z1);
+      if (z0 + z1 != 0.0f) nvfp4::report(p.dev_status, NVFP4_ERR_NONFINITE);
       if (L::kSplit && ranks > 1) {
         // the ring's memory: every load and MMA has left it (all D_b were waited for);
         // [column][MMA row], so that neighbouring lanes write neighbouring words

@@ -1,4 +1,5 @@
-"""Edges of the verify step's operators on the GPU: signs of zeros, rows of tiny values, memory of other streams.
+"""Edges of the verify step's operators on the GPU: signs of zeros, tiny values, the range of scales, memory
+of other streams.
 
 Codes are compared byte by byte, so that -0 (0x80) and +0 (0x00) differ: the
 contract gives every code the sign of its value, also where it rounds to zero.
@@ -7,7 +8,7 @@ import pytest
 import torch
 
 import verify_step_ref as ref
-from test_gpu_verify_step import check_norm, nd, randn, u8
+from test_gpu_verify_step import check_gemm, check_norm, gemm_tol, make_gemm, nd, randn, u8
 
 pytestmark = pytest.mark.gpu
 
@@ -162,3 +163,48 @@ def test_outputs_are_allocated_on_the_calls_stream(dev, handle):
     with pytest.raises(ValueError):
         m.spec_verify(p, tok, u, r, out_accepted=bad, stream=stream)
     assert torch.cuda.current_stream().cuda_stream == current
+
+
+# ------------------------------------------------------ products of scales
+
+# every tile: few tokens (split over K and not), many, with a ragged last block of rows and columns
+RANGE_SIZES = [(1, 300, 2064), (20, 260, 272), (50, 200, 400), (100, 500, 1040), (300, 20000, 272)]
+
+
+@pytest.mark.parametrize("m,n,k", RANGE_SIZES)
+def test_gemm_reports_scales_out_of_range(dev, m, n, k):
+    """A product of scales past binary32's range makes its results not finite, even where the
+    block's sum is zero: the status says so; other results are as they were."""
+    mod = nd()
+    a, w = make_gemm(dev, m, n, k)
+    last = ref.BLOCK * (ref.blocks(n) - 1)
+    w.codes[last:, :ref.BLOCK] = 0
+    status = torch.zeros(1, dtype=torch.int32, device=dev)
+    want = mod.fp8b_gemm(a, w, out_dtype=torch.float32, dev_status=status)
+    assert status.item() == 0
+    check_gemm(want, a, w)
+    for sa, sw in ((1e30, 1e30), (float("inf"), 1.0), (1.0, float("nan"))):
+        a2 = mod.Fp8BlockActs(a.codes, a.scales.clone(), m, k)
+        w2 = mod.Fp8BlockWeight(w.codes, w.scales.clone(), n, k)
+        a2.scales[0, m - 1] = sa
+        w2.scales[-1, 0] = sw
+        status.zero_()
+        got = mod.fp8b_gemm(a2, w2, out_dtype=torch.float32, dev_status=status)
+        assert status.item() == 7
+        assert not torch.isfinite(got[m - 1, last:]).any()
+        assert torch.equal(got[:m - 1, :last], want[:m - 1, :last])
+
+
+@pytest.mark.parametrize("m,n,k", RANGE_SIZES)
+def test_gemm_of_tiny_scales(dev, m, n, k):
+    """Products of scales below 2^-126 round to multiples of 2^-149: by at most 2^-150 times a block's
+    sum, which is below 128 x 448^2 < 2^24.7; so 2^-125 for each block beside the usual tolerance, and
+    sums below 2^-126 another 2^-150 each."""
+    a, w = make_gemm(dev, m, n, k)
+    a.scales.mul_(2.0 ** -80)   # 2^-10 .. 2^-2 of make_gemm, times this
+    w.scales.mul_(2.0 ** -52)
+    status = torch.zeros(1, dtype=torch.int32, device=dev)
+    got = nd().fp8b_gemm(a, w, out_dtype=torch.float32, dev_status=status)
+    c, s = ref.gemm(a.codes, a.scales, w.codes, w.scales)
+    assert status.item() == 0
+    assert ((got.double() - c).abs() <= gemm_tol(c, s, k, False) + ref.blocks(k) * 2.0 ** -124).all()
