@@ -406,6 +406,9 @@ typedef struct fp8b_norm_input {
  *   y = h / sqrt(mean(h^2) + eps) * gamma     (y = h without gamma)
  *   per row and 128 columns: s = fl32(max|y| / 448),
  *   code = E4M3_RNE_satfinite(fl32(y / s)) with the sign of y; +0 where s = 0.
+ *   (Exactly so without gamma, where y is a BF16 value.  With it fl32(y / s) may be off by
+ *   an ulp where y / s is within 2^-20 ulp of halfway between two FP32 numbers, which
+ *   decides about 2^-39 of the codes.)
  * h is the new residual stream (residual_out); the norm reads it as rounded, as
  * the next sublayer will.  y stays in FP32 until its codes are rounded; sums are
  * FP32 in a fixed order.  gamma as stored, as in w4a16_act_segment.
@@ -467,8 +470,8 @@ typedef struct spec_verify_input {
  *   drafts were accepted: the lowest j with  w_0 + ... + w_j > r sum(w), r the
  *   sequence's sample_u; the last j with w_j > 0 where rounding or r >= 1 leaves
  *   none.  w without any mass falls back to p_a; p_a without any, to token 0.
- * Sums are carried in two binary32 words and joined in binary64 (about 2^-46 of
- * sum(w)), in a fixed order: the same call gives the same tokens.
+ * Sums are carried in two binary32 words (about 2^-46 of sum(w)), in a fixed order:
+ * the same call gives the same tokens.
  *   out_tokens  device int32 [batch, ld_out], ld_out >= g + 1: the accepted drafts,
  *               the sampled token, then -1 up to g.
  *   accepted    device int32 [batch]: a.

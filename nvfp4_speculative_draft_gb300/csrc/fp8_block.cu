@@ -5,8 +5,8 @@
 //     s = fl32(amax / 448),   c = E4M3_RNE_SATFINITE(fl32(x / s))
 //
 // Both are bound by HBM: every input element is read once and held in registers
-// between the maximum and its codes, every output written once.  The correctly
-// rounded quotient's code comes from the rounding test of e4m3.cuh.
+// between the maximum and its codes, every output written once.  Codes come from the
+// quotient's one correction step (e4m3.cuh).
 
 #include "e4m3.cuh"
 

@@ -32,14 +32,20 @@
 //                  5 us are launch, pipeline fill and the exchange of partial tiles.
 //   77 rows        18.2 us for 77 x 17408 x 5120 (0.74 of HBM): 136 tiles on 152 SMs, each K block's
 //                  32 KB from L2.
-//   prefill        2048 x 17408 x 5120 133.7 us, 2730 TFLOP/s, 0.71 of twice the measured BF16 rate.
-//                  Taking D_b out of TMEM for its scales after every K block is the price of the
-//                  format: a K block's MMAs take 512 cycles, the epilogue's loads and packed FMAs
-//                  (at 2 cycles a warp) 460, and the handovers between them, with TMEM full at two
-//                  buffers of 256 columns, raise the period to 750.  Without the epilogue the same
-//                  kernel takes 122 us, without loads either 106.  Measured and not kept: CTA pairs
-//                  (145 us, the handovers cross SMs), weights as MMA rows at 256 tokens (182 us, a
-//                  scale per column from shared memory), two MMA warps (137 us).
+//   prefill        2048 x 17408 x 5120 133.7 us in a short graph of calls, 2730 TFLOP/s, 0.71 of
+//                  twice the measured BF16 rate; 148 to 155 us in long runs of calls, under the
+//                  power limit (0.61 to 0.64).  FP32 out 151 us.  A K block's MMAs take 512 cycles,
+//                  the tile's period is 750.  Above the floor of 95 us are, by trials of the same
+//                  kernel: about 13 us of the last wave (1088 tiles on 152 SMs are 7.16 waves, run
+//                  as eight; SMs are active 86 % of the time), about 16 us of operand loads
+//                  (without epilogue 122 us, without loads either 106), and 12 us of the epilogue,
+//                  which takes every D_b out of TMEM for its scales, with TMEM full at two buffers
+//                  of 256 columns.  No unit is busy throughout (tensor pipe 66 %, shared memory's
+//                  data pipe 57 % while SMs are active).  Measured and not kept: CTA pairs (145 us,
+//                  the handovers cross SMs), weights as MMA rows at 256 tokens (182 us, a scale
+//                  per column from shared memory), two MMA warps (137 us).
+//   129 to 1024 rows against narrow outputs   tiles do not fill the SMs: 256 x 5120 x 5120 14.8 us
+//                  and 512 x 5120 x 5120 19.7 us (floors 4.4 and 7.0), 80 tiles on 152 SMs, unsplit.
 #include <cooperative_groups.h>
 #include <cuda_bf16.h>
 
@@ -550,7 +556,8 @@ int launch_fp8b_gemm(const fp8b_act* a, const fp8b_weight* w, void* c, int c_dty
   // K is split while that finds idle SMs and leaves eight blocks to each CTA.  Where two
   // CTAs share an SM, clusters (which stay within a group of SMs) fill about 8/5 of the
   // SMs' number: 5120 x 10240, one token: 6 parts 12.4 us, 7 parts 17.4, 3 parts 13.0, 1
-  // part 21.9.
+  // part 21.9.  (Six parts at most for every shape, of the eight that a cluster may hold:
+  // measured at this one.)
   const int64_t slots = tile <= 32 ? (int64_t)sms * 8 / 5 : sms;
   int split = 1;
   while (tile <= 128 && split < 6 && items * (split + 1) <= slots && kblocks / (split + 1) >= 8) ++split;

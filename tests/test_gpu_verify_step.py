@@ -234,7 +234,7 @@ def test_gemm(dev, m, n, k, dtype):
     check_gemm(got, a, w)
 
 
-# (the last five: 256-column tiles, alone for up to 128 rows and as pairs of CTAs beyond, a pair's second half empty or ragged)
+# (the last five: 256-column tiles, several a CTA, one row of tiles and more, the last rows and columns ragged)
 @pytest.mark.parametrize("m,n,k", [(1, 5120, 10240), (24, 20000, 5120), (2048, 2176, 5120), (1, 151936, 512), (128, 40000, 272),
                                    (300, 20001, 256), (385, 40000, 144), (1000, 9000, 400), (600, 20000, 1152)])
 def test_gemm_large(dev, m, n, k):
