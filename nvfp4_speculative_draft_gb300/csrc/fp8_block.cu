@@ -21,7 +21,7 @@ constexpr int kBlock = 128;  // rows and columns of a weight block, columns of a
 // One CTA per 128 x 128 block: thread t holds the eight 16-byte vectors of rows
 // t/16 + 16 i, columns 8 (t % 16).., so a warp's load covers two rows x 256 bytes and
 // a CTA has 32 KB in flight.  Bound by HBM (3 bytes an element) once the quotients
-// cost few instructions: 151936 x 5120 takes 363 us, 6.44 TB/s, 0.95 of the measured
+// cost few instructions: 151936 x 5120 takes 362 us, 6.45 TB/s, 0.95 of the measured
 // copy; with a rounding test and a division in doubt it took 432, with a second
 // correction step of the quotient 404.  Measured and not kept: a persistent CTA with
 // a TMA ring of blocks (390 us even without the quotients), 512 threads a block (377),
@@ -75,8 +75,8 @@ fp8b_quantize_kernel(const uint4* __restrict__ w, int64_t n, int64_t k, int64_t 
 //
 // Bound by HBM (7 bytes an element with the residual) while it stays below about 20
 // instructions an element, hence the packed FP32 and BF16 arithmetic; 32 registers
-// keep 2048 threads on an SM.  8192 x 5120 with residual and gamma takes 45.4 us,
-// 6.49 TB/s, 0.96 of the measured copy (72.5 us with scalar arithmetic, divisions and
+// keep 2048 threads on an SM.  8192 x 5120 with residual and gamma takes 44.6 to
+// 45.8 us, 6.44 TB/s, 0.95 of the measured copy at least (72.5 us with scalar arithmetic, divisions and
 // one vector a thread; a CTA that walks over rows with the next row's loads in flight
 // is slower, 55 us).  One row of 5120: 2.4 us, mostly the launch.
 struct NormParams {

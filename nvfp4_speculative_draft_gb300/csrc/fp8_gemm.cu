@@ -27,25 +27,26 @@
 // NVFP4_ERR_TIMEOUT in the caller's status word and the CTA unwinds.
 //
 // What bounds it, and what it measured (BF16 out unless stated):
-//   few tokens     HBM, the weight stream: 10 x 151936 x 5120 (FP32 out) 114.5 us, 6.85 TB/s, 1.0
-//                  of the measured copy; 1 x 5120 x 10240 11.6 us, 4.5 TB/s (0.67), of which about
+//   few tokens     HBM, the weight stream: 10 x 151936 x 5120 (FP32 out) 114 to 117 us, 6.7 to 6.85
+//                  TB/s, 0.99 to 1.0 of the measured copy; 1 x 5120 x 10240 11.6 us, 4.5 TB/s (0.67), of which about
 //                  5 us are launch, pipeline fill and the exchange of partial tiles.
 //   77 rows        18.2 us for 77 x 17408 x 5120 (0.74 of HBM): 136 tiles on 152 SMs, each K block's
 //                  32 KB from L2.
 //   prefill        2048 x 17408 x 5120 133.7 us in a short graph of calls, 2730 TFLOP/s, 0.71 of
 //                  twice the measured BF16 rate; 148 to 155 us in long runs of calls, under the
-//                  power limit (0.61 to 0.64).  FP32 out 151 us.  A K block's MMAs take 512 cycles,
+//                  power limit (0.61 to 0.64).  FP32 out 150 us.  A K block's MMAs take 512 cycles,
 //                  the tile's period is 750.  Above the floor of 95 us are, by trials of the same
 //                  kernel: about 13 us of the last wave (1088 tiles on 152 SMs are 7.16 waves, run
-//                  as eight; SMs are active 86 % of the time), about 16 us of operand loads
+//                  as eight; SMs are active 87 % of the time), about 16 us of operand loads
 //                  (without epilogue 122 us, without loads either 106), and 12 us of the epilogue,
 //                  which takes every D_b out of TMEM for its scales, with TMEM full at two buffers
 //                  of 256 columns.  No unit is busy throughout (tensor pipe 66 %, shared memory's
 //                  data pipe 57 % while SMs are active).  Measured and not kept: CTA pairs (145 us,
 //                  the handovers cross SMs), weights as MMA rows at 256 tokens (182 us, a scale
 //                  per column from shared memory), two MMA warps (137 us).
-//   129 to 1024 rows against narrow outputs   tiles do not fill the SMs: 256 x 5120 x 5120 14.8 us
-//                  and 512 x 5120 x 5120 19.7 us (floors 4.4 and 7.0), 80 tiles on 152 SMs, unsplit.
+//   129 to 1024 rows against narrow outputs   tiles do not fill the SMs: 256 x 5120 x 5120 14.3
+//                  to 14.8 us, 512 x 5120 x 5120 18.8 to 19.7 us (floors 4.4 and 7.0): 80 tiles on
+//                  152 SMs, unsplit.
 #include <cooperative_groups.h>
 #include <cuda_bf16.h>
 
