@@ -10,6 +10,7 @@ does not need it: where it does not compile, ``build()`` warns, and the verify
 step's calls raise ImportError.
 """
 import concurrent.futures as cf
+import contextlib
 import glob
 import os
 import subprocess
@@ -74,14 +75,15 @@ def build_binding(force=False):
            f"-D_GLIBCXX_USE_CXX11_ABI={int(torch._C._GLIBCXX_USE_CXX11_ABI)}", src, "-o", tmp,
            "-L", os.path.join(home, "lib"), "-ltorch_python", "-ltorch_cuda", "-ltorch_cpu", "-lc10",
            "-lc10_cuda"]
-    if os.path.exists(target):
-        os.remove(target)
     try:
         r = subprocess.run(cmd, capture_output=True, text=True)
+        error = f"g++ failed on {src}:\n{r.stdout}\n{r.stderr}" if r.returncode != 0 else None
     except OSError as e:
-        raise RuntimeError(f"g++ did not run: {e}") from e
-    if r.returncode != 0:
-        raise RuntimeError(f"g++ failed on {src}:\n{r.stdout}\n{r.stderr}")
+        error = f"g++ did not run: {e}"
+    if error is not None:
+        with contextlib.suppress(FileNotFoundError):
+            os.remove(target)
+        raise RuntimeError(error)
     os.replace(tmp, target)
     return target
 
