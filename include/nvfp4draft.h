@@ -65,6 +65,7 @@ extern "C" {
 #define NVFP4_ERR_NONFINITE 7  /* device: Inf/NaN in the quantiser's input   */
 #define NVFP4_ERR_DTYPE 8      /* unknown output dtype                       */
 #define NVFP4_ERR_INDEX 9      /* device: a gather index out of range; row 0 */
+#define NVFP4_ERR_PAGES 10     /* device: kv_plan had no page for a sequence  */
 
 /* Output element types. */
 #define NVFP4_DTYPE_F32 0
@@ -484,6 +485,189 @@ typedef struct spec_verify_input {
  */
 int spec_verify(const spec_verify_input *in, int32_t *out_tokens, int64_t ld_out,
                 int32_t *accepted, const nvfp4_exec *ex);
+
+/*
+ * The attention step: positions, the paged KV cache and attention, between a
+ * layer's QKV projection and its output projection.
+ *
+ *   kv_plan           block tables, slot maps and positions of a batch's new
+ *                     tokens, from the requests' lengths
+ *   rope_kv_write     rotary positions (one axis or several) on q and k; k and v
+ *                     into the cache's pages
+ *   prompt_attention  causal attention over whole prompts, packed
+ *   paged_attention   attention of new tokens, one to many per sequence, over the
+ *                     paged cache
+ *
+ * BF16 tensors, FP32 arithmetic.  Launched with programmatic stream serialisation
+ * like the verify step's kernels: no global memory is touched before the previous
+ * kernel on the stream has completed.  Outputs must not overlap inputs, except
+ * where a call says so.
+ */
+
+/* Largest batch of kv_plan (its prefix sums are held in one SM's shared memory). */
+#define KV_PLAN_MAX_BATCH 8192
+/* Largest page of the cache, in tokens. */
+#define KV_MAX_PAGE 65536
+/* Largest head of rope_kv_write. */
+#define ROPE_MAX_DIM 512
+
+/* Rows of heads: element (token, head, i) at data[token * ld_token + head * ld_head + i];
+ * 16-byte aligned, strides multiples of 8 elements. */
+typedef struct attn_rows {
+    void *data;
+    int64_t ld_token, ld_head;
+} attn_rows;
+
+/* Pages of the cache: element (page, token, head, i) at
+ * data[page * ld_page + token * ld_token + head * ld_head + i]; 16-byte aligned,
+ * strides multiples of 8 elements. */
+typedef struct kv_pages {
+    void *data;
+    int64_t ld_page, ld_token, ld_head;
+} kv_pages;
+
+/* Input of kv_plan (device pointers, int32). */
+typedef struct kv_plan_input {
+    const int32_t *lens;        /* [batch] tokens in the cache                      */
+    const int32_t *num_new;     /* [batch] tokens that come; 0 or less: none        */
+    const int32_t *held;        /* [batch] pages held, or NULL: ceil(lens / page)   */
+    int32_t *block_table;       /* [batch, ld_table]: the pages held; the new ones
+                                   are written behind them                          */
+    int64_t ld_table, max_pages; /* entries of a row in use: 0 < max_pages <= ld    */
+    const int32_t *free_pages;  /* [free_capacity], a stack: its top is the last
+                                   of the first *free_count                         */
+    int64_t free_capacity;      /* >= 0                                             */
+    const int32_t *free_count;  /* [1]                                              */
+    int64_t batch;              /* 0..KV_PLAN_MAX_BATCH                             */
+    int64_t page_size;          /* 1..KV_MAX_PAGE                                   */
+    int64_t tokens;             /* rows of positions and slots, < 2^31              */
+} kv_plan_input;
+
+typedef struct kv_plan_output {
+    int32_t *cu_new;       /* [batch + 1] prefix sums of the new tokens              */
+    int32_t *kv_lens;      /* [batch] lengths with the new tokens; may be lens       */
+    int32_t *positions;    /* [tokens]                                               */
+    int32_t *slots;        /* [tokens] page * page_size + offset, or -1              */
+    int32_t *held;         /* [batch] pages held afterwards, or NULL; may be held    */
+    int32_t *free_count;   /* [1] pages left, or NULL; may be the input's            */
+} kv_plan_output;
+
+/*
+ * kv_plan -- per sequence s, in order, with n = max(num_new, 0), len = max(lens, 0):
+ *   need = ceil((len + n) / page_size) (0 where n = 0); extra = max(0, need - held)
+ *   pages from the stack's top become entries held, held + 1, ... of its table row;
+ *   kv_lens = len + n, held = max(held, need); new token j: row cu_new[s] + j of
+ *   positions (len + j) and slots (its page times page_size plus its offset).
+ * A sequence that cannot be served -- the pages of those before it and its own exceed
+ * the stack, need exceeds max_pages, or its tokens end past `tokens` -- takes none,
+ * keeps its length, and its tokens' slots are -1 (NVFP4_ERR_PAGES to dev_status); so
+ * do all later ones that need pages, once the stack is exceeded.  (A refused token whose
+ * position no int32 holds gets 2^31 - 1.)  Rows past the last
+ * new token get position 0 and slot -1 (a padded batch).  Pages kept from refused
+ * drafts (held above ceil(lens / page_size)) are used before new ones.
+ * lens, num_new, held, free_pages and free_count are only read, unless given as outputs:
+ * the same call on the same inputs writes the same.
+ * A free count outside [0, free_capacity] is clamped, a slot that no int32 holds or of a
+ * negative page is -1 (both: NVFP4_ERR_INDEX).  Workspace: none.
+ */
+int kv_plan(const kv_plan_input *in, const kv_plan_output *out, const nvfp4_exec *ex);
+
+/* Input of rope_kv_write. */
+typedef struct rope_kv_input {
+    attn_rows q, k, v;          /* [tokens, heads | kv_heads | kv_heads, dim]; v is
+                                   read only with a cache                           */
+    int64_t tokens;             /* >= 0, < 2^31                                     */
+    int64_t heads, kv_heads;    /* >= 1, < 2^20                                     */
+    int64_t dim;                /* multiple of 16, 16..ROPE_MAX_DIM                 */
+    int64_t rot_dim;            /* multiple of 16, 16..dim: the first elements are
+                                   rotated, the others kept                         */
+    const int32_t *positions;   /* [axes, ld_positions] (device)                    */
+    int64_t ld_positions;       /* >= tokens; 0: all axes share one row             */
+    int64_t axes;               /* >= 1                                             */
+    const uint64_t *turns;      /* [rot_dim / 2] (device): frequency / (2 pi) in
+                                   units of 2^-64 turns per position                */
+    const uint8_t *axis;        /* [rot_dim / 2] (device): the axis of each pair;
+                                   NULL: axis 0; values past axes count as 0        */
+    kv_pages k_cache, v_cache;  /* [pages, page_size, kv_heads, dim] or data NULL   */
+    int64_t pages, page_size;   /* pages * page_size <= 2^31 - 1                    */
+    const int32_t *slots;       /* [tokens] (device), with a cache                  */
+} rope_kv_input;
+
+typedef struct rope_kv_output {
+    attn_rows q;                /* rotated q; may be q itself                       */
+    attn_rows k;                /* rotated k, or data NULL; may be k itself         */
+} rope_kv_output;
+
+/*
+ * rope_kv_write -- pair i of a head is its elements i and rot_dim / 2 + i:
+ *   t = positions[axis[i]] * 2 pi turns[i] 2^-64;
+ *   (x, y) -> (x cos t - y sin t, x sin t + y cos t), FP32, rounded once to BF16.
+ * The fraction of a turn is exact however far the position; the sines are off by at
+ * most 4e-7.  Rotated k and v as they are go to the cache at each token's slot; a
+ * negative slot writes nothing, one past the cache neither (NVFP4_ERR_INDEX).  Two
+ * tokens of one slot: one of them.  Workspace: none.
+ */
+int rope_kv_write(const rope_kv_input *in, const rope_kv_output *out, const nvfp4_exec *ex);
+
+/* Most CTAs of an attention launch, and its workspace: per CTA two partial results of
+ * an item that several CTAs share (sums of up to 256 rows of 128, or 128 of 256, with
+ * their maxima and weights) and a record of the item. */
+#define ATTENTION_MAX_CTAS 160
+#define ATTENTION_WS_BYTES ((size_t)ATTENTION_MAX_CTAS * (2 * (256 * 128 + 512) * 4 + 64))
+
+/* Queries, keys and values of prompt_attention. */
+typedef struct prompt_attention_input {
+    attn_rows q, k, v;         /* [tokens, heads | kv_heads | kv_heads, dim]         */
+    const int32_t *cu;         /* [batch + 1] (device): sequence s is rows cu[s] ..
+                                  cu[s + 1] - 1                                       */
+    int64_t tokens, batch;     /* tokens >= 0, < 2^31 - 512; batch >= 0, < 2^20       */
+    int64_t heads, kv_heads;   /* heads a multiple of kv_heads, at most 128 times it  */
+    int64_t dim;               /* 64, 128 or 256                                      */
+    float scale;               /* of the scores, finite                               */
+} prompt_attention_input;
+
+/*
+ * prompt_attention -- per sequence, causal, query head h with key head h / (heads / kv_heads):
+ *   out[i] = sum_{j <= i} softmax_j(scale q_i . k_j) v_j
+ * on the BF16 tensor cores: products and sums in FP32; the weights relative to the running
+ * maximum are rounded to BF16 before they multiply v, their sum is not; one rounding of the
+ * result.  Rows that no sequence covers (past cu[batch]) are left as they were.  cu outside
+ * [0, tokens] is clamped, a sequence whose offsets descend is empty (both: NVFP4_ERR_INDEX).
+ *   out   [tokens, heads, dim] BF16.
+ * Values of tokens that a query does not see but that share a tile of 128 with ones that
+ * another query of its sequence sees must be finite.  Other sequences' may be anything.
+ * Sums are split over SMs by a rule on the lengths and joined in a fixed order: the same
+ * call gives the same bits.
+ * Workspace: ATTENTION_WS_BYTES, 16-byte aligned; nothing need be in it, nothing is kept
+ * there.  Waits inside the kernel are bounded; one that runs out writes NVFP4_ERR_TIMEOUT
+ * to dev_status and leaves the output incomplete.
+ */
+int prompt_attention(const prompt_attention_input *in, const attn_rows *out, const nvfp4_exec *ex);
+
+/* Queries and cache of paged_attention. */
+typedef struct paged_attention_input {
+    attn_rows q;               /* [tokens, heads, dim]                                */
+    kv_pages k, v;             /* [pages, page_size, kv_heads, dim]                   */
+    int64_t pages, page_size;  /* pages >= 1, < 2^31; page_size a multiple of 16,
+                                  16..KV_MAX_PAGE                                     */
+    const int32_t *block_table; /* [batch, ld_table] (device)                         */
+    int64_t ld_table, max_pages; /* entries of a row in use: 0 < max_pages <= ld      */
+    const int32_t *kv_lens;    /* [batch] (device): cached tokens, the new ones
+                                  included                                            */
+    const int32_t *cu;         /* [batch + 1] (device): the new tokens' rows of q     */
+    int64_t tokens, batch, heads, kv_heads, dim;  /* as in prompt_attention           */
+    float scale;
+} paged_attention_input;
+
+/*
+ * paged_attention -- query j of a sequence's n stands at position kv_len - n + j and sees
+ * the cached positions up to its own; arithmetic, rows that no sequence covers, splitting and
+ * workspace as prompt_attention.  A query before position 0, as where kv_len < n, sees
+ * nothing: zeros.  kv_len past max_pages * page_size is clamped, a page outside the cache
+ * counts as zeros (both: NVFP4_ERR_INDEX).  Table entries and slots behind kv_len are not
+ * used: they may hold anything.
+ */
+int paged_attention(const paged_attention_input *in, const attn_rows *out, const nvfp4_exec *ex);
 
 #ifdef __cplusplus
 }

@@ -20,6 +20,10 @@ The calls keep the C names:
 * :func:`fp8b_rmsnorm`       residual addition + RMSNorm -> FP8 rows, one scale per 128 columns
 * :func:`fp8b_gemm`          the product of the two, one row to thousands
 * :func:`spec_verify`        verification of drafted tokens against the target's probabilities
+* :func:`kv_plan`            block tables, slot maps and positions of a batch's new tokens
+* :func:`rope_kv_write`      rotary positions (one axis or several) and the write to the paged cache
+* :func:`prompt_attention`   causal attention over packed prompts, grouped heads
+* :func:`paged_attention`    attention of new tokens over the paged cache
 
 The C library checks what it can see (null pointers, sizes, leading
 dimensions, alignment); the extents, dtypes and devices of the tensors are
@@ -47,9 +51,19 @@ own head, then the accepted drafts and the next token)::
     logits = nd.fp8b_gemm(a, head8, out_dtype=torch.float32)   # [batch * (g + 1), vocab]
     p = torch.softmax(logits.view(batch, g + 1, -1), -1)
     tokens, accepted = nd.spec_verify(p, drafted, accept_u, sample_u, draft_probs=q)
+
+The attention step of a layer over the paged cache, between its projections (``plan`` once a
+step, the rest once a layer)::
+
+    rotary = nd.rotary_table(head_dim, theta=1e6, device="cuda")       # load time
+    plan = nd.kv_plan(lens, num_new, block_table, free_pages, free_count, page_size=16,
+                      tokens=x.shape[0])
+    q, _ = nd.rope_kv_write(q, k, v, plan.positions, rotary, k_cache, v_cache, plan.slots)
+    o = nd.paged_attention(q, k_cache, v_cache, block_table, plan.kv_lens, plan.cu_new)
 """
 import ctypes
 import importlib.util
+import math
 import os
 from dataclasses import dataclass
 from typing import Optional, Sequence
@@ -62,7 +76,8 @@ LIB_PATH = os.path.join(_PKG, "_build", "libnvfp4draft.so")
 NVFP4_OK = 0
 NVFP4_ERR_INDEX = 9
 STATUS_NAMES = {0: "OK", 1: "ERR_NULL", 2: "ERR_SHAPE", 3: "ERR_ALIGN", 4: "ERR_WORKSPACE",
-                5: "ERR_CUDA", 6: "ERR_TIMEOUT", 7: "ERR_NONFINITE", 8: "ERR_DTYPE", 9: "ERR_INDEX"}
+                5: "ERR_CUDA", 6: "ERR_TIMEOUT", 7: "ERR_NONFINITE", 8: "ERR_DTYPE", 9: "ERR_INDEX",
+                10: "ERR_PAGES"}
 DTYPE_F32 = 0
 DTYPE_BF16 = 1
 GEMV_MAX_M = 32
@@ -82,9 +97,14 @@ QUANTIZE_WS_BYTES = 16
 FP8B_BLOCK = 128
 FP8B_MAX_K = 32768
 SPEC_MAX_DRAFT = 1024
+KV_PLAN_MAX_BATCH = 8192
+ROPE_MAX_DIM = 512
+ATTENTION_MAX_CTAS = 160
+ATTENTION_WS_BYTES = ATTENTION_MAX_CTAS * (2 * (256 * 128 + 512) * 4 + 64)
 EXPORTED = ("nvfp4_quantize", "w4a16_gemv", "w4a16_gemv_argmax", "w4a16_gemv_argmax_ex",
             "w4a16_gemm", "fp8w_quantize", "fp8w_gemv", "fp8w_gemv_argmax", "fp8w_gemv_argmax_ex",
-            "fp8b_quantize", "fp8b_rmsnorm", "fp8b_gemm", "spec_verify")
+            "fp8b_quantize", "fp8b_rmsnorm", "fp8b_gemm", "spec_verify", "kv_plan", "rope_kv_write",
+            "prompt_attention", "paged_attention")
 
 
 class Nvfp4Error(RuntimeError):
@@ -172,6 +192,56 @@ class _VerifyInput(ctypes.Structure):
                 ("batch", ctypes.c_int64), ("g", ctypes.c_int64), ("vocab", ctypes.c_int64)]
 
 
+class _Rows(ctypes.Structure):
+    _fields_ = [("data", ctypes.c_void_p), ("ld_token", ctypes.c_int64), ("ld_head", ctypes.c_int64)]
+
+
+class _Pages(ctypes.Structure):
+    _fields_ = [("data", ctypes.c_void_p), ("ld_page", ctypes.c_int64), ("ld_token", ctypes.c_int64),
+                ("ld_head", ctypes.c_int64)]
+
+
+class _PlanInput(ctypes.Structure):
+    _fields_ = [("lens", ctypes.c_void_p), ("num_new", ctypes.c_void_p), ("held", ctypes.c_void_p),
+                ("block_table", ctypes.c_void_p), ("ld_table", ctypes.c_int64),
+                ("max_pages", ctypes.c_int64), ("free_pages", ctypes.c_void_p),
+                ("free_capacity", ctypes.c_int64), ("free_count", ctypes.c_void_p),
+                ("batch", ctypes.c_int64), ("page_size", ctypes.c_int64), ("tokens", ctypes.c_int64)]
+
+
+class _PlanOutput(ctypes.Structure):
+    _fields_ = [(n, ctypes.c_void_p) for n in ("cu_new", "kv_lens", "positions", "slots", "held",
+                                               "free_count")]
+
+
+class _RopeInput(ctypes.Structure):
+    _fields_ = [("q", _Rows), ("k", _Rows), ("v", _Rows), ("tokens", ctypes.c_int64),
+                ("heads", ctypes.c_int64), ("kv_heads", ctypes.c_int64), ("dim", ctypes.c_int64),
+                ("rot_dim", ctypes.c_int64), ("positions", ctypes.c_void_p),
+                ("ld_positions", ctypes.c_int64), ("axes", ctypes.c_int64), ("turns", ctypes.c_void_p),
+                ("axis", ctypes.c_void_p), ("k_cache", _Pages), ("v_cache", _Pages),
+                ("pages", ctypes.c_int64), ("page_size", ctypes.c_int64), ("slots", ctypes.c_void_p)]
+
+
+class _RopeOutput(ctypes.Structure):
+    _fields_ = [("q", _Rows), ("k", _Rows)]
+
+
+class _PromptInput(ctypes.Structure):
+    _fields_ = [("q", _Rows), ("k", _Rows), ("v", _Rows), ("cu", ctypes.c_void_p),
+                ("tokens", ctypes.c_int64), ("batch", ctypes.c_int64), ("heads", ctypes.c_int64),
+                ("kv_heads", ctypes.c_int64), ("dim", ctypes.c_int64), ("scale", ctypes.c_float)]
+
+
+class _PagedInput(ctypes.Structure):
+    _fields_ = [("q", _Rows), ("k", _Pages), ("v", _Pages), ("pages", ctypes.c_int64),
+                ("page_size", ctypes.c_int64), ("block_table", ctypes.c_void_p),
+                ("ld_table", ctypes.c_int64), ("max_pages", ctypes.c_int64),
+                ("kv_lens", ctypes.c_void_p), ("cu", ctypes.c_void_p), ("tokens", ctypes.c_int64),
+                ("batch", ctypes.c_int64), ("heads", ctypes.c_int64), ("kv_heads", ctypes.c_int64),
+                ("dim", ctypes.c_int64), ("scale", ctypes.c_float)]
+
+
 class _Exec(ctypes.Structure):
     _fields_ = [("stream", ctypes.c_void_p), ("workspace", ctypes.c_void_p),
                 ("workspace_bytes", ctypes.c_size_t), ("dev_status", ctypes.c_void_p)]
@@ -210,6 +280,10 @@ def load(path: str = LIB_PATH):
     L.fp8b_rmsnorm.argtypes = [P(_NormInput), P(_Fp8BlockActs), P(_Exec)]
     L.fp8b_gemm.argtypes = [P(_Fp8BlockActs), P(_Fp8BlockWeight), vp, i32, i64, P(_Exec)]
     L.spec_verify.argtypes = [P(_VerifyInput), vp, i64, vp, P(_Exec)]
+    L.kv_plan.argtypes = [P(_PlanInput), P(_PlanOutput), P(_Exec)]
+    L.rope_kv_write.argtypes = [P(_RopeInput), P(_RopeOutput), P(_Exec)]
+    L.prompt_attention.argtypes = [P(_PromptInput), P(_Rows), P(_Exec)]
+    L.paged_attention.argtypes = [P(_PagedInput), P(_Rows), P(_Exec)]
     for f in EXPORTED + ("w4a16_gemv_argmax_noalloc",):
         getattr(L, f).restype = ctypes.c_int
     _LIB = L
@@ -627,7 +701,8 @@ def _native():
     if _NATIVE is None:
         L, native = load(), _load_binding()
         native.bind(*(ctypes.cast(getattr(L, f), ctypes.c_void_p).value
-                      for f in ("fp8b_quantize", "fp8b_rmsnorm", "fp8b_gemm", "spec_verify")), Nvfp4Error)
+                      for f in ("fp8b_quantize", "fp8b_rmsnorm", "fp8b_gemm", "spec_verify", "kv_plan",
+                                "rope_kv_write", "prompt_attention", "paged_attention")), Nvfp4Error)
         _NATIVE = native
     return _NATIVE
 
@@ -707,3 +782,132 @@ def spec_verify(target_probs: torch.Tensor, draft_tokens: torch.Tensor, accept_u
     is absent and its outputs are left as they were)."""
     return _native().verify(target_probs, draft_tokens, accept_u, sample_u, draft_probs, num_draft,
                             out_tokens, out_accepted, _raw(stream), dev_status)
+
+
+# ------------------------------------------------- the attention step (paged KV cache)
+#
+# Marshalled by the native module like the verify step's calls, outputs (and attention's
+# workspace) on the call's stream.
+
+@dataclass
+class RotaryTable:
+    """Frequencies of rotary positions: one entry per pair of a head's elements."""
+    turns: torch.Tensor  # int64 [pairs]: frequency / (2 pi) in units of 2^-64, modulo 2^64
+    axis: torch.Tensor   # uint8 [pairs]: the position axis of each pair
+    axes: int
+
+
+@dataclass
+class KvPlan:
+    """Where a batch's new tokens go (device tensors, int32)."""
+    cu_new: torch.Tensor      # [batch + 1] prefix sums of the new tokens
+    kv_lens: torch.Tensor     # [batch] lengths with the new tokens
+    positions: torch.Tensor   # [tokens]
+    slots: torch.Tensor       # [tokens] page * page_size + offset, or -1
+    held: torch.Tensor        # [batch] pages held afterwards
+    free_count: torch.Tensor  # [1] pages left on the free stack
+
+
+def rotary_table(rot_dim: int, theta: float = 10000.0, sections: Optional[Sequence[int]] = None,
+                 interleaved: bool = False, inv_freq: Optional[Sequence[float]] = None,
+                 device="cuda") -> RotaryTable:
+    """Frequencies theta^(-2 i / rot_dim) radians per position (or ``inv_freq``, rot_dim / 2 of
+    them) for the pairs i of a head's first ``rot_dim`` elements.
+
+    ``sections``: pairs of each position axis (time, height, width, ...), rot_dim / 2 in all;
+    default one axis.  They lie one after the other, or ``interleaved``: pair i belongs to axis
+    i modulo the number of axes while that axis has pairs left, else to axis 0."""
+    pairs = rot_dim // 2
+    _need(rot_dim >= 16 and rot_dim % 16 == 0, "rot_dim must be a multiple of 16")
+    sections = [pairs] if sections is None else [int(n) for n in sections]
+    axes = len(sections)
+    _need(1 <= axes <= 256 and min(sections) >= 0 and sum(sections) == pairs,
+          f"sections must add up to {pairs} pairs")
+    if inv_freq is None:
+        _need(theta > 0, "theta must be positive")
+        inv_freq = [float(theta) ** (-2.0 * i / rot_dim) for i in range(pairs)]
+    else:
+        inv_freq = [float(f) for f in inv_freq]
+        _need(len(inv_freq) == pairs and all(math.isfinite(f) for f in inv_freq),
+              f"inv_freq must be {pairs} finite numbers")
+    if interleaved:
+        left, axis = list(sections), []
+        for i in range(pairs):
+            a = i % axes if left[i % axes] > 0 else 0
+            left[a] -= 1
+            axis.append(a)
+        _need(min(left) == 0 == max(left), "sections cannot be interleaved")
+    else:
+        axis = [a for a, n in enumerate(sections) for _ in range(n)]
+    # the fraction is kept exactly: Python's integers, then two's complement
+    turns = [int(math.ldexp(f / (2.0 * math.pi), 64)) % (1 << 64) for f in inv_freq]
+    turns = [t - (1 << 64) if t >= 1 << 63 else t for t in turns]
+    return RotaryTable(torch.tensor(turns, dtype=torch.int64, device=device),
+                       torch.tensor(axis, dtype=torch.uint8, device=device), axes)
+
+
+def kv_plan(lens: torch.Tensor, num_new: torch.Tensor, block_table: torch.Tensor,
+            free_pages: torch.Tensor, free_count: torch.Tensor, page_size: int, tokens: int,
+            held: Optional[torch.Tensor] = None, out: Optional[KvPlan] = None, stream=None,
+            dev_status: Optional[torch.Tensor] = None) -> KvPlan:
+    """Pages, slots and positions of the ``num_new`` tokens that come behind each sequence's
+    ``lens`` cached ones (int32 [batch] on the GPU; 0 or less: none).
+
+    New pages come off the top of the stack ``free_pages[:free_count]`` and are written to
+    ``block_table`` [batch, max_pages] behind the ``held`` ones (default ceil(lens /
+    page_size)).  ``tokens`` rows of positions and slots are written; those past the last new
+    token, and those of a sequence without a page (NVFP4_ERR_PAGES to dev_status), get slot -1.
+
+    Nothing but the table's new entries is changed, unless ``out`` holds the inputs: its
+    ``kv_lens``, ``held`` and ``free_count`` may be lens, held and free_count."""
+    o = (None,) * 6 if out is None else (out.cu_new, out.kv_lens, out.positions, out.slots, out.held,
+                                         out.free_count)
+    r = _native().plan(lens, num_new, block_table, free_pages, free_count, page_size, tokens, held, *o,
+                       _raw(stream), dev_status)
+    return KvPlan(*r) if out is None else out
+
+
+def rope_kv_write(q: torch.Tensor, k: torch.Tensor, v: Optional[torch.Tensor], positions: torch.Tensor,
+                  rotary: RotaryTable, k_cache: Optional[torch.Tensor] = None,
+                  v_cache: Optional[torch.Tensor] = None, slots: Optional[torch.Tensor] = None,
+                  q_out: Optional[torch.Tensor] = None, k_out: Optional[torch.Tensor] = None,
+                  stream=None, dev_status: Optional[torch.Tensor] = None):
+    """Rotary positions on q [tokens, heads, dim] and k [tokens, kv_heads, dim] (BF16, any
+    strides along tokens and heads), the rotated k and v to ``slots`` (int32 [tokens], negative:
+    nowhere) of the caches [pages, page_size, kv_heads, dim].
+
+    positions int32 [tokens], or [axes, tokens] with a row for each of the table's axes.
+    Returns (q, k): new tensors, or ``q_out`` / ``k_out``, which may be q and k themselves; with
+    a cache k is None unless ``k_out`` is given.  Without one v is not used."""
+    return _native().rope(q, k, v, positions, rotary.turns, rotary.axis, rotary.axes, k_cache, v_cache, slots,
+                          q_out, k_out, _raw(stream), dev_status)
+
+
+def prompt_attention(q: torch.Tensor, k: torch.Tensor, v: torch.Tensor, cu_seqlens: torch.Tensor,
+                     scale: Optional[float] = None, out: Optional[torch.Tensor] = None,
+                     workspace: Optional[torch.Tensor] = None, stream=None,
+                     dev_status: Optional[torch.Tensor] = None) -> torch.Tensor:
+    """Causal attention of packed prompts: sequence s is rows cu_seqlens[s] .. cu_seqlens[s + 1]
+    of q [tokens, heads, dim], k and v [tokens, kv_heads, dim] (BF16; dim 64, 128 or 256), and
+    query head h reads key head h // (heads // kv_heads).  ``scale`` defaults to dim ** -0.5.
+    Rows that no sequence covers are left as they were in ``out``.
+
+    ``workspace``: ATTENTION_WS_BYTES bytes, needed during the call only; by default the
+    allocator's, on the call's stream."""
+    return _native().prompt(q, k, v, cu_seqlens, scale, out, workspace, _raw(stream), dev_status)
+
+
+def paged_attention(q: torch.Tensor, k_cache: torch.Tensor, v_cache: torch.Tensor,
+                    block_table: torch.Tensor, kv_lens: torch.Tensor, cu_new: torch.Tensor,
+                    scale: Optional[float] = None, out: Optional[torch.Tensor] = None,
+                    workspace: Optional[torch.Tensor] = None, stream=None,
+                    dev_status: Optional[torch.Tensor] = None) -> torch.Tensor:
+    """Attention of each sequence's new tokens, rows cu_new[s] .. cu_new[s + 1] of q [tokens,
+    heads, dim], over its ``kv_lens[s]`` cached tokens, the new ones included: query j of n
+    stands at position kv_lens[s] - n + j and sees the positions up to its own.
+
+    k_cache, v_cache [pages, page_size, kv_heads, dim] (BF16, any strides but the last; page
+    size a multiple of 16); block_table int32 [batch, max_pages].  Other arguments as in
+    :func:`prompt_attention`."""
+    return _native().paged(q, k_cache, v_cache, block_table, kv_lens, cu_new, scale, out, workspace,
+                           _raw(stream), dev_status)

@@ -174,6 +174,38 @@ int gemv_argmax_ex(const w4a16_act_segment* seg, int nseg, int m, const WeightRe
                      ld_mask);
 }
 
+bool rows_aligned(const attn_rows& r) {
+  return aligned16(r.data) && r.ld_token % 8 == 0 && r.ld_head % 8 == 0;
+}
+bool pages_aligned(const kv_pages& r) {
+  return aligned16(r.data) && r.ld_page % 8 == 0 && r.ld_token % 8 == 0 && r.ld_head % 8 == 0;
+}
+// A stride in the range of a TMA descriptor (2^40 bytes).
+bool strides_fit(int64_t a, int64_t b, int64_t c) {
+  const int64_t most = (int64_t)1 << 39;
+  return a >= 0 && a < most && b >= 0 && b < most && c >= 0 && c < most;
+}
+
+// Argument checks that the two attention calls share.
+int attention(const paged_attention_input& in, const attn_rows* out, const nvfp4_exec* ex) {
+  if (out == nullptr) return NVFP4_ERR_NULL;
+  if (in.tokens < 0 || in.tokens >= 0x7FFFFFFF - 512 || in.batch < 0 || in.batch >= 1 << 20 || in.kv_heads < 1 ||
+      in.heads < 1 || in.heads % in.kv_heads != 0 || in.heads / in.kv_heads > 128 || in.heads >= 1 << 20 ||
+      (in.dim != 64 && in.dim != 128 && in.dim != 256) || !(in.scale - in.scale == 0.0f))
+    return NVFP4_ERR_SHAPE;
+  if (in.tokens == 0 || in.batch == 0) return NVFP4_OK;
+  if (in.q.data == nullptr || in.k.data == nullptr || in.v.data == nullptr || in.cu == nullptr || out->data == nullptr)
+    return NVFP4_ERR_NULL;
+  if (!strides_fit(in.q.ld_token, in.q.ld_head, 0) || !strides_fit(in.k.ld_page, in.k.ld_token, in.k.ld_head) ||
+      !strides_fit(in.v.ld_page, in.v.ld_token, in.v.ld_head))
+    return NVFP4_ERR_SHAPE;
+  if (!rows_aligned(in.q) || !pages_aligned(in.k) || !pages_aligned(in.v) || !rows_aligned(*out) || !aligned4(in.cu))
+    return NVFP4_ERR_ALIGN;
+  if (ex == nullptr || ex->workspace == nullptr || ex->workspace_bytes < ATTENTION_WS_BYTES || !aligned16(ex->workspace))
+    return NVFP4_ERR_WORKSPACE;
+  return launch_attention(&in, out, ex->workspace, status_of(ex), stream_of(ex));
+}
+
 }  // namespace
 
 extern "C" {
@@ -371,6 +403,81 @@ int spec_verify(const spec_verify_input* in, int32_t* out_tokens, int64_t ld_out
       !aligned4(out_tokens) || !aligned4(accepted))
     return NVFP4_ERR_ALIGN;
   return launch_spec_verify(in, out_tokens, ld_out, accepted, status_of(ex), stream_of(ex));
+}
+
+int kv_plan(const kv_plan_input* in, const kv_plan_output* out, const nvfp4_exec* ex) {
+  if (in == nullptr || out == nullptr || in->free_count == nullptr || out->cu_new == nullptr)
+    return NVFP4_ERR_NULL;
+  if (in->batch < 0 || in->batch > KV_PLAN_MAX_BATCH || in->page_size < 1 || in->page_size > KV_MAX_PAGE ||
+      in->tokens < 0 || in->tokens > 0x7FFFFFFF || in->free_capacity < 0 || in->free_capacity > 0x7FFFFFFF)
+    return NVFP4_ERR_SHAPE;
+  if ((in->batch > 0 && (in->lens == nullptr || in->num_new == nullptr || in->block_table == nullptr ||
+                         out->kv_lens == nullptr)) ||
+      (in->free_capacity > 0 && in->free_pages == nullptr) ||
+      (in->tokens > 0 && (out->positions == nullptr || out->slots == nullptr)))
+    return NVFP4_ERR_NULL;
+  if (in->batch > 0 && (in->max_pages < 1 || in->max_pages > in->ld_table || in->max_pages > 0x7FFFFFFF))
+    return NVFP4_ERR_SHAPE;
+  if (!aligned4(in->lens) || !aligned4(in->num_new) || !aligned4(in->held) || !aligned4(in->block_table) ||
+      !aligned4(in->free_pages) || !aligned4(in->free_count) || !aligned4(out->cu_new) || !aligned4(out->kv_lens) ||
+      !aligned4(out->positions) || !aligned4(out->slots) || !aligned4(out->held) || !aligned4(out->free_count))
+    return NVFP4_ERR_ALIGN;
+  return launch_kv_plan(in, out, status_of(ex), stream_of(ex));
+}
+
+int rope_kv_write(const rope_kv_input* in, const rope_kv_output* out, const nvfp4_exec* ex) {
+  if (in == nullptr || out == nullptr) return NVFP4_ERR_NULL;
+  if (in->tokens < 0 || in->tokens > 0x7FFFFFFF || in->heads < 1 || in->heads >= 1 << 20 || in->kv_heads < 1 ||
+      in->kv_heads >= 1 << 20 || in->dim < 16 || in->dim % 16 != 0 || in->dim > ROPE_MAX_DIM || in->rot_dim < 16 ||
+      in->rot_dim % 16 != 0 || in->rot_dim > in->dim || in->axes < 1 || in->axes > 256 ||
+      (in->ld_positions < in->tokens && in->ld_positions != 0))
+    return NVFP4_ERR_SHAPE;
+  const bool cached = in->k_cache.data != nullptr;
+  if (cached != (in->v_cache.data != nullptr)) return NVFP4_ERR_NULL;
+  if (cached && (in->pages < 1 || in->page_size < 1 || in->page_size > KV_MAX_PAGE ||
+                 in->pages > 0x7FFFFFFF / in->page_size))
+    return NVFP4_ERR_SHAPE;
+  if (in->tokens == 0) return NVFP4_OK;
+  if (in->q.data == nullptr || in->k.data == nullptr || in->positions == nullptr || in->turns == nullptr ||
+      out->q.data == nullptr || (cached && (in->v.data == nullptr || in->slots == nullptr)))
+    return NVFP4_ERR_NULL;
+  if (!rows_aligned(in->q) || !rows_aligned(in->k) || (cached && !rows_aligned(in->v)) || !rows_aligned(out->q) ||
+      (out->k.data != nullptr && !rows_aligned(out->k)) || !pages_aligned(in->k_cache) ||
+      !pages_aligned(in->v_cache) || !aligned4(in->positions) || !aligned4(in->slots) ||
+      (reinterpret_cast<uintptr_t>(in->turns) & 7u))
+    return NVFP4_ERR_ALIGN;
+  return launch_rope_kv_write(in, out, status_of(ex), stream_of(ex));
+}
+
+int prompt_attention(const prompt_attention_input* in, const attn_rows* out, const nvfp4_exec* ex) {
+  if (in == nullptr) return NVFP4_ERR_NULL;
+  paged_attention_input a = {};
+  a.q = in->q;
+  a.k = kv_pages{in->k.data, 0, in->k.ld_token, in->k.ld_head};
+  a.v = kv_pages{in->v.data, 0, in->v.ld_token, in->v.ld_head};
+  a.pages = 1;
+  a.page_size = in->tokens;
+  a.cu = in->cu;
+  a.tokens = in->tokens;
+  a.batch = in->batch;
+  a.heads = in->heads;
+  a.kv_heads = in->kv_heads;
+  a.dim = in->dim;
+  a.scale = in->scale;
+  return attention(a, out, ex);
+}
+
+int paged_attention(const paged_attention_input* in, const attn_rows* out, const nvfp4_exec* ex) {
+  if (in == nullptr) return NVFP4_ERR_NULL;
+  if (in->pages < 1 || in->pages > 0x7FFFFFFF || in->page_size < 16 || in->page_size % 16 != 0 ||
+      in->page_size > KV_MAX_PAGE)
+    return NVFP4_ERR_SHAPE;
+  if (in->batch > 0 && (in->max_pages < 1 || in->max_pages > in->ld_table || in->max_pages > 0x7FFFFFFF))
+    return NVFP4_ERR_SHAPE;
+  if (in->batch > 0 && in->tokens > 0 && (in->block_table == nullptr || in->kv_lens == nullptr))
+    return NVFP4_ERR_NULL;
+  if (!aligned4(in->block_table) || !aligned4(in->kv_lens)) return NVFP4_ERR_ALIGN;
+  return attention(*in, out, ex);
 }
 
 }  // extern "C"

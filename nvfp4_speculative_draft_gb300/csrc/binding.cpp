@@ -1,4 +1,4 @@
-// binding.cpp -- native argument marshalling of the verify step's calls.
+// binding.cpp -- native argument marshalling of the verify step's and the attention step's calls.
 //
 // A single token's kernels take two to ten microseconds, less than a Python function
 // needs to check a call's tensors, allocate its outputs and fill the C structs.  This
@@ -18,11 +18,13 @@
 #include <torch/csrc/Exceptions.h>
 #include <torch/csrc/autograd/python_variable.h>
 
+#include <cmath>
 #include <cstdint>
 #include <optional>
 #include <sstream>
 #include <stdexcept>
 #include <string>
+#include <utility>
 
 #include "nvfp4draft.h"
 
@@ -37,6 +39,10 @@ struct Library {
   decltype(&::fp8b_rmsnorm) rmsnorm = nullptr;
   decltype(&::fp8b_gemm) gemm = nullptr;
   decltype(&::spec_verify) verify = nullptr;
+  decltype(&::kv_plan) plan = nullptr;
+  decltype(&::rope_kv_write) rope = nullptr;
+  decltype(&::prompt_attention) prompt = nullptr;
+  decltype(&::paged_attention) paged = nullptr;
   PyObject* error = nullptr;
 } lib;
 
@@ -61,6 +67,8 @@ const char* dtype_text(at::ScalarType t) {
     case at::kBFloat16: return "torch.bfloat16";
     case at::kFloat: return "torch.float32";
     case at::kInt: return "torch.int32";
+    case at::kLong: return "torch.int64";
+    case at::kByte: return "torch.uint8";
     case at::kFloat8_e4m3fn: return "torch.float8_e4m3fn (or torch.uint8)";
     default: return "another type";
   }
@@ -387,14 +395,284 @@ PyObject* verify(PyObject*, PyObject* const* a, Py_ssize_t nargs) {
   CALL_END
 }
 
-// bind(quantize, rmsnorm, gemm, verify, error): the library's functions by address
+// ------------------------------------------------------------ attention step
+
+// [tokens, heads, dim] BF16 rows with unit stride along dim.
+const Tensor& need_heads(PyObject* o, const char* name, at::Device dev, int64_t tokens, int64_t heads, int64_t dim) {
+  const Tensor* t = tensor_of(o);
+  if (!is(t, at::kBFloat16, dev, {tokens, heads, dim}) || (t->stride(2) != 1 && dim != 1))
+    refuse(name, t, at::kBFloat16, {tokens, heads, dim}, " with unit stride along the last axis");
+  return *t;
+}
+// The first tensor of a call, which gives its sizes.
+const Tensor& first_heads(PyObject* o, const char* name) {
+  const Tensor& t = *tensor_of(o);
+  if (t.scalar_type() != at::kBFloat16 || t.dim() != 3 || (t.stride(2) != 1 && t.size(2) != 1))
+    refuse(name, &t, at::kBFloat16, {-1, -1, -1}, " with unit stride along the last axis");
+  return t;
+}
+// Strides for the library: those of an extent of 1 are arbitrary in torch.
+attn_rows rows_of(const Tensor& t) {
+  attn_rows r{t.data_ptr(), t.stride(0), t.stride(1)};
+  if (t.size(1) <= 1) r.ld_head = (t.size(2) + 7) / 8 * 8;
+  if (t.size(0) <= 1) r.ld_token = t.size(1) <= 1 ? r.ld_head : t.size(1) * r.ld_head;
+  return r;
+}
+// What is written to: no element twice.
+void need_distinct(const Tensor& t, const char* name) {
+  int64_t order[4], n = 0;
+  for (int64_t i = 0; i < t.dim(); ++i)
+    if (t.size(i) != 1) order[n++] = i;
+  for (int64_t i = 1; i < n; ++i)
+    for (int64_t j = i; j > 0 && t.stride(order[j]) < t.stride(order[j - 1]); --j) std::swap(order[j], order[j - 1]);
+  int64_t reach = 1;  // elements up to the last of the axes so far
+  for (int64_t i = 0; i < n; ++i) {
+    if (t.stride(order[i]) < reach) throw Refusal(std::string(name) + " must not overlap itself");
+    reach += (t.size(order[i]) - 1) * t.stride(order[i]);
+  }
+}
+const Tensor& need_pages(PyObject* o, const char* name, at::Device dev, at::IntArrayRef shape) {
+  const Tensor* t = tensor_of(o);
+  const bool any = shape.empty();  // the first of the two
+  if (t == nullptr || t->scalar_type() != at::kBFloat16 || t->device() != dev || t->dim() != 4 ||
+      (!any && t->sizes() != shape) || (t->stride(3) != 1 && t->size(3) != 1))
+    refuse(name, t, at::kBFloat16, any ? at::IntArrayRef({-1, -1, -1, -1}) : shape,
+           " [pages, page size, heads, dim] with unit stride along the last axis");
+  return *t;
+}
+kv_pages pages_of(const Tensor& t) {
+  kv_pages r{t.data_ptr(), t.stride(0), t.stride(1), t.stride(2)};
+  if (t.size(2) <= 1) r.ld_head = (t.size(3) + 7) / 8 * 8;
+  if (t.size(1) <= 1) r.ld_token = t.size(2) <= 1 ? r.ld_head : t.size(2) * r.ld_head;
+  if (t.size(0) <= 1) r.ld_page = t.size(1) <= 1 ? r.ld_token : t.size(1) * r.ld_token;
+  return r;
+}
+int64_t number(PyObject* o) {
+  const int64_t x = PyLong_AsLongLong(o);
+  if (x == -1 && PyErr_Occurred()) throw python_error();
+  return x;
+}
+// An int32 vector, given or made.
+Tensor vector_or_new(PyObject* o, const char* name, at::Device dev, int64_t n) {
+  return o != Py_None ? need_vector(o, name, at::kInt, dev, n) : make({n}, at::kInt, dev);
+}
+
+// plan(lens, num_new, block_table, free_pages, free_count, page_size, tokens, held | None,
+//      cu_new | None, kv_lens | None, positions | None, slots | None, held_out | None,
+//      free_count_out | None, stream, dev_status) -> six tensors
+PyObject* plan(PyObject*, PyObject* const* a, Py_ssize_t nargs) {
+  CALL_BEGIN(16)
+  const at::Device dev = device_of(a[0], "lens");
+  const Tensor& lens = *tensor_of(a[0]);
+  if (lens.dim() != 1) refuse("lens", &lens, at::kInt, {-1}, "");
+  kv_plan_input in{};
+  in.batch = lens.size(0);
+  in.lens = need_vector(a[0], "lens", at::kInt, dev, in.batch).data_ptr<int32_t>();
+  in.num_new = need_vector(a[1], "num_new", at::kInt, dev, in.batch).data_ptr<int32_t>();
+  const Tensor* table = tensor_of(a[2]);
+  if (table == nullptr || table->dim() != 2) refuse("block_table", table, at::kInt, {in.batch, -1}, kRowsText);
+  need_rows(a[2], "block_table", at::kInt, dev, {in.batch, table->size(1)});
+  in.block_table = table->data_ptr<int32_t>();
+  in.max_pages = table->size(1);
+  in.ld_table = in.batch > 1 ? table->stride(0) : in.max_pages;
+  const Tensor* free = tensor_of(a[3]);
+  if (free == nullptr || free->dim() != 1) refuse("free_pages", free, at::kInt, {-1}, " contiguous");
+  in.free_capacity = free->size(0);
+  in.free_pages = need_vector(a[3], "free_pages", at::kInt, dev, in.free_capacity).data_ptr<int32_t>();
+  in.free_count = need_vector(a[4], "free_count", at::kInt, dev, 1).data_ptr<int32_t>();
+  in.page_size = number(a[5]);
+  in.tokens = number(a[6]);
+  if (in.tokens < 0 || in.tokens > 0x7FFFFFFF) throw Refusal("tokens must be in 0 .. 2^31 - 1");
+  if (a[7] != Py_None) in.held = need_vector(a[7], "held", at::kInt, dev, in.batch).data_ptr<int32_t>();
+  const Call call(dev, a[14], a[15]);
+  const Tensor cu = vector_or_new(a[8], "cu_new", dev, in.batch + 1);
+  const Tensor kv = vector_or_new(a[9], "kv_lens", dev, in.batch);
+  const Tensor positions = vector_or_new(a[10], "positions", dev, in.tokens);
+  const Tensor slots = vector_or_new(a[11], "slots", dev, in.tokens);
+  const Tensor held = vector_or_new(a[12], "held_out", dev, in.batch);
+  const Tensor count = vector_or_new(a[13], "free_count_out", dev, 1);
+  const kv_plan_output out{cu.data_ptr<int32_t>(),    kv.data_ptr<int32_t>(),   positions.data_ptr<int32_t>(),
+                           slots.data_ptr<int32_t>(), held.data_ptr<int32_t>(), count.data_ptr<int32_t>()};
+  const int rc = lib.plan(&in, &out, &call.ex);
+  if (rc != NVFP4_OK) return fail("kv_plan", rc);
+  return Py_BuildValue("(NNNNNN)", wrap(cu), wrap(kv), wrap(positions), wrap(slots), wrap(held), wrap(count));
+  CALL_END
+}
+
+// rope(q, k, v | None, positions, turns, axis, axes, k_cache | None, v_cache | None, slots | None,
+//      q_out | None, k_out | None, stream, dev_status) -> (q, k | None)
+PyObject* rope(PyObject*, PyObject* const* a, Py_ssize_t nargs) {
+  CALL_BEGIN(14)
+  const at::Device dev = device_of(a[0], "q");
+  const Tensor& q = first_heads(a[0], "q");
+  rope_kv_input in{};
+  rope_kv_output out{};
+  in.tokens = q.size(0);
+  in.heads = q.size(1);
+  in.dim = q.size(2);
+  const Tensor* kt = tensor_of(a[1]);
+  in.kv_heads = kt != nullptr && kt->dim() == 3 ? kt->size(1) : 1;
+  const Tensor& k = need_heads(a[1], "k", dev, in.tokens, in.kv_heads, in.dim);
+  in.q = rows_of(q);
+  in.k = rows_of(k);
+  in.axes = number(a[6]);
+  const Tensor* pos = tensor_of(a[3]);
+  if (pos != nullptr && pos->dim() == 2) {
+    need_rows(a[3], "positions", at::kInt, dev, {in.axes, in.tokens});
+    in.ld_positions = in.axes > 1 ? pos->stride(0) : in.tokens;
+  } else {  // one row for all axes
+    need_vector(a[3], "positions", at::kInt, dev, in.tokens);
+  }
+  in.positions = pos->data_ptr<int32_t>();
+  const Tensor* turns = tensor_of(a[4]);
+  if (turns == nullptr || turns->dim() != 1) refuse("rotary.turns", turns, at::kLong, {-1}, " contiguous");
+  const int64_t pairs = turns->size(0);
+  in.rot_dim = 2 * pairs;
+  if (in.rot_dim > in.dim) throw Refusal("the rotary table has more pairs than a head");
+  in.turns = reinterpret_cast<const uint64_t*>(need_vector(a[4], "rotary.turns", at::kLong, dev, pairs).data_ptr());
+  in.axis = need_vector(a[5], "rotary.axis", at::kByte, dev, pairs).data_ptr<uint8_t>();
+  const bool cached = a[7] != Py_None;
+  if (cached != (a[8] != Py_None) || cached != (a[9] != Py_None))
+    throw Refusal("k_cache, v_cache and slots go together");
+  if (cached) {
+    const Tensor& kc = need_pages(a[7], "k_cache", dev, {});
+    if (kc.size(2) != in.kv_heads || kc.size(3) != in.dim) throw Refusal("k_cache must have the heads of k");
+    const Tensor& vc = need_pages(a[8], "v_cache", dev, kc.sizes());
+    need_distinct(kc, "k_cache");
+    need_distinct(vc, "v_cache");
+    in.k_cache = pages_of(kc);
+    in.v_cache = pages_of(vc);
+    in.pages = kc.size(0);
+    in.page_size = kc.size(1);
+    in.v = rows_of(need_heads(a[2], "v", dev, in.tokens, in.kv_heads, in.dim));
+    in.slots = need_vector(a[9], "slots", at::kInt, dev, in.tokens).data_ptr<int32_t>();
+  }
+  const Call call(dev, a[12], a[13]);
+  const Tensor qo = a[10] != Py_None ? need_heads(a[10], "q_out", dev, in.tokens, in.heads, in.dim)
+                                     : make({in.tokens, in.heads, in.dim}, at::kBFloat16, dev);
+  need_distinct(qo, "q_out");
+  out.q = rows_of(qo);
+  Tensor ko;
+  if (a[11] != Py_None) {
+    ko = need_heads(a[11], "k_out", dev, in.tokens, in.kv_heads, in.dim);
+    need_distinct(ko, "k_out");
+  } else if (!cached) {
+    ko = make({in.tokens, in.kv_heads, in.dim}, at::kBFloat16, dev);
+  }
+  if (ko.defined()) out.k = rows_of(ko);
+  const int rc = lib.rope(&in, &out, &call.ex);
+  if (rc != NVFP4_OK) return fail("rope_kv_write", rc);
+  return Py_BuildValue("(NN)", a[10] != Py_None ? Py_NewRef(a[10]) : wrap(qo),
+                       a[11] != Py_None ? Py_NewRef(a[11]) : ko.defined() ? wrap(ko) : Py_NewRef(Py_None));
+  CALL_END
+}
+
+// scale | None: 1 / sqrt(dim)
+float scale_of(PyObject* o, int64_t dim) {
+  if (o == Py_None) return (float)(1.0 / std::sqrt((double)dim));
+  const double x = PyFloat_AsDouble(o);
+  if (x == -1.0 && PyErr_Occurred()) throw python_error();
+  return (float)x;
+}
+// out | None, workspace | None -> the output and the call's workspace, which lives until the
+// call's work is queued: the allocator hands its memory on in stream order.
+struct AttentionOutputs {
+  Tensor out, workspace;
+  attn_rows rows;
+  AttentionOutputs(PyObject* given, PyObject* ws, const Tensor& q, Call& call) {
+    out = given != Py_None ? need_heads(given, "out", q.device(), q.size(0), q.size(1), q.size(2))
+                           : make(q.sizes(), at::kBFloat16, q.device());
+    need_distinct(out, "out");
+    rows = rows_of(out);
+    if (ws != Py_None) {
+      const Tensor* t = tensor_of(ws);
+      if (t == nullptr || t->device() != q.device() || !t->is_contiguous())
+        throw Refusal("workspace must be a contiguous tensor on the call's device");
+      workspace = *t;
+    } else {
+      workspace = make({(int64_t)ATTENTION_WS_BYTES}, at::kByte, q.device());
+    }
+    call.ex.workspace = workspace.data_ptr();
+    call.ex.workspace_bytes = workspace.nbytes();
+  }
+};
+
+// prompt(q, k, v, cu, scale | None, out | None, workspace | None, stream, dev_status) -> out
+PyObject* prompt(PyObject*, PyObject* const* a, Py_ssize_t nargs) {
+  CALL_BEGIN(9)
+  const at::Device dev = device_of(a[0], "q");
+  const Tensor& q = first_heads(a[0], "q");
+  prompt_attention_input in{};
+  in.tokens = q.size(0);
+  in.heads = q.size(1);
+  in.dim = q.size(2);
+  const Tensor* kt = tensor_of(a[1]);
+  in.kv_heads = kt != nullptr && kt->dim() == 3 ? kt->size(1) : 1;
+  in.q = rows_of(q);
+  in.k = rows_of(need_heads(a[1], "k", dev, in.tokens, in.kv_heads, in.dim));
+  in.v = rows_of(need_heads(a[2], "v", dev, in.tokens, in.kv_heads, in.dim));
+  const Tensor* cu = tensor_of(a[3]);
+  if (cu == nullptr || cu->dim() != 1 || cu->size(0) < 1) refuse("cu_seqlens", cu, at::kInt, {-1}, " contiguous");
+  in.batch = cu->size(0) - 1;
+  in.cu = need_vector(a[3], "cu_seqlens", at::kInt, dev, in.batch + 1).data_ptr<int32_t>();
+  in.scale = scale_of(a[4], in.dim);
+  Call call(dev, a[7], a[8]);
+  const AttentionOutputs o(a[5], a[6], q, call);
+  const int rc = lib.prompt(&in, &o.rows, &call.ex);
+  if (rc != NVFP4_OK) return fail("prompt_attention", rc);
+  return a[5] != Py_None ? Py_NewRef(a[5]) : wrap(o.out);
+  CALL_END
+}
+
+// paged(q, k_cache, v_cache, block_table, kv_lens, cu_new, scale | None, out | None,
+//       workspace | None, stream, dev_status) -> out
+PyObject* paged(PyObject*, PyObject* const* a, Py_ssize_t nargs) {
+  CALL_BEGIN(11)
+  const at::Device dev = device_of(a[0], "q");
+  const Tensor& q = first_heads(a[0], "q");
+  paged_attention_input in{};
+  in.tokens = q.size(0);
+  in.heads = q.size(1);
+  in.dim = q.size(2);
+  in.q = rows_of(q);
+  const Tensor& kc = need_pages(a[1], "k_cache", dev, {});
+  if (kc.size(3) != in.dim) throw Refusal("k_cache must have heads of the size of q's");
+  const Tensor& vc = need_pages(a[2], "v_cache", dev, kc.sizes());
+  in.pages = kc.size(0);
+  in.page_size = kc.size(1);
+  in.kv_heads = kc.size(2);
+  in.k = pages_of(kc);
+  in.v = pages_of(vc);
+  const Tensor* lens = tensor_of(a[4]);
+  if (lens == nullptr || lens->dim() != 1) refuse("kv_lens", lens, at::kInt, {-1}, " contiguous");
+  in.batch = lens->size(0);
+  in.kv_lens = need_vector(a[4], "kv_lens", at::kInt, dev, in.batch).data_ptr<int32_t>();
+  const Tensor* table = tensor_of(a[3]);
+  if (table == nullptr || table->dim() != 2) refuse("block_table", table, at::kInt, {in.batch, -1}, kRowsText);
+  need_rows(a[3], "block_table", at::kInt, dev, {in.batch, table->size(1)});
+  in.block_table = table->data_ptr<int32_t>();
+  in.max_pages = table->size(1);
+  in.ld_table = in.batch > 1 ? table->stride(0) : in.max_pages;
+  in.cu = need_vector(a[5], "cu_new", at::kInt, dev, in.batch + 1).data_ptr<int32_t>();
+  in.scale = scale_of(a[6], in.dim);
+  Call call(dev, a[9], a[10]);
+  const AttentionOutputs o(a[7], a[8], q, call);
+  const int rc = lib.paged(&in, &o.rows, &call.ex);
+  if (rc != NVFP4_OK) return fail("paged_attention", rc);
+  return a[7] != Py_None ? Py_NewRef(a[7]) : wrap(o.out);
+  CALL_END
+}
+
+// bind(quantize, rmsnorm, gemm, verify, plan, rope, prompt, paged, error): the library's
+// functions by address
 PyObject* bind(PyObject*, PyObject* const* a, Py_ssize_t nargs) {
-  if (nargs != 5) {
-    PyErr_SetString(PyExc_TypeError, "bind takes four addresses and an exception class");
+  constexpr int kCalls = 8;
+  if (nargs != kCalls + 1) {
+    PyErr_SetString(PyExc_TypeError, "bind takes eight addresses and an exception class");
     return nullptr;
   }
-  void* f[4];
-  for (int i = 0; i < 4; ++i) {
+  void* f[kCalls];
+  for (int i = 0; i < kCalls; ++i) {
     f[i] = PyLong_AsVoidPtr(a[i]);
     if (f[i] == nullptr) {
       if (!PyErr_Occurred()) PyErr_SetString(PyExc_ValueError, "null address");
@@ -405,8 +683,12 @@ PyObject* bind(PyObject*, PyObject* const* a, Py_ssize_t nargs) {
   lib.rmsnorm = reinterpret_cast<decltype(lib.rmsnorm)>(f[1]);
   lib.gemm = reinterpret_cast<decltype(lib.gemm)>(f[2]);
   lib.verify = reinterpret_cast<decltype(lib.verify)>(f[3]);
+  lib.plan = reinterpret_cast<decltype(lib.plan)>(f[4]);
+  lib.rope = reinterpret_cast<decltype(lib.rope)>(f[5]);
+  lib.prompt = reinterpret_cast<decltype(lib.prompt)>(f[6]);
+  lib.paged = reinterpret_cast<decltype(lib.paged)>(f[7]);
   Py_XDECREF(lib.error);
-  lib.error = Py_NewRef(a[4]);
+  lib.error = Py_NewRef(a[kCalls]);
   Py_RETURN_NONE;
 }
 
@@ -416,6 +698,10 @@ PyMethodDef methods[] = {{"bind", FAST(bind), METH_FASTCALL, nullptr},
                          {"rmsnorm", FAST(rmsnorm), METH_FASTCALL, nullptr},
                          {"gemm", FAST(gemm), METH_FASTCALL, nullptr},
                          {"verify", FAST(verify), METH_FASTCALL, nullptr},
+                         {"plan", FAST(plan), METH_FASTCALL, nullptr},
+                         {"rope", FAST(rope), METH_FASTCALL, nullptr},
+                         {"prompt", FAST(prompt), METH_FASTCALL, nullptr},
+                         {"paged", FAST(paged), METH_FASTCALL, nullptr},
                          {nullptr, nullptr, 0, nullptr}};
 PyModuleDef module = {PyModuleDef_HEAD_INIT, "_binding", nullptr, -1, methods, nullptr, nullptr, nullptr, nullptr};
 

@@ -160,3 +160,8 @@ int launch_fp8b_gemm(const fp8b_act* a, const fp8b_weight* w, void* c, int c_dty
                      int32_t* dev_status, cudaStream_t stream);
 int launch_spec_verify(const spec_verify_input* in, int32_t* out_tokens, int64_t ld_out,
                        int32_t* accepted, int32_t* dev_status, cudaStream_t stream);
+int launch_kv_plan(const kv_plan_input* in, const kv_plan_output* out, int32_t* dev_status, cudaStream_t stream);
+int launch_rope_kv_write(const rope_kv_input* in, const rope_kv_output* out, int32_t* dev_status,
+                         cudaStream_t stream);
+int launch_attention(const paged_attention_input* in, const attn_rows* out, void* workspace, int32_t* dev_status,
+                     cudaStream_t stream);  // (block_table NULL: packed prompts, one page of all tokens)

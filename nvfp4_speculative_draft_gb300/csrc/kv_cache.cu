@@ -1,0 +1,334 @@
+// kv_cache.cu -- the paged KV cache: which pages a batch's new tokens go to, and the
+// write of their rotated keys and their values.
+#include <cooperative_groups.h>
+
+#include "common.cuh"
+
+namespace {
+
+namespace cg = cooperative_groups;
+
+// ------------------------------------------------------------------- plan
+//
+// Per sequence: n new tokens behind len cached ones, need = ceil((len + n) / page)
+// pages, extra = max(0, need - held) of them from the top of the free stack, in the
+// order of the sequences.  Two prefix sums over the batch (tokens, then extra pages)
+// give every token its row and every new page its place; both are formed by each CTA
+// of one cluster for itself, in shared memory, and tokens and pages are then shared
+// out evenly, each finding its sequence by bisection.  All reads that an in-place call
+// overwrites come before the cluster's barrier, all writes behind it.
+
+constexpr int kPlanThreads = 512;
+constexpr int kPlanWarps = kPlanThreads / 32;
+
+struct PlanParams {
+  kv_plan_input in;
+  kv_plan_output out;
+  int32_t* dev_status;
+};
+
+// Exclusive prefix sums of each thread's value over the CTA; total to all.
+template <typename T>
+__device__ __forceinline__ T block_scan(T v, T* warp_sums, T& total) {
+  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+  T sum = v;
+#pragma unroll
+  for (int d = 1; d < 32; d <<= 1) {
+    const T o = __shfl_up_sync(0xFFFFFFFFu, sum, d);
+    if (lane >= d) sum += o;
+  }
+  __syncthreads();  // the sums of the scan before are read
+  if (lane == 31) warp_sums[warp] = sum;
+  __syncthreads();
+  T before = 0;
+  total = 0;
+#pragma unroll
+  for (int w = 0; w < kPlanWarps; ++w) {
+    const T x = warp_sums[w];
+    if (w < warp) before += x;
+    total += x;
+  }
+  return before + sum - v;
+}
+
+// Last s in [0, batch) with start[s] <= i (start ascends, start[0] <= i).
+__device__ __forceinline__ int find_sequence(const int32_t* start, int batch, int32_t i) {
+  int lo = 0, hi = batch;
+  while (hi - lo > 1) {
+    const int mid = (lo + hi) >> 1;
+    if (start[mid] <= i)
+      lo = mid;
+    else
+      hi = mid;
+  }
+  return lo;
+}
+
+__global__ void __launch_bounds__(kPlanThreads) kv_plan_kernel(const __grid_constant__ PlanParams p) {
+  extern __shared__ int32_t plan_smem[];
+  __shared__ int64_t sums64[kPlanWarps];
+  const int batch = (int)p.in.batch, page = (int)p.in.page_size;
+  const int64_t tokens = p.in.tokens, width = p.in.max_pages;
+  // per sequence: first token, first extra page, cached length, held pages; -1 - held where refused
+  int32_t* const s_token = plan_smem;
+  int32_t* const s_page = plan_smem + batch;
+  int32_t* const s_len = plan_smem + 2 * batch;
+  int32_t* const s_held = plan_smem + 3 * batch;
+  nvfp4::wait_for_previous_kernel();
+
+  cg::cluster_group cluster = cg::this_cluster();
+  const int rank = (int)cluster.block_rank(), ranks = (int)cluster.num_blocks();
+  int64_t left = *p.in.free_count;
+  int error = 0;
+  if (left < 0 || left > p.in.free_capacity) {
+    error = NVFP4_ERR_INDEX;
+    left = left < 0 ? 0 : p.in.free_capacity;
+  }
+  // each thread a run of neighbouring sequences
+  const int run = (batch + kPlanThreads - 1) / kPlanThreads;
+  const int first = min(batch, (int)threadIdx.x * run), last = min(batch, first + run);
+  int64_t mine = 0;
+  for (int s = first; s < last; ++s) mine += max(nvfp4::ld_ro(p.in.num_new + s), 0);
+  int64_t total;
+  int64_t at = block_scan<int64_t>(mine, sums64, total);
+  const int32_t used = (int32_t)min(total, tokens);
+  // pages wanted by the sequences that fit their table's row and the tokens
+  auto wanted = [&](int s, int64_t start, int32_t& n, int32_t& len, int32_t& held, bool& fits) -> int64_t {
+    n = max(nvfp4::ld_ro(p.in.num_new + s), 0);
+    len = max(nvfp4::ld_ro(p.in.lens + s), 0);
+    const int64_t least = ((int64_t)len + page - 1) / page;
+    const int64_t have = p.in.held != nullptr ? max(nvfp4::ld_ro(p.in.held + s), 0) : least;
+    held = (int32_t)min(have, width);
+    const int64_t need = n > 0 ? ((int64_t)len + n + page - 1) / page : 0;
+    fits = n == 0 || (need <= width && start + n <= tokens && (int64_t)len + n <= 0x7FFFFFFF);
+    return fits && need > held ? need - held : 0;
+  };
+  int64_t extra = 0;
+  {
+    int64_t start = at;
+    for (int s = first; s < last; ++s) {
+      int32_t n, len, held;
+      bool fits;
+      extra += wanted(s, start, n, len, held, fits);
+      start += n;
+    }
+  }
+  int64_t all_extra;
+  int64_t upto = block_scan<int64_t>(extra, sums64, all_extra);
+  int64_t taken = 0;  // pages taken by this thread's run, counted from the stack's top
+  for (int s = first; s < last; ++s) {
+    int32_t n, len, held;
+    bool fits;
+    const int64_t e = wanted(s, at, n, len, held, fits);
+    const bool ok = fits && (e == 0 || upto + e <= left);
+    s_token[s] = (int32_t)min(at, tokens);
+    s_page[s] = (int32_t)min(upto, left);
+    s_len[s] = len;
+    s_held[s] = ok ? held : -1 - held;
+    if (!ok) error = NVFP4_ERR_PAGES;
+    at += n;
+    upto += e;
+    if (ok && e > 0) taken = upto;
+  }
+  if (error) nvfp4::report(p.dev_status, error);
+  // the most that any sequence took up to (its prefix counts those before it, which all got theirs)
+  __syncthreads();
+  __shared__ unsigned long long most;
+  if (threadIdx.x == 0) most = 0ull;
+  __syncthreads();
+  if (taken > 0) atomicMax(&most, (unsigned long long)taken);
+  __syncthreads();
+  taken = (int64_t)most;
+  cluster.sync();
+
+  const int me = rank * kPlanThreads + (int)threadIdx.x, step = ranks * kPlanThreads;
+  for (int s = me; s < batch; s += step) {
+    const int32_t next = s + 1 < batch ? s_token[s + 1] : used;
+    const int32_t held = s_held[s] < 0 ? -1 - s_held[s] : s_held[s];
+    const int64_t n = s_held[s] < 0 ? 0 : next - s_token[s];
+    const int64_t kv = s_len[s] + n, need = n > 0 ? (kv + page - 1) / page : 0;
+    p.out.cu_new[s + 1] = next;
+    p.out.kv_lens[s] = (int32_t)kv;
+    if (p.out.held != nullptr) p.out.held[s] = (int32_t)max((int64_t)held, need);
+  }
+  if (me == 0) {
+    p.out.cu_new[0] = 0;
+    if (p.out.free_count != nullptr) *p.out.free_count = (int32_t)(left - taken);
+  }
+  const int32_t* top = p.in.free_pages + left - 1;
+  for (int64_t f = me; f < taken; f += step) {
+    const int s = find_sequence(s_page, batch, (int32_t)f);
+    p.in.block_table[s * p.in.ld_table + s_held[s] + (f - s_page[s])] = top[-f];
+  }
+  for (int64_t i = me; i < tokens; i += step) {
+    int32_t position = 0, slot = -1;
+    if (i < used) {
+      const int s = find_sequence(s_token, batch, (int32_t)i);
+      const int64_t at_kv = (int64_t)s_len[s] + (i - s_token[s]);
+      position = (int32_t)min(at_kv, (int64_t)0x7FFFFFFF);
+      const int32_t held = s_held[s];
+      if (held >= 0) {
+        const int32_t entry = position / page;
+        const int32_t id = entry < held ? p.in.block_table[s * p.in.ld_table + entry]
+                                        : top[-((int64_t)s_page[s] + entry - held)];
+        const int64_t where = (int64_t)id * page + position % page;
+        if (id >= 0 && where <= 0x7FFFFFFF)
+          slot = (int32_t)where;
+        else
+          nvfp4::report(p.dev_status, NVFP4_ERR_INDEX);
+      }
+    }
+    p.out.positions[i] = position;
+    p.out.slots[i] = slot;
+  }
+}
+
+// ------------------------------------------------------------------ rotary
+//
+// Pair i of a head, elements i and half + i:  (x, y) -> (x cos t - y sin t, x sin t + y cos t),
+// t = position[axis(i)] frequency(i).  The frequency is held as turns per position in
+// 64-bit fixed point: position times it wraps around to the fraction of a turn exactly,
+// however far the position (a binary32 angle at position 100 000 is off by 0.004).
+// The sines of a CTA's tokens are formed once, in shared memory; FP32 arithmetic, one
+// rounding to BF16.
+
+constexpr int kRopeThreads = 256;
+constexpr int kRopeTokens = 4;  // tokens of a CTA
+
+struct RopeParams {
+  rope_kv_input in;
+  rope_kv_output out;
+  int32_t* dev_status;
+};
+
+__device__ __forceinline__ uint4 load16(const __nv_bfloat16* p) {
+  uint4 v;
+  asm volatile("ld.global.v4.u32 {%0, %1, %2, %3}, [%4];" : "=r"(v.x), "=r"(v.y), "=r"(v.z), "=r"(v.w) : "l"(p));
+  return v;
+}
+__device__ __forceinline__ void store16(__nv_bfloat16* p, const uint4& v) {
+  asm volatile("st.global.v4.u32 [%0], {%1, %2, %3, %4};" ::"l"(p), "r"(v.x), "r"(v.y), "r"(v.z), "r"(v.w)
+               : "memory");
+}
+__device__ __forceinline__ uint32_t pack_bf16(float lo, float hi) {
+  const __nv_bfloat162 b = __floats2bfloat162_rn(lo, hi);
+  return *reinterpret_cast<const uint32_t*>(&b);
+}
+
+// Eight pairs: a = elements i.., b = elements half + i..
+__device__ __forceinline__ void rotate(uint4& a, uint4& b, const float2* cs) {
+  uint32_t x[4] = {a.x, a.y, a.z, a.w}, y[4] = {b.x, b.y, b.z, b.w};
+#pragma unroll
+  for (int j = 0; j < 4; ++j) {
+    const float4 t = reinterpret_cast<const float4*>(cs)[j];  // cos, sin of two pairs
+    const float x0 = __uint_as_float(x[j] << 16), x1 = __uint_as_float(x[j] & 0xFFFF0000u);
+    const float y0 = __uint_as_float(y[j] << 16), y1 = __uint_as_float(y[j] & 0xFFFF0000u);
+    x[j] = pack_bf16(x0 * t.x - y0 * t.y, x1 * t.z - y1 * t.w);
+    y[j] = pack_bf16(x0 * t.y + y0 * t.x, x1 * t.w + y1 * t.z);
+  }
+  a = make_uint4(x[0], x[1], x[2], x[3]);
+  b = make_uint4(y[0], y[1], y[2], y[3]);
+}
+
+__global__ void __launch_bounds__(kRopeThreads) rope_kv_kernel(const __grid_constant__ RopeParams p) {
+  __shared__ float2 angles[kRopeTokens][ROPE_MAX_DIM / 2];
+  __shared__ int64_t k_at[kRopeTokens], v_at[kRopeTokens];
+  const rope_kv_input& in = p.in;
+  const int half = (int)in.rot_dim / 2, dim = (int)in.dim;
+  const int64_t t0 = (int64_t)blockIdx.x * kRopeTokens;
+  const int count = (int)min(in.tokens - t0, (int64_t)kRopeTokens);
+  nvfp4::wait_for_previous_kernel();
+  for (int i = threadIdx.x; i < count * half; i += kRopeThreads) {
+    const int t = i / half, j = i - t * half;
+    const int axis = in.axis != nullptr ? in.axis[j] : 0;
+    const int64_t position = nvfp4::ld_ro(in.positions + (axis < in.axes ? axis : 0) * in.ld_positions + t0 + t);
+    const uint64_t turns = (uint64_t)position * in.turns[j];
+    float s, c;
+    sincospif((float)(int32_t)(turns >> 32) * 0x1p-31f, &s, &c);
+    angles[t][j] = make_float2(c, s);
+  }
+  const bool cached = in.k_cache.data != nullptr;
+  if (cached && (int)threadIdx.x < count) {
+    const int32_t slot = nvfp4::ld_ro(in.slots + t0 + threadIdx.x);
+    const int32_t page = slot / (int32_t)in.page_size, off = slot - page * (int32_t)in.page_size;
+    const bool ok = slot >= 0 && page < in.pages;
+    if (slot >= 0 && !ok) nvfp4::report(p.dev_status, NVFP4_ERR_INDEX);
+    k_at[threadIdx.x] = ok ? page * in.k_cache.ld_page + off * in.k_cache.ld_token : -1;
+    v_at[threadIdx.x] = ok ? page * in.v_cache.ld_page + off * in.v_cache.ld_token : -1;
+  }
+  __syncthreads();
+  // items: 16 elements of a (token, head): the two ends of eight pairs, or two neighbouring vectors
+  const int per_head = dim / 16, rot_items = half / 8;
+  const int q_heads = (int)in.heads, k_heads = q_heads + (int)in.kv_heads;
+  const int all = k_heads + (in.v.data != nullptr && cached ? (int)in.kv_heads : 0);
+  const int per_token = all * per_head;
+  for (int t = 0; t < count; ++t) {
+    const int64_t token = t0 + t;
+    for (int w = (int)blockIdx.y * kRopeThreads + (int)threadIdx.x; w < per_token; w += kRopeThreads * (int)gridDim.y) {
+      const int h = w / per_head, i = w - h * per_head;
+      const bool turn = i < rot_items && h < k_heads;
+      int lo, hi;
+      if (turn) {
+        lo = 8 * i;
+        hi = half + 8 * i;
+      } else {
+        lo = h < k_heads ? 2 * half + 16 * (i - rot_items) : 16 * i;
+        hi = lo + 8;
+      }
+      const __nv_bfloat16* src;
+      __nv_bfloat16 *dst = nullptr, *cache = nullptr;
+      if (h < q_heads) {
+        src = (const __nv_bfloat16*)in.q.data + token * in.q.ld_token + h * in.q.ld_head;
+        dst = (__nv_bfloat16*)p.out.q.data + token * p.out.q.ld_token + h * p.out.q.ld_head;
+      } else if (h < k_heads) {
+        const int kh = h - q_heads;
+        src = (const __nv_bfloat16*)in.k.data + token * in.k.ld_token + kh * in.k.ld_head;
+        if (p.out.k.data != nullptr) dst = (__nv_bfloat16*)p.out.k.data + token * p.out.k.ld_token + kh * p.out.k.ld_head;
+        if (cached && k_at[t] >= 0) cache = (__nv_bfloat16*)in.k_cache.data + k_at[t] + kh * in.k_cache.ld_head;
+      } else {
+        const int vh = h - k_heads;
+        src = (const __nv_bfloat16*)in.v.data + token * in.v.ld_token + vh * in.v.ld_head;
+        if (v_at[t] >= 0) cache = (__nv_bfloat16*)in.v_cache.data + v_at[t] + vh * in.v_cache.ld_head;
+      }
+      if (!turn && dst == src) dst = nullptr;  // in place: what is not rotated stays
+      if (dst == nullptr && cache == nullptr) continue;
+      uint4 a = load16(src + lo), b = load16(src + hi);
+      if (turn) rotate(a, b, &angles[t][8 * i]);
+      if (dst != nullptr) {
+        store16(dst + lo, a);
+        store16(dst + hi, b);
+      }
+      if (cache != nullptr) {
+        store16(cache + lo, a);
+        store16(cache + hi, b);
+      }
+    }
+  }
+}
+
+}  // namespace
+
+int launch_kv_plan(const kv_plan_input* in, const kv_plan_output* out, int32_t* dev_status, cudaStream_t stream) {
+  PlanParams p{*in, *out, dev_status};
+  const size_t smem = (size_t)in->batch * 16;
+  if (nvfp4::occupancy((const void*)kv_plan_kernel, kPlanThreads, smem) < 1) return NVFP4_ERR_CUDA;
+  // one CTA while each thread has a few tokens at most, else a cluster of eight
+  const unsigned ranks = in->tokens + in->batch <= 2 * kPlanThreads ? 1 : 8;
+  void* args[] = {&p};
+  return nvfp4::launch_dependent((const void*)kv_plan_kernel, dim3(ranks), dim3(kPlanThreads), smem, stream, ranks,
+                                 args) == cudaSuccess
+             ? NVFP4_OK
+             : NVFP4_ERR_CUDA;
+}
+
+int launch_rope_kv_write(const rope_kv_input* in, const rope_kv_output* out, int32_t* dev_status,
+                         cudaStream_t stream) {
+  RopeParams p{*in, *out, dev_status};
+  const int64_t groups = nvfp4::cdiv(in->tokens, kRopeTokens);
+  if (groups > 0x7FFFFFFF) return NVFP4_ERR_SHAPE;
+  void* args[] = {&p};
+  return nvfp4::launch_dependent((const void*)rope_kv_kernel, dim3((unsigned)groups), dim3(kRopeThreads), 0, stream, 1,
+                                 args) == cudaSuccess
+             ? NVFP4_OK
+             : NVFP4_ERR_CUDA;
+}
