@@ -1,90 +1,994 @@
 // attention.cu -- causal attention with grouped heads over packed prompts and over the
-// paged cache.
+// paged cache, on the 5th-generation tensor cores (sm_103a).
 //
-// One warp per (query, head): scores by shuffles, the softmax's maximum and sum carried
-// along, everything in FP32.
-#include "common.cuh"
+//   out_i = sum_{j <= i} softmax_j(scale q_i . k_j) v_j
+//
+// The query heads that share a key head are rows of one tile: row r of 128 is token
+// r / group, head r % group of it, so one token of many heads and many tokens of one
+// head take the same path.  An item is one key head's NQ such tiles of a sequence
+// against the keys that they see, 128 keys at a time:
+//   S = Q K^T        tcgen05.mma, both operands in shared memory, FP32 into TMEM
+//   P = exp2(S c - m)  registers; BF16 back into TMEM over S
+//   O += P V         tcgen05.mma, P from TMEM, V from shared memory (rows of keys as
+//                    they are in memory: the transposed operand form)
+// with the softmax's running maximum m and sum carried along.  m is raised, and O and
+// the sum rescaled, only when a tile's maximum exceeds it by 2^8: P is then at most 256
+// and loses nothing (FP32 and BF16 keep their relative precision), and O, which lies in
+// TMEM, is rarely touched.
+//   NQ = 2 (heads of 64 and 128): two tiles of rows share each tile of keys; a
+//          warpgroup of softmax threads, a row each, for either, so that one's
+//          exponentials run while the tensor core works on the other's products;
+//   NQ = 1 (few rows, and heads of 256, whose O takes 256 of TMEM's 512 columns): both
+//          warpgroups work on the same tile, half of its keys each, and exchange the
+//          rows' maxima through shared memory; S is double buffered.
+//   warps 0..7  softmax; they rescale and finish O as well
+//   warp 8      allocates TMEM, issues the MMAs: S two steps ahead of the P V it waits for
+//   warp 9      schedules the items and loads K and V (TMA) into a ring
+//   warp 10     loads Q
+//
+// Schedule: the items of all sequences and heads are laid end to end on a line, a tile of
+// keys 128 units long and an item's start kItemCost, and every CTA takes an equal share of
+// it, whatever the lengths: each finds its share from the lengths on the device.  An item
+// that a share's border cuts leaves the parts' (maximum, sum, O) in the workspace, FP32, and
+// a second kernel joins them in the order of the keys.  The borders depend on the lengths
+// alone, so results do not depend on timing.
+//
+// Keys that no row of an item sees are not loaded (zeros instead), those that some row
+// does not see get weight 0 by selection.
+#include <cuda_bf16.h>
+
+#include "tc.cuh"
 
 namespace {
 
-constexpr int kThreads = 256;
+using namespace nvfp4::tc;
+using nvfp4::ld_ro;
+
+constexpr int kRows = 128;                    // MMA rows of a tile of queries
+constexpr int kKeys = 128;                    // keys of a tile
+constexpr int kSoftmaxWarps = 8;
+constexpr int kWarps = kSoftmaxWarps + 4;     // (three of the last four work)
+constexpr int kThreads = 32 * kWarps;
+constexpr int kDescs = 4;                     // item descriptors in flight
+constexpr int kItemCost = kKeys;              // an item's fixed cost, in keys
+constexpr int kMinShare = 2 * kKeys + kItemCost;  // of a CTA, where there are that few
+constexpr float kRescale = 8.0f;              // log2 of what the maximum may lag behind
+constexpr float kLog2e = 1.4426950408889634f;
+
+template <int D, int NQ>
+struct Tile {
+  static constexpr int kUnitDims = D < 128 ? D : 128;  // of a unit of the ring: 128 keys of as many dims
+  static constexpr int kUnits = D / kUnitDims;         // of a tile of K, and of V
+  static constexpr int kBlocks = kUnitDims / 64;       // swizzled columns of 128 bytes
+  static constexpr int kUnitBytes = kKeys * kUnitDims * 2;
+  static constexpr int kQTile = kRows * D * 2;
+  static constexpr int kQBytes = NQ * kQTile;
+  static constexpr int kXchBytes = NQ == 1 ? 2 * 2 * kRows * 4 : 0;
+  static constexpr int kDescBytes = kDescs * 64;
+  static constexpr int kRest = kXchBytes + kDescBytes + 512;
+  static constexpr int kFit = (227 * 1024 - kQBytes - kRest) / kUnitBytes;
+  static constexpr int kStages = kFit < 10 ? kFit : 10;
+  static constexpr size_t kSmemBytes = (size_t)kQBytes + (size_t)kStages * kUnitBytes + kRest;
+  static constexpr int kCols = NQ == 2 ? kKeys : kKeys / 2;  // of S, a softmax thread's
+  static constexpr int kOut = NQ == 2 ? D : D / 2;           // of O, a softmax thread's
+  static_assert(kStages >= 5 && kStages > kUnits, "ring");
+  static_assert(2 * kKeys + NQ * D <= 512, "TMEM");
+};
 
 struct Params {
-  paged_attention_input in;
-  attn_rows out;
+  const int32_t* cu;
+  const int32_t* kv_lens;  // nullptr: prompts
+  const int32_t* table;
+  int64_t ld_table, capacity;  // tokens of a table row
+  int tokens, batch, kv_heads, group;
+  int page_size, box;          // tokens of a page and of a TMA box
+  int pages;
+  float scale;                 // |scale| log2 e, never 0
+  int negative;
+  __nv_bfloat16* out;
+  int64_t ld_token, ld_head;
+  unsigned char* ws;
   int32_t* dev_status;
 };
 
-template <int D>
-__global__ void __launch_bounds__(kThreads) attention_kernel(const __grid_constant__ Params p) {
-  constexpr int E = D / 32;
-  const paged_attention_input& in = p.in;
-  const int lane = threadIdx.x & 31;
-  nvfp4::wait_for_previous_kernel();
-  const int64_t item = (int64_t)blockIdx.x * (kThreads / 32) + (threadIdx.x >> 5);
-  const int64_t row = item / in.heads, head = item % in.heads, kv_head = head / (in.heads / in.kv_heads);
-  if (row >= in.tokens) return;
-  // the sequence of the row
-  int64_t seq = -1, begin = 0, end = 0;
-  for (int64_t s = 0; s < in.batch; ++s) {
-    if (in.cu[s] < 0 || in.cu[s + 1] > in.tokens || in.cu[s] > in.cu[s + 1] ||
-        (in.block_table != nullptr && in.kv_lens[s] > in.max_pages * in.page_size))
-      nvfp4::report(p.dev_status, NVFP4_ERR_INDEX);
-    const int64_t a = min(max((int64_t)in.cu[s], (int64_t)0), in.tokens), b = min((int64_t)in.cu[s + 1], in.tokens);
-    if (row >= a && row < b) {
-      seq = s;
-      begin = a;
-      end = b;
-      break;
+struct Sequence {
+  int begin, n;  // rows of q
+  int len;       // keys
+  int off;       // position of the first query (may be negative)
+};
+
+// What the roles need of an item, in shared memory.
+struct __align__(16) Item {
+  int row0, rows;   // tokens: first row of q, number (0: no more items)
+  int pos0, end;    // position of the first; keys that some row sees
+  int head, first;  // key head; first tile of this part
+  int last, slot;   // past its last tile; -1: the whole item, else the part's place
+};
+
+// An item cut by a share's border, for the kernel that joins its parts.
+struct Record {
+  int parts, row0, rows, head;
+};
+
+__host__ __device__ constexpr int64_t slot_floats(int d, int nq) { return (int64_t)nq * kRows * (d + 2); }
+constexpr size_t kRecordBytes = (size_t)ATTENTION_MAX_CTAS * 64;
+
+__device__ __forceinline__ Sequence sequence(const Params& p, int s) {
+  const int a = ld_ro(p.cu + s), b = ld_ro(p.cu + s + 1);
+  Sequence q;
+  q.begin = min(max(a, 0), p.tokens);
+  q.n = max(min(max(b, 0), p.tokens) - q.begin, 0);
+  q.len = q.n;
+  if (p.kv_lens != nullptr) q.len = (int)min((int64_t)max(ld_ro(p.kv_lens + s), 0), p.capacity);
+  q.off = q.len - q.n;
+  return q;
+}
+__device__ __forceinline__ bool consistent(const Params& p, int s) {
+  const int a = ld_ro(p.cu + s), b = ld_ro(p.cu + s + 1);
+  return a >= 0 && b <= p.tokens && a <= b && (p.kv_lens == nullptr || ld_ro(p.kv_lens + s) <= p.capacity);
+}
+
+// The line: item t of a (sequence, head) starts `before(t)` behind its head's start.
+template <int NQ>
+struct Line {
+  int per;       // tokens of an item
+  int64_t base;  // length of item 0
+  int items;
+  int64_t length;
+  __device__ __forceinline__ Line(const Sequence& q, int group) {
+    per = NQ * (kRows / group);
+    items = (q.n + per - 1) / per;
+    const int64_t cached = max(q.off, 0);
+    base = cached + per + kItemCost;
+    length = items > 0 ? before(items - 1) + cached + q.n + kItemCost : 0;
+  }
+  __device__ __forceinline__ int64_t before(int64_t t) const { return t * base + per * (t * (t - 1) / 2); }
+};
+
+__device__ __forceinline__ void tma_load_4d(uint32_t dst, const CUtensorMap* map, int c0, int c1, int c2, int c3,
+                                            uint32_t bar) {
+  asm volatile(
+      "cp.async.bulk.tensor.4d.shared::cluster.global.mbarrier::complete_tx::bytes"
+      " [%0], [%1, {%2, %3, %4, %5}], [%6];" ::"r"(dst),
+      "l"(reinterpret_cast<uint64_t>(map)), "r"(c0), "r"(c1), "r"(c2), "r"(c3), "r"(bar)
+      : "memory");
+}
+// kind::f16 with BF16 operands, D = F32; bit 16: B is N-major in shared memory.
+constexpr uint32_t idesc_bf16(int n, bool b_transposed) {
+  return (1u << 4) | (1u << 7) | (1u << 10) | ((b_transposed ? 1u : 0u) << 16) | ((uint32_t)(n >> 3) << 17) |
+         ((uint32_t)(kRows >> 4) << 24);
+}
+__device__ __forceinline__ void mma_ss(uint32_t d, uint64_t a, uint64_t b, uint32_t idesc, uint32_t accumulate) {
+  asm volatile(
+      "{\n .reg .pred p;\n setp.ne.b32 p, %4, 0;\n"
+      " tcgen05.mma.cta_group::1.kind::f16 [%0], %1, %2, %3, p;\n}" ::"r"(d),
+      "l"(a), "l"(b), "r"(idesc), "r"(accumulate)
+      : "memory");
+}
+__device__ __forceinline__ void mma_ts(uint32_t d, uint32_t a, uint64_t b, uint32_t idesc, uint32_t accumulate) {
+  asm volatile(
+      "{\n .reg .pred p;\n setp.ne.b32 p, %4, 0;\n"
+      " tcgen05.mma.cta_group::1.kind::f16 [%0], [%1], %2, %3, p;\n}" ::"r"(d),
+      "r"(a), "l"(b), "r"(idesc), "r"(accumulate)
+      : "memory");
+}
+// V as B: 64-element columns of 128 keys 16 KB apart (leading), 8-key groups 1 KB apart
+// (stride), 128-byte swizzle.
+__device__ __forceinline__ uint64_t desc_v(uint32_t addr) {
+  return (uint64_t)((addr >> 4) & 0x3FFFu) | ((uint64_t)(kKeys * 128 >> 4) << 16) | ((uint64_t)(1024 >> 4) << 32) |
+         ((uint64_t)1 << 46) | ((uint64_t)2 << 61);
+}
+__device__ __forceinline__ void tmem_store(uint32_t taddr, const uint32_t (&v)[16]) {
+  asm volatile(
+      "tcgen05.st.sync.aligned.32x32b.x16.b32 [%0], {%1,%2,%3,%4,%5,%6,%7,%8,%9,%10,%11,%12,%13,%14,%15,%16};" ::"r"(taddr),
+      "r"(v[0]), "r"(v[1]), "r"(v[2]), "r"(v[3]), "r"(v[4]), "r"(v[5]), "r"(v[6]), "r"(v[7]), "r"(v[8]), "r"(v[9]),
+      "r"(v[10]), "r"(v[11]), "r"(v[12]), "r"(v[13]), "r"(v[14]), "r"(v[15])
+      : "memory");
+}
+__device__ __forceinline__ void tmem_store_wait() { asm volatile("tcgen05.wait::st.sync.aligned;" ::: "memory"); }
+__device__ __forceinline__ float exp2_approx(float x) {  // 2^-22 relative; 0 for -inf
+  float y;
+  asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"(x));
+  return y;
+}
+__device__ __forceinline__ uint64_t fma2(uint64_t a, uint64_t b, uint64_t c) {
+  uint64_t d;
+  asm("fma.rn.f32x2 %0, %1, %2, %3;" : "=l"(d) : "l"(a), "l"(b), "l"(c));
+  return d;
+}
+__device__ __forceinline__ uint64_t add2(uint64_t a, uint64_t b) {
+  uint64_t d;
+  asm("add.rn.f32x2 %0, %1, %2;" : "=l"(d) : "l"(a), "l"(b));
+  return d;
+}
+__device__ __forceinline__ uint32_t to_bf16x2(float lo, float hi) {
+  const __nv_bfloat162 b = __floats2bfloat162_rn(lo, hi);
+  return *reinterpret_cast<const uint32_t*>(&b);
+}
+// All softmax threads: true if `ok` holds for all of them (so they leave together).
+__device__ __forceinline__ bool softmax_agree(bool ok) {
+  uint32_t r;
+  asm volatile(
+      "{\n .reg .pred p, q;\n setp.ne.b32 p, %1, 0;\n barrier.cta.red.and.pred q, 1, %2, p;\n selp.u32 %0, 1, 0, q;\n}"
+      : "=r"(r)
+      : "r"((uint32_t)ok), "n"(32 * kSoftmaxWarps)
+      : "memory");
+  return r != 0;
+}
+
+// ----------------------------------------------------------------- kernel
+
+template <int D, int NQ>
+__global__ void __launch_bounds__(kThreads, 1)
+attention_kernel(const __grid_constant__ CUtensorMap map_q, const __grid_constant__ CUtensorMap map_k,
+                 const __grid_constant__ CUtensorMap map_v, const __grid_constant__ Params p) {
+  using L = Tile<D, NQ>;
+  constexpr int kStages = L::kStages, kUnits = L::kUnits, kBlocks = L::kBlocks;
+  extern __shared__ __align__(1024) unsigned char smem[];
+  unsigned char* const ring_ptr = smem + L::kQBytes;
+  float* const xch = reinterpret_cast<float*>(ring_ptr + kStages * L::kUnitBytes);
+  Item* const items = reinterpret_cast<Item*>(reinterpret_cast<unsigned char*>(xch) + L::kXchBytes);
+  const uint32_t q_smem = smem_u32(smem), ring = q_smem + L::kQBytes;
+  const uint32_t bars = smem_u32(items) + L::kDescBytes;
+  auto full = [&](int s) { return bars + 8u * s; };
+  auto empty = [&](int s) { return bars + 8u * (kStages + s); };
+  auto item_full = [&](int i) { return bars + 8u * (2 * kStages + i); };
+  auto item_empty = [&](int i) { return bars + 8u * (2 * kStages + kDescs + i); };
+  constexpr int kFixed = 2 * kStages + 2 * kDescs;
+  const uint32_t q_full = bars + 8u * kFixed, q_empty = bars + 8u * (kFixed + 1);
+  auto s_full = [&](int b) { return bars + 8u * (kFixed + 2 + b); };
+  auto p_full = [&](int b) { return bars + 8u * (kFixed + 4 + b); };
+  auto pv_done = [&](int t) { return bars + 8u * (kFixed + 6 + t); };
+  const uint32_t drain_bar = bars + 8u * (kFixed + 8);
+  static_assert(8 * (kFixed + 9 + kWarps + 1) + 12 <= 512, "shared memory behind the items");
+  int64_t* const sums = reinterpret_cast<int64_t*>(reinterpret_cast<unsigned char*>(items) + L::kDescBytes + 8 * (kFixed + 9));
+  int64_t& start_at = sums[kWarps];
+  uint32_t* const tmem_slot = reinterpret_cast<uint32_t*>(sums + kWarps + 1);
+  volatile uint32_t* abort = tmem_slot + 1;
+  int& start_seq = reinterpret_cast<int*>(tmem_slot)[2];
+  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+
+  if (q_smem & 1023u) {  // (the swizzled tiles need it; the declaration asks for it)
+    nvfp4::report(p.dev_status, NVFP4_ERR_ALIGN);
+    return;
+  }
+  if (threadIdx.x == 0) {
+    for (int s = 0; s < kStages; ++s) {
+      mbar_init(full(s), 1);
+      mbar_init(empty(s), 1);
     }
+    for (int i = 0; i < kDescs; ++i) {
+      mbar_init(item_full(i), 1);
+      mbar_init(item_empty(i), kSoftmaxWarps + 2);
+    }
+    mbar_init(q_full, 1);
+    mbar_init(q_empty, 1);
+    for (int b = 0; b < 2; ++b) {
+      mbar_init(s_full(b), 1);
+      mbar_init(p_full(b), NQ == 2 ? kSoftmaxWarps / 2 : kSoftmaxWarps);
+      mbar_init(pv_done(b), 1);
+    }
+    mbar_init(drain_bar, 1);
+    *abort = 0u;
+    asm volatile("fence.mbarrier_init.release.cluster;" ::: "memory");
   }
-  if (seq < 0) return;
-  int64_t len = end - begin;
-  if (in.block_table != nullptr) len = min((int64_t)in.kv_lens[seq], in.max_pages * in.page_size);
-  const int64_t seen = min(len, len - (end - begin) + (row - begin) + 1);
-  const __nv_bfloat16* q = (const __nv_bfloat16*)in.q.data + row * in.q.ld_token + head * in.q.ld_head;
-  float qv[E], o[E], m = -INFINITY, l = 0.0f;
-  for (int e = 0; e < E; ++e) {
-    qv[e] = __bfloat162float(q[lane + 32 * e]) * in.scale;
-    o[e] = 0.0f;
+  if (warp == 8) {
+    asm volatile("tcgen05.alloc.cta_group::1.sync.aligned.shared::cta.b32 [%0], %1;" ::"r"(smem_u32(tmem_slot)), "r"(512)
+                 : "memory");
+    asm volatile("tcgen05.relinquish_alloc_permit.cta_group::1.sync.aligned;" ::: "memory");
   }
-  for (int64_t j = 0; j < seen; ++j) {
-    int64_t page = 0, at = begin + j;
-    if (in.block_table != nullptr) {
-      page = in.block_table[seq * in.ld_table + j / in.page_size];
-      at = j % in.page_size;
-      if (page < 0 || page >= in.pages) {
+  if (threadIdx.x >= 288 && threadIdx.x < 291) {
+    const CUtensorMap* m = threadIdx.x == 288 ? &map_q : threadIdx.x == 289 ? &map_k : &map_v;
+    asm volatile("prefetch.tensormap [%0];" ::"l"(reinterpret_cast<uint64_t>(m)) : "memory");
+  }
+  nvfp4::wait_for_previous_kernel();
+
+  // This CTA's share [x0, x1) of the line, and the sequence that x0 lies in.
+  const int run = (p.batch + kThreads - 1) / kThreads;
+  const int s0 = min(p.batch, (int)threadIdx.x * run), s1 = min(p.batch, s0 + run);
+  int64_t mine = 0;
+  for (int s = s0; s < s1; ++s) {
+    mine += p.kv_heads * Line<NQ>(sequence(p, s), p.group).length;
+    if (blockIdx.x == 0 && !consistent(p, s)) nvfp4::report(p.dev_status, NVFP4_ERR_INDEX);
+  }
+  int64_t upto = mine;
+#pragma unroll
+  for (int d = 1; d < 32; d <<= 1) {
+    const int64_t o = __shfl_up_sync(0xFFFFFFFFu, upto, d);
+    if (lane >= d) upto += o;
+  }
+  if (lane == 31) sums[warp] = upto;
+  if (threadIdx.x == 0) start_seq = p.batch;
+  tc_fence_before();
+  __syncthreads();
+  tc_fence_after();
+  const uint32_t tmem = *tmem_slot;
+  int64_t total = 0;
+#pragma unroll
+  for (int w = 0; w < kWarps; ++w) {
+    if (w == warp) upto += total;
+    total += sums[w];
+  }
+  const int64_t wanted = total / kMinShare;
+  const int shares = (int)(wanted < 1 ? 1 : wanted < gridDim.x ? wanted : gridDim.x);
+  const int64_t x0 = (int)blockIdx.x < shares ? total * blockIdx.x / shares : total;
+  const int64_t x1 = (int)blockIdx.x < shares ? total * (blockIdx.x + 1) / shares : total;
+  if (x0 < x1 && upto > x0 && upto - mine <= x0) {
+    int64_t at = upto - mine;
+    int s = s0;
+    for (; s + 1 < s1; ++s) {
+      const int64_t len = p.kv_heads * Line<NQ>(sequence(p, s), p.group).length;
+      if (at + len > x0) break;
+      at += len;
+    }
+    start_seq = s;
+    start_at = at;
+  }
+  __syncthreads();
+
+  const int per_tile = kRows / p.group;  // tokens of a tile of rows
+  int issued = 0, q_issued = 0;          // units and Q loads issued (TMA warps)
+
+  // NQ = 2: the softmax's threads take registers that the others have no use for
+  // (256 x 208 + 128 x 88 = 384 x 168, what the block was launched with).
+  if (NQ == 2 && warp >= kSoftmaxWarps) asm volatile("setmaxnreg.dec.sync.aligned.u32 88;");
+  if (warp == 9) {
+    // ------------------------------------------------- schedule, K and V loads
+    // (all lanes together; a lane per box of a unit issues)
+    const int boxes = kKeys / p.box;
+    const int sub = lane / kBlocks, block = lane % kBlocks;
+    const bool loads = sub < boxes;
+    bool ok = true;
+    int seq = start_seq, head = 0, t = 0;
+    Sequence q{}, next_q{};
+    int64_t head_at = 0;
+    if (seq < p.batch) {
+      q = sequence(p, seq);
+      const Line<NQ> line(q, p.group);
+      head = (int)((x0 - start_at) / line.length);
+      head_at = start_at + head * line.length;
+      int lo = 0, hi = line.items;  // the item that x0 lies in
+      while (hi - lo > 1) {
+        const int mid = (lo + hi) >> 1;
+        if (head_at + line.before(mid) <= x0)
+          lo = mid;
+        else
+          hi = mid;
+      }
+      t = lo;
+      if (seq + 1 < p.batch) next_q = sequence(p, seq + 1);
+    }
+    // The next part of this CTA's share, or rows = 0.  `row` is its table row, `begin` its
+    // first token in packed prompts.
+    struct Part {
+      Item it;
+      int64_t row;
+      int begin;
+      int record;  // parts of the whole item, where this is the first of several
+    };
+    auto advance = [&]() -> Part {
+      Part r{};
+      r.it.rows = 0;
+      while (seq < p.batch) {
+        const Line<NQ> line(q, p.group);
+        if (t >= line.items) {
+          t = 0;
+          head_at += line.length;
+          if (q.n == 0 || ++head >= p.kv_heads) {
+            head = 0;
+            ++seq;
+            q = next_q;
+            if (seq + 1 < p.batch) next_q = sequence(p, seq + 1);
+          }
+          continue;
+        }
+        const int64_t at = head_at + line.before(t) + kItemCost;  // of tile 0
+        if (at - kItemCost >= x1) break;
+        const int row = t * line.per, rows = min(line.per, q.n - row);
+        const int end = max(q.off + row + rows, 0);
+        const int tiles = max((end + kKeys - 1) / kKeys, 1);
+        const int64_t a = at >= x0 ? 0 : (x0 - at + kKeys - 1) / kKeys;
+        const int64_t b = at >= x1 ? 0 : (x1 - at + kKeys - 1) / kKeys;
+        ++t;
+        if (a >= tiles || b <= a) continue;
+        r.it.row0 = q.begin + row;
+        r.it.rows = rows;
+        r.it.pos0 = q.off + row;
+        r.it.end = end;
+        r.it.head = head;
+        r.it.first = (int)a;
+        r.it.last = (int)min(b, (int64_t)tiles);
+        r.it.slot = a > 0 ? 0 : b < tiles ? 1 : -1;
+        r.row = seq * p.ld_table;
+        r.begin = q.begin;
+        if (a == 0 && b < tiles) {
+          const int64_t last_tile = at + (int64_t)(tiles - 1) * kKeys;
+          r.record = (int)(((last_tile + 1) * shares - 1) / total) - (int)blockIdx.x + 1;
+        }
+        break;
+      }
+      return r;
+    };
+    // The page of this lane's box of a tile; past the cache (zeros) where no row sees it.
+    auto page_of = [&](const Part& r, int tile) -> int {
+      const int j = tile * kKeys + sub * p.box;
+      if (!loads || j >= r.it.end) return p.pages;
+      if (p.table == nullptr) return 0;
+      const int id = ld_ro(p.table + r.row + j / p.page_size);
+      if (id < 0 || id >= p.pages) {
         nvfp4::report(p.dev_status, NVFP4_ERR_INDEX);
-        page = -1;
+        return p.pages;
+      }
+      return id;
+    };
+    int unit = 0;
+    auto load_unit = [&](const CUtensorMap* map, const Part& r, int tile, int page, int u) {
+      const int s = unit % kStages;
+      if (unit >= kStages) ok = ok && mbar_wait(empty(s), (unit / kStages - 1) & 1, abort, p.dev_status);
+      ok = __all_sync(0xFFFFFFFFu, ok);
+      if (!ok) return;
+      issued = unit + 1;
+      const bool withheld = nvfp4::kWithhold && blockIdx.x == 0 && unit == 0;  // test build: never issued
+      ++unit;
+      if (withheld) return;
+      if (lane == 0) mbar_arrive_expect_tx(full(s), L::kUnitBytes);
+      __syncwarp();
+      if (loads) {
+        const int j = tile * kKeys + sub * p.box;
+        const int token = p.table == nullptr ? r.begin + j : j % p.page_size;
+        tma_load_4d(ring + (uint32_t)(s * L::kUnitBytes + block * (kKeys * 128) + sub * p.box * 128), map,
+                    u * L::kUnitDims + block * 64, r.it.head, token, page, full(s));
+      }
+    };
+    auto load_tile = [&](const CUtensorMap* map, const Part& r, int tile, int page) {
+      for (int u = 0; u < kUnits && ok; ++u) load_unit(map, r, tile, page, u);
+    };
+    Part cur = advance();
+    int page = cur.it.rows ? page_of(cur, cur.it.first) : 0;
+    Part prev{};
+    int prev_tile = -1, prev_page = 0, count = 0, record = 0;
+    Part recorded{};
+    while (ok) {
+      const int i = count % kDescs;
+      if (count >= kDescs) ok = mbar_wait(item_empty(i), (count / kDescs - 1) & 1, abort, p.dev_status);
+      ok = __all_sync(0xFFFFFFFFu, ok);
+      if (!ok) break;
+      if (lane == 0) {
+        items[i] = cur.it;
+        mbar_arrive(item_full(i));
+      }
+      __syncwarp();
+      ++count;
+      if (cur.it.rows == 0) break;
+      if (cur.record) {
+        record = cur.record;
+        recorded = cur;
+      }
+      const Part next = advance();
+      int next_first = 0;
+      if (next.it.rows) next_first = page_of(next, next.it.first);
+      for (int tile = cur.it.first; tile < cur.it.last && ok; ++tile) {
+        const int next_page = tile + 1 < cur.it.last ? page_of(cur, tile + 1) : next_first;
+        load_tile(&map_k, cur, tile, page);
+        if constexpr (NQ == 2) {
+          load_tile(&map_v, cur, tile, page);
+        } else {
+          // V one tile behind K, as the MMAs take them
+          if (prev_tile >= 0) load_tile(&map_v, prev, prev_tile, prev_page);
+          prev = cur;
+          prev_tile = tile;
+          prev_page = page;
+        }
+        page = next_page;
+      }
+      cur = next;
+    }
+    if (NQ == 1 && ok && prev_tile >= 0) {
+      unit += kUnits;  // the place of a K that does not come: V's is the same for every tile
+      load_tile(&map_v, prev, prev_tile, prev_page);
+    }
+    if (lane == 0) {
+      Record* rec = reinterpret_cast<Record*>(p.ws + (size_t)blockIdx.x * 64);
+      *rec = Record{record, recorded.it.row0, recorded.it.rows, recorded.it.head};
+    }
+  } else if (warp == 10) {
+    // ------------------------------------------------------------------ Q loads
+    if (lane == 0) {
+      for (int count = 0;; ++count) {
+        const int i = count % kDescs;
+        if (!mbar_wait(item_full(i), (count / kDescs) & 1, abort, p.dev_status)) break;
+        const Item it = items[i];
+        mbar_arrive(item_empty(i));
+        if (it.rows == 0) break;
+        if (count > 0 && !mbar_wait(q_empty, (count - 1) & 1, abort, p.dev_status)) break;
+        q_issued = count + 1;
+        mbar_arrive_expect_tx(q_full, (uint32_t)(NQ * (D / 64) * per_tile * p.group * 128));
+        for (int t = 0; t < NQ; ++t)
+          for (int b = 0; b < D / 64; ++b)
+            tma_load_4d(q_smem + (uint32_t)(t * L::kQTile + b * (kRows * 128)), &map_q, b * 64, 0, it.head,
+                        it.row0 + t * per_tile, q_full);
       }
     }
-    const __nv_bfloat16* k = (const __nv_bfloat16*)in.k.data + page * in.k.ld_page + at * in.k.ld_token + kv_head * in.k.ld_head;
-    const __nv_bfloat16* v = (const __nv_bfloat16*)in.v.data + page * in.v.ld_page + at * in.v.ld_token + kv_head * in.v.ld_head;
-    float s = 0.0f;
-    if (page >= 0)
-      for (int e = 0; e < E; ++e) s += qv[e] * __bfloat162float(k[lane + 32 * e]);
-    for (int d = 16; d; d >>= 1) s += __shfl_xor_sync(0xFFFFFFFFu, s, d);
-    const float next = fmaxf(m, s), keep = __expf(m - next), w = __expf(s - next);
-    l = l * keep + w;
-    for (int e = 0; e < E; ++e) o[e] = o[e] * keep + (page >= 0 ? w * __bfloat162float(v[lane + 32 * e]) : 0.0f);
-    m = next;
+  } else if (warp == 8) {
+    // --------------------------------------------------------------------- MMAs
+    // Steps g = 0, 1, ... over all items: NQ = 2: tile of keys g / 2, rows g % 2; NQ = 1: tile
+    // g.  S of step g into buffer g % 2.  Two cursors, S's two steps ahead.
+    constexpr uint32_t kIdescS = idesc_bf16(kKeys, false), kIdescO = idesc_bf16(L::kUnitDims, true);
+    bool ok = true;
+    struct Cursor {
+      int count, tile, first, last, end, rows, x;  // item, tile of it; tiles of the CTA before
+      int row_tile;
+    };
+    Cursor cs{}, cp{};
+    auto fetch = [&](Cursor& c, bool release) {  // the cursor's next item
+      const int i = c.count % kDescs;
+      ok = mbar_wait(item_full(i), (c.count / kDescs) & 1, abort, p.dev_status);
+      ok = __all_sync(0xFFFFFFFFu, ok);
+      if (!ok) return;
+      const Item it = items[i];
+      c.rows = it.rows;
+      c.tile = c.first = it.first;
+      c.last = it.last;
+      c.end = it.end;
+      c.row_tile = 0;
+      ++c.count;
+      __syncwarp();
+      if (release && lane == 0) mbar_arrive(item_empty(i));
+    };
+    auto step = [&](Cursor& c, bool release) {
+      if (NQ == 2 && c.row_tile == 0) {
+        c.row_tile = 1;
+        return;
+      }
+      c.row_tile = 0;
+      ++c.x;
+      if (++c.tile == c.last) fetch(c, release);
+    };
+    auto wait_unit = [&](int unit) {
+      ok = ok && mbar_wait(full(unit % kStages), (unit / kStages) & 1, abort, p.dev_status);
+      ok = __all_sync(0xFFFFFFFFu, ok);
+    };
+    int gs = 0;
+    auto issue_s = [&]() {
+      if (cs.tile == cs.first && cs.row_tile == 0) {
+        ok = mbar_wait(q_full, (cs.count - 1) & 1, abort, p.dev_status);
+        ok = __all_sync(0xFFFFFFFFu, ok);
+        if (!ok) return;
+      }
+      const int u0 = NQ == 2 ? 2 * cs.x * kUnits : cs.x == 0 ? 0 : (2 * cs.x - 1) * kUnits;
+      const uint32_t d = tmem + (uint32_t)(gs & 1) * kKeys;
+      const bool last_use = NQ == 1 || cs.row_tile == 1;
+#pragma unroll
+      for (int u = 0; u < kUnits; ++u) {
+        if (NQ == 1 || cs.row_tile == 0) wait_unit(u0 + u);
+        if (!ok) return;
+        tc_fence_after();
+        const uint64_t a = smem_desc(q_smem + (uint32_t)(cs.row_tile * L::kQTile + u * kBlocks * (kRows * 128)));
+        const uint64_t b = smem_desc(ring + (uint32_t)((u0 + u) % kStages * L::kUnitBytes));
+        if (elect_one()) {
+#pragma unroll
+          for (int kk = 0; kk < L::kUnitDims / 16; ++kk) {
+            const uint64_t at = (uint64_t)((kk / 4) * (kRows * 128 >> 4) + (kk % 4) * 2);
+            mma_ss(d, a + at, b + at, kIdescS, (u > 0 || kk > 0) ? 1u : 0u);
+          }
+          if (last_use) mma_commit(empty((u0 + u) % kStages));
+          if (u == kUnits - 1) {
+            mma_commit(s_full(gs & 1));
+            if (last_use && cs.tile + 1 == cs.last) mma_commit(q_empty);
+          }
+        }
+        __syncwarp();
+      }
+      ++gs;
+      step(cs, false);
+    };
+    int gp = 0;
+    auto issue_pv = [&]() {
+      ok = mbar_wait(p_full(gp & 1), (gp >> 1) & 1, abort, p.dev_status);
+      ok = __all_sync(0xFFFFFFFFu, ok);
+      if (!ok) return;
+      const int u0 = NQ == 2 ? (2 * cp.x + 1) * kUnits : (2 * cp.x + 2) * kUnits;
+      const int seen = min(max(cp.end - cp.tile * kKeys, 1), kKeys);
+      const int steps = (seen + 15) / 16;  // of 16 keys
+      const uint32_t a = tmem + (uint32_t)(gp & 1) * kKeys;
+      const uint32_t o = tmem + 2 * kKeys + (uint32_t)(cp.row_tile * D);
+      const bool last_use = NQ == 1 || cp.row_tile == 1;
+#pragma unroll
+      for (int u = 0; u < kUnits; ++u) {
+        if (NQ == 1 || cp.row_tile == 0) wait_unit(u0 + u);
+        if (!ok) return;
+        tc_fence_after();
+        const uint64_t b = desc_v(ring + (uint32_t)((u0 + u) % kStages * L::kUnitBytes));
+        if (elect_one()) {
+          for (int kk = 0; kk < steps; ++kk)
+            mma_ts(o + (uint32_t)(u * L::kUnitDims), a + (uint32_t)(8 * kk), b + (uint64_t)(kk * (16 * 128 >> 4)), kIdescO,
+                   (cp.tile > cp.first || kk > 0) ? 1u : 0u);
+          if (last_use) mma_commit(empty((u0 + u) % kStages));
+          if (u == kUnits - 1) mma_commit(pv_done(gp & 1));
+        }
+        __syncwarp();
+      }
+      ++gp;
+      step(cp, true);
+    };
+    fetch(cs, false);
+    if (ok) fetch(cp, true);
+    for (int i = 0; i < 2 && ok && cs.rows; ++i) issue_s();
+    while (ok && cp.rows) {
+      issue_pv();
+      if (ok && cs.rows) issue_s();
+    }
+  } else if (warp < kSoftmaxWarps) {
+    // ------------------------------------------------------------------ softmax
+    if constexpr (NQ == 2) asm volatile("setmaxnreg.inc.sync.aligned.u32 208;");
+    constexpr int kCols = L::kCols, kOut = L::kOut;
+    const int group_of = warp >> 2;                                  // warpgroup
+    const int r = (warp & 3) * 32 + lane;                            // row of the tile
+    const uint32_t lanes = tmem + ((uint32_t)((warp & 3) * 32) << 16);
+    const int t = NQ == 2 ? group_of : 0;
+    const int c0 = NQ == 2 ? 0 : group_of * kCols;
+    const int token = r / p.group, g = r - token * p.group;
+    const uint32_t o_addr = lanes + 2 * kKeys + (uint32_t)(t * D + (NQ == 1 ? group_of * kOut : 0));
+    const float scale = p.scale;
+    const uint64_t scale2 = pack2(__float_as_uint(scale), __float_as_uint(scale));
+    // P V of the CTA's tile i is complete.  A barrier per buffer of S: the wait before last on
+    // one, two steps ago, is known to be over from S of this tile, so parities suffice.
+    auto wait_pv = [&](int i) {
+      return mbar_wait(pv_done(NQ == 2 ? t : i & 1), (NQ == 2 ? i : i >> 1) & 1, abort, p.dev_status);
+    };
+    bool ok = true;
+    int x = 0, exchanges = 0;
+    for (int count = 0;; ++count) {  // (NQ = 1: the warps leave together, at an exchange)
+      const int di = count % kDescs;
+      ok = ok && mbar_wait(item_full(di), (count / kDescs) & 1, abort, p.dev_status);
+      ok = NQ == 1 ? softmax_agree(ok) : (bool)__all_sync(0xFFFFFFFFu, ok);
+      if (!ok) break;
+      const Item it = items[di];
+      __syncwarp();
+      if (lane == 0) mbar_arrive(item_empty(di));
+      if (it.rows == 0) break;
+      const bool valid = token < per_tile && t * per_tile + token < it.rows;
+      const bool busy = __any_sync(0xFFFFFFFFu, valid);  // this warp has rows
+      const int limit = valid ? it.pos0 + t * per_tile + token + 1 : 0;  // keys that the row sees
+      float m = -INFINITY, l = 0.0f;
+      for (int tile = it.first; tile < it.last; ++tile, ++x) {
+        const int b = NQ == 2 ? t : x & 1;
+        ok = ok && mbar_wait(s_full(b), (NQ == 2 ? x : x >> 1) & 1, abort, p.dev_status);
+        if (NQ == 2) {
+          ok = __all_sync(0xFFFFFFFFu, ok);
+          if (!ok) break;
+        }
+        tc_fence_after();
+        const uint32_t s_addr = lanes + (uint32_t)(b * kKeys + c0);
+        uint32_t s[kCols / 32][32];
+        float top = -INFINITY;
+        if (busy) {
+#pragma unroll
+          for (int c = 0; c < kCols / 32; ++c) tmem_issue(s_addr + 32 * c, s[c]);
+#pragma unroll
+          for (int c = 0; c < kCols / 32; ++c) tmem_wait(s[c]);
+          if (p.negative) {
+#pragma unroll
+            for (int i = 0; i < kCols; ++i) s[i / 32][i % 32] ^= 0x80000000u;
+          }
+          const int seen = limit - tile * kKeys - c0;
+          if (__any_sync(0xFFFFFFFFu, seen < kCols)) {
+#pragma unroll
+            for (int i = 0; i < kCols; ++i)
+              if (i >= seen) s[i / 32][i % 32] = 0xFF800000u;
+          }
+          float top4[4] = {-INFINITY, -INFINITY, -INFINITY, -INFINITY};
+#pragma unroll
+          for (int i = 0; i < kCols; i += 8)
+#pragma unroll
+            for (int e = 0; e < 4; ++e)
+              top4[e] = fmaxf(top4[e], fmaxf(__uint_as_float(s[(i + 2 * e) / 32][(i + 2 * e) % 32]),
+                                             __uint_as_float(s[(i + 2 * e + 1) / 32][(i + 2 * e + 1) % 32])));
+          top = fmaxf(fmaxf(top4[0], top4[1]), fmaxf(top4[2], top4[3]));
+        }
+        if constexpr (NQ == 1) {
+          float* at = xch + (exchanges & 1) * 2 * kRows + r;
+          ++exchanges;
+          at[group_of * kRows] = top;
+          ok = softmax_agree(ok);
+          if (!ok) break;
+          top = fmaxf(top, at[(group_of ^ 1) * kRows]);
+        }
+        if (busy) {
+          // the reference maximum: raised for the whole warp once a row needs it
+          const float raised = fmaxf(m, top);
+          const bool grow = m == -INFINITY ? raised > m : (raised - m) * scale > kRescale;
+          if (__any_sync(0xFFFFFFFFu, grow)) {
+            const float keep = m == -INFINITY ? 0.0f : exp2_approx((m - raised) * scale);
+            l *= keep;
+            m = raised;
+            if (tile > it.first) {
+              ok = ok && wait_pv(x - 1);
+              ok = __all_sync(0xFFFFFFFFu, ok);
+              tc_fence_after();
+              const uint64_t keep2 = pack2(__float_as_uint(keep), __float_as_uint(keep));
+#pragma unroll 1
+              for (int c = 0; c < kOut; c += 16) {
+                uint32_t o[16];
+                tmem_issue(o_addr + c, o);
+                tmem_wait(o);
+#pragma unroll
+                for (int i = 0; i < 16; i += 2) {
+                  float lo, hi;
+                  unpack2(fma2(pack2(o[i], o[i + 1]), keep2, 0ull), lo, hi);
+                  o[i] = __float_as_uint(lo);
+                  o[i + 1] = __float_as_uint(hi);
+                }
+                tmem_store(o_addr + c, o);
+              }
+            }
+          }
+          const float shift = m == -INFINITY ? 0.0f : -m * scale;
+          const uint64_t shift2 = pack2(__float_as_uint(shift), __float_as_uint(shift));
+          uint64_t sum[2] = {0ull, 0ull};
+          const uint32_t p_addr = lanes + (uint32_t)(b * kKeys + c0 / 2);
+#pragma unroll
+          for (int c = 0; c < kCols / 32; ++c) {
+            uint32_t w[16];
+#pragma unroll
+            for (int i = 0; i < 16; ++i) {
+              float lo, hi;
+              unpack2(fma2(pack2(s[c][2 * i], s[c][2 * i + 1]), scale2, shift2), lo, hi);
+              lo = exp2_approx(lo);
+              hi = exp2_approx(hi);
+              sum[i & 1] = add2(sum[i & 1], pack2(__float_as_uint(lo), __float_as_uint(hi)));
+              w[i] = to_bf16x2(lo, hi);
+            }
+            tmem_store(p_addr + 16 * c, w);
+          }
+          float s0f, s1f;
+          unpack2(add2(sum[0], sum[1]), s0f, s1f);
+          l += s0f + s1f;
+          tmem_store_wait();
+        }
+        // Values behind the last key that any row sees may be anything: zeros for those of
+        // them that the last 16 keys of P V take in.
+        if (tile * kKeys + kKeys > it.end && (NQ == 1 || t == 0)) {
+          const int from = max(it.end - tile * kKeys, 0), to = (max(from, 1) + 15) / 16 * 16;
+          const int u0 = NQ == 2 ? (2 * x + 1) * kUnits : (2 * x + 2) * kUnits;
+          const int threads = NQ == 2 ? 128 : 256, me = threadIdx.x % threads;
+          // A stage's barrier tells this load from the one before only once that one is complete:
+          // it is S's or an earlier tile's, but with two units a tile and five stages V's of the
+          // tile before.
+          static_assert(kUnits == 1 || NQ == 1, "stages");
+          if (kUnits == 2 && x > 0) ok = ok && wait_pv(x - 1);
+          for (int u = 0; u < kUnits; ++u) {
+            ok = ok && mbar_wait(full((u0 + u) % kStages), ((u0 + u) / kStages) & 1, abort, p.dev_status);
+            unsigned char* v = ring_ptr + (u0 + u) % kStages * L::kUnitBytes;
+            if (ok)
+              for (int i = from * 8 * kBlocks + me; i < to * 8 * kBlocks; i += threads) {
+                const int key = i / (8 * kBlocks), piece = i % (8 * kBlocks);
+                *reinterpret_cast<uint4*>(v + piece / 8 * (kKeys * 128) + key * 128 + piece % 8 * 16) = make_uint4(0, 0, 0, 0);
+              }
+          }
+          fence_proxy_async();
+        }
+        tc_fence_before();
+        __syncwarp();
+        if (lane == 0) mbar_arrive(p_full(b));
+      }
+      if (NQ == 2 && !ok) break;
+      // the part's end: O / l to the output, or (m, l, O) to the workspace
+      if constexpr (NQ == 1) {
+        float* at = xch + (exchanges & 1) * 2 * kRows + r;
+        ++exchanges;
+        at[group_of * kRows] = l;
+        ok = softmax_agree(ok);
+        if (!ok) break;
+        l += at[(group_of ^ 1) * kRows];
+      }
+      ok = wait_pv(x - 1);
+      ok = __all_sync(0xFFFFFFFFu, ok);
+      tc_fence_after();
+      if (busy && ok) {
+        float* part = nullptr;
+        __nv_bfloat16* out = nullptr;
+        float norm = 1.0f;
+        if (it.slot < 0) {
+          norm = 1.0f / l;
+          out = p.out + (int64_t)(it.row0 + t * per_tile + token) * p.ld_token + (it.head * p.group + g) * p.ld_head +
+                (NQ == 1 ? group_of * kOut : 0);
+        } else {
+          float* slot = reinterpret_cast<float*>(p.ws + kRecordBytes) + (2 * (int64_t)blockIdx.x + it.slot) * slot_floats(D, NQ);
+          const int row = t * kRows + r;
+          if (valid && (NQ == 2 || group_of == 0)) *reinterpret_cast<float2*>(slot + 2 * row) = make_float2(m, l);
+          part = slot + 2 * NQ * kRows + (int64_t)row * D + (NQ == 1 ? group_of * kOut : 0);
+        }
+#pragma unroll 1
+        for (int c = 0; c < kOut; c += 32) {
+          uint32_t o[32];
+          tmem_issue(o_addr + c, o);
+          tmem_wait(o);
+          if (!valid) continue;
+          if (part != nullptr) {
+#pragma unroll
+            for (int i = 0; i < 32; i += 4)
+              *reinterpret_cast<uint4*>(part + c + i) = make_uint4(o[i], o[i + 1], o[i + 2], o[i + 3]);
+          } else {
+#pragma unroll
+            for (int i = 0; i < 32; i += 8) {
+              uint32_t w[4];
+#pragma unroll
+              for (int e = 0; e < 4; ++e) {
+                // (a row that sees nothing: 0, whatever O holds)
+                const float lo = l != 0.0f ? __uint_as_float(o[i + 2 * e]) * norm : 0.0f;
+                const float hi = l != 0.0f ? __uint_as_float(o[i + 2 * e + 1]) * norm : 0.0f;
+                w[e] = to_bf16x2(lo, hi);
+              }
+              *reinterpret_cast<uint4*>(out + c + i) = make_uint4(w[0], w[1], w[2], w[3]);
+            }
+          }
+        }
+      }
+    }
   }
-  __nv_bfloat16* out = (__nv_bfloat16*)p.out.data + row * p.out.ld_token + head * p.out.ld_head;
-  for (int e = 0; e < E; ++e) out[lane + 32 * e] = __float2bfloat16_rn(l > 0.0f ? o[e] / l : 0.0f);
+  tc_fence_before();
+  __syncthreads();
+  if (*abort) {
+    // A wait ran out: what is in flight lands (bounded) before TMEM and shared memory go.
+    if (warp == 9 && lane == 0)
+      for (int u = issued > kStages ? issued - kStages : 0; u < issued; ++u)
+        mbar_drain(full(u % kStages), (uint32_t)(u / kStages) & 1u, p.dev_status);
+    if (warp == 10 && lane == 0 && q_issued > 0) mbar_drain(q_full, (uint32_t)(q_issued - 1) & 1u, p.dev_status);
+    if (warp == 8 && elect_one()) {
+      mma_commit(drain_bar);
+      mbar_drain(drain_bar, 0u, p.dev_status);
+    }
+    __syncthreads();
+  }
+  if (warp == 8) {
+    __syncwarp();
+    tc_fence_after();
+    asm volatile("tcgen05.dealloc.cta_group::1.sync.aligned.b32 %0, %1;" ::"r"(tmem), "r"(512) : "memory");
+  }
+}
+
+// ------------------------------------------------------------------- join
+//
+// One block per (CTA whose share begins an item that others finish, group of rows): a warp
+// per row and slice of the parts, then over the slices, all in the order of the keys.
+
+constexpr int kJoinWarps = 8;
+
+template <int D, int NQ>
+__global__ void __launch_bounds__(32 * kJoinWarps) attention_join_kernel(const __grid_constant__ Params p) {
+  constexpr int E = D / 32;  // of a lane
+  __shared__ float acc[kJoinWarps][D];
+  __shared__ float2 stats[kJoinWarps];
+  nvfp4::wait_for_previous_kernel();
+  const int c = blockIdx.x, warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+  const Record rec = *reinterpret_cast<const Record*>(p.ws + (size_t)c * 64);
+  if (rec.parts <= 0) return;
+  const int per_tile = kRows / p.group, rows = rec.rows * p.group;
+  const float* slots = reinterpret_cast<const float*>(p.ws + kRecordBytes);
+  const int first = rec.parts * warp / kJoinWarps, last = rec.parts * (warp + 1) / kJoinWarps;
+  for (int i = blockIdx.y; i < rows; i += gridDim.y) {
+    const int token = i / p.group, g = i - token * p.group;
+    const int row = token / per_tile * kRows + token % per_tile * p.group + g;
+    float m = -INFINITY, l = 0.0f, o[E];
+#pragma unroll
+    for (int e = 0; e < E; ++e) o[e] = 0.0f;
+    for (int k = first; k < last; ++k) {
+      const float* slot = slots + (2 * (int64_t)(c + k) + (k == 0 ? 1 : 0)) * slot_floats(D, NQ);
+      const float2 ml = *reinterpret_cast<const float2*>(slot + 2 * row);
+      float v[E];
+#pragma unroll
+      for (int e = 0; e < E; ++e) v[e] = slot[2 * NQ * kRows + (int64_t)row * D + lane + 32 * e];
+      if (ml.y == 0.0f) continue;  // (sees none of this part's keys)
+      const float top = fmaxf(m, ml.x);
+      const float a = m == -INFINITY ? 0.0f : exp2_approx((m - top) * p.scale), b = exp2_approx((ml.x - top) * p.scale);
+      m = top;
+      l = l * a + ml.y * b;
+#pragma unroll
+      for (int e = 0; e < E; ++e) o[e] = o[e] * a + v[e] * b;
+    }
+#pragma unroll
+    for (int e = 0; e < E; ++e) acc[warp][lane + 32 * e] = o[e];
+    if (lane == 0) stats[warp] = make_float2(m, l);
+    __syncthreads();
+    if (threadIdx.x < D / 2) {
+      float top = -INFINITY, total = 0.0f;
+      float2 sum = make_float2(0.0f, 0.0f);
+#pragma unroll
+      for (int w = 0; w < kJoinWarps; ++w) top = fmaxf(top, stats[w].x);
+#pragma unroll
+      for (int w = 0; w < kJoinWarps; ++w) {
+        if (stats[w].y == 0.0f) continue;
+        const float b = exp2_approx((stats[w].x - top) * p.scale);
+        total += stats[w].y * b;
+        const float2 v = *reinterpret_cast<const float2*>(&acc[w][2 * threadIdx.x]);
+        sum.x += v.x * b;
+        sum.y += v.y * b;
+      }
+      const float norm = 1.0f / total;
+      __nv_bfloat16* out = p.out + (int64_t)(rec.row0 + token) * p.ld_token + (rec.head * p.group + g) * p.ld_head;
+      reinterpret_cast<uint32_t*>(out)[threadIdx.x] = total != 0.0f ? to_bf16x2(sum.x * norm, sum.y * norm) : 0u;
+    }
+    __syncthreads();
+  }
+}
+
+// One map for the caches and for packed keys (one page of all tokens).
+bool encode_kv(CUtensorMap* map, const kv_pages& x, const paged_attention_input& in, int box) {
+  const cuuint64_t dims[4] = {(cuuint64_t)in.dim, (cuuint64_t)in.kv_heads, (cuuint64_t)in.page_size, (cuuint64_t)in.pages};
+  const cuuint64_t strides[3] = {(cuuint64_t)x.ld_head * 2, (cuuint64_t)x.ld_token * 2,
+                                 in.pages > 1 ? (cuuint64_t)x.ld_page * 2 : 16};
+  const cuuint32_t boxes[4] = {64, 1, (cuuint32_t)box, 1};
+  const cuuint32_t each[4] = {1, 1, 1, 1};
+  return nvfp4::encode_tiled(map, CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, 4, x.data, dims, strides, boxes, each,
+                             CU_TENSOR_MAP_SWIZZLE_128B);
+}
+
+template <int D, int NQ>
+int launch(const paged_attention_input& in, const attn_rows& out, void* workspace, int32_t* dev_status,
+           cudaStream_t stream) {
+  using L = Tile<D, NQ>;
+  Params p;
+  p.cu = in.cu;
+  p.kv_lens = in.block_table != nullptr ? in.kv_lens : nullptr;
+  p.table = in.block_table;
+  p.ld_table = in.ld_table;
+  const int64_t capacity = in.max_pages * in.page_size;
+  p.capacity = capacity < 0x7FFFFFFF ? capacity : 0x7FFFFFFF;
+  p.tokens = (int)in.tokens;
+  p.batch = (int)in.batch;
+  p.kv_heads = (int)in.kv_heads;
+  p.group = (int)(in.heads / in.kv_heads);
+  p.page_size = (int)in.page_size;
+  p.pages = (int)in.pages;
+  p.box = kKeys;
+  if (in.block_table != nullptr)
+    while (in.page_size % p.box != 0) p.box /= 2;
+  p.negative = in.scale < 0.0f;
+  p.scale = (in.scale < 0.0f ? -in.scale : in.scale) * kLog2e;
+  if (!(p.scale >= 1e-37f)) p.scale = 1e-37f;  // (a score that is masked stays so: 0 times -inf is not a number)
+  p.out = static_cast<__nv_bfloat16*>(out.data);
+  p.ld_token = out.ld_token;
+  p.ld_head = out.ld_head;
+  p.ws = static_cast<unsigned char*>(workspace);
+  p.dev_status = dev_status;
+
+  CUtensorMap mq, mk, mv;
+  const cuuint64_t dims[4] = {(cuuint64_t)D, (cuuint64_t)p.group, (cuuint64_t)p.kv_heads, (cuuint64_t)in.tokens};
+  const cuuint64_t strides[3] = {(cuuint64_t)in.q.ld_head * 2, (cuuint64_t)in.q.ld_head * p.group * 2,
+                                 (cuuint64_t)in.q.ld_token * 2};
+  const cuuint32_t boxes[4] = {64, (cuuint32_t)p.group, 1, (cuuint32_t)(kRows / p.group)};
+  const cuuint32_t each[4] = {1, 1, 1, 1};
+  if (!nvfp4::encode_tiled(&mq, CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, 4, in.q.data, dims, strides, boxes, each,
+                           CU_TENSOR_MAP_SWIZZLE_128B) ||
+      !encode_kv(&mk, in.k, in, p.box) || !encode_kv(&mv, in.v, in, p.box))
+    return NVFP4_ERR_CUDA;
+  const void* kern = (const void*)attention_kernel<D, NQ>;
+  if (nvfp4::occupancy(kern, kThreads, L::kSmemBytes) < 1) return NVFP4_ERR_CUDA;
+  const int sms = nvfp4::sm_count();
+  const unsigned grid = (unsigned)(sms < ATTENTION_MAX_CTAS ? sms : ATTENTION_MAX_CTAS);
+  void* args[] = {&mq, &mk, &mv, &p};
+  if (nvfp4::launch_dependent(kern, dim3(grid), dim3(kThreads), L::kSmemBytes, stream, 1, args) != cudaSuccess)
+    return NVFP4_ERR_CUDA;
+  void* join_args[] = {&p};
+  if (nvfp4::launch_dependent((const void*)attention_join_kernel<D, NQ>, dim3(grid, 8), dim3(32 * kJoinWarps), 0, stream, 1,
+                              join_args) != cudaSuccess)
+    return NVFP4_ERR_CUDA;
+  return NVFP4_OK;
 }
 
 }  // namespace
 
 int launch_attention(const paged_attention_input* in, const attn_rows* out, void* workspace, int32_t* dev_status,
                      cudaStream_t stream) {
-  (void)workspace;
-  Params p{*in, *out, dev_status};
-  const int64_t blocks = nvfp4::cdiv(in->tokens * in->heads, kThreads / 32);
-  if (blocks > 0x7FFFFFFF) return NVFP4_ERR_SHAPE;
-  const void* kern = in->dim == 64 ? (const void*)attention_kernel<64>
-                                   : in->dim == 128 ? (const void*)attention_kernel<128> : (const void*)attention_kernel<256>;
-  void* args[] = {&p};
-  return nvfp4::launch_dependent(kern, dim3((unsigned)blocks), dim3(kThreads), 0, stream, 1, args) == cudaSuccess
-             ? NVFP4_OK
-             : NVFP4_ERR_CUDA;
+  // Two tiles of rows an item where sequences bring more than one tile's on average.
+  const int64_t rows = in->tokens * (in->heads / in->kv_heads);
+  const bool two = in->dim <= 128 && rows > kRows * in->batch;
+  switch (in->dim) {
+    case 64: return two ? launch<64, 2>(*in, *out, workspace, dev_status, stream)
+                        : launch<64, 1>(*in, *out, workspace, dev_status, stream);
+    case 128: return two ? launch<128, 2>(*in, *out, workspace, dev_status, stream)
+                         : launch<128, 1>(*in, *out, workspace, dev_status, stream);
+    default: return launch<256, 1>(*in, *out, workspace, dev_status, stream);
+  }
 }
