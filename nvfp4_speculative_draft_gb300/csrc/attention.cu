@@ -33,8 +33,9 @@
 // a second kernel joins them in the order of the keys.  The borders depend on the lengths
 // alone, so results do not depend on timing.
 //
-// Keys that no row of an item sees are not loaded (zeros instead), those that some row
-// does not see get weight 0 by selection.
+// Keys that a row does not see get weight 0 by selection, and P V stops at the last one that
+// some row of the item sees (rounded up to 16, values behind it zeroed): what lies there, in
+// other sequences or unused slots, does not matter.
 #include <cuda_bf16.h>
 
 #include "tc.cuh"
@@ -81,7 +82,8 @@ struct Params {
   const int32_t* table;
   int64_t ld_table, capacity;  // tokens of a table row
   int tokens, batch, kv_heads, group;
-  int page_size, box;          // tokens of a page and of a TMA box
+  int page_size, page_shift;   // tokens of a page; log2 of it, or -1
+  int box;                     // tokens of a TMA box
   int pages;
   float scale;                 // |scale| log2 e, never 0
   int negative;
@@ -113,19 +115,20 @@ struct Record {
 __host__ __device__ constexpr int64_t slot_floats(int d, int nq) { return (int64_t)nq * kRows * (d + 2); }
 constexpr size_t kRecordBytes = (size_t)ATTENTION_MAX_CTAS * 64;
 
-__device__ __forceinline__ Sequence sequence(const Params& p, int s) {
+__device__ __forceinline__ Sequence sequence(const Params& p, int s, bool* consistent = nullptr) {
   const int a = ld_ro(p.cu + s), b = ld_ro(p.cu + s + 1);
+  const int64_t cached = p.kv_lens != nullptr ? ld_ro(p.kv_lens + s) : 0;
   Sequence q;
   q.begin = min(max(a, 0), p.tokens);
   q.n = max(min(max(b, 0), p.tokens) - q.begin, 0);
-  q.len = q.n;
-  if (p.kv_lens != nullptr) q.len = (int)min((int64_t)max(ld_ro(p.kv_lens + s), 0), p.capacity);
+  q.len = p.kv_lens != nullptr ? (int)min(max(cached, (int64_t)0), p.capacity) : q.n;
   q.off = q.len - q.n;
+  if (consistent != nullptr) *consistent = a >= 0 && b <= p.tokens && a <= b && cached <= p.capacity;
   return q;
 }
-__device__ __forceinline__ bool consistent(const Params& p, int s) {
-  const int a = ld_ro(p.cu + s), b = ld_ro(p.cu + s + 1);
-  return a >= 0 && b <= p.tokens && a <= b && (p.kv_lens == nullptr || ld_ro(p.kv_lens + s) <= p.capacity);
+// (64-bit division takes several times a 32-bit one's time)
+__device__ __forceinline__ int64_t quotient(int64_t a, int64_t b) {
+  return ((a | b) >> 32) == 0 ? (int64_t)((uint32_t)a / (uint32_t)b) : a / b;
 }
 
 // The line: item t of a (sequence, head) starts `before(t)` behind its head's start.
@@ -145,12 +148,21 @@ struct Line {
   __device__ __forceinline__ int64_t before(int64_t t) const { return t * base + per * (t * (t - 1) / 2); }
 };
 
-__device__ __forceinline__ void tma_load_4d(uint32_t dst, const CUtensorMap* map, int c0, int c1, int c2, int c3,
-                                            uint32_t bar) {
+// TMA and MMA instructions are issued by one lane of a converged warp, by predicate and not
+// by a branch: their operands are then uniform values, which these instructions take as they
+// are (issued behind a branch, or by a lane each, one takes 80 to 110 cycles).
+__device__ __forceinline__ void tma_load_4d(uint32_t lead, uint32_t dst, const CUtensorMap* map, int c0, int c1, int c2,
+                                            int c3, uint32_t bar) {
   asm volatile(
-      "cp.async.bulk.tensor.4d.shared::cluster.global.mbarrier::complete_tx::bytes"
-      " [%0], [%1, {%2, %3, %4, %5}], [%6];" ::"r"(dst),
-      "l"(reinterpret_cast<uint64_t>(map)), "r"(c0), "r"(c1), "r"(c2), "r"(c3), "r"(bar)
+      "{\n .reg .pred l;\n setp.ne.b32 l, %7, 0;\n"
+      " @l cp.async.bulk.tensor.4d.shared::cluster.global.mbarrier::complete_tx::bytes [%0], [%1, {%2, %3, %4, %5}], [%6];\n}" ::"r"(dst),
+      "l"(reinterpret_cast<uint64_t>(map)), "r"(c0), "r"(c1), "r"(c2), "r"(c3), "r"(bar), "r"(lead)
+      : "memory");
+}
+__device__ __forceinline__ void commit(uint32_t lead, uint32_t bar) {
+  asm volatile(
+      "{\n .reg .pred l;\n setp.ne.b32 l, %1, 0;\n"
+      " @l tcgen05.commit.cta_group::1.mbarrier::arrive::one.shared::cluster.b64 [%0];\n}" ::"r"(bar), "r"(lead)
       : "memory");
 }
 // kind::f16 with BF16 operands, D = F32; bit 16: B is N-major in shared memory.
@@ -158,25 +170,48 @@ constexpr uint32_t idesc_bf16(int n, bool b_transposed) {
   return (1u << 4) | (1u << 7) | (1u << 10) | ((b_transposed ? 1u : 0u) << 16) | ((uint32_t)(n >> 3) << 17) |
          ((uint32_t)(kRows >> 4) << 24);
 }
-__device__ __forceinline__ void mma_ss(uint32_t d, uint64_t a, uint64_t b, uint32_t idesc, uint32_t accumulate) {
+// Shared-memory operands, lower word of the descriptor: start address >> 4, leading offset
+// (V as B: 64-element columns of 128 keys, 16 KB apart); upper word: 8-row groups 1 KB apart,
+// version 1, 128-byte swizzle.
+constexpr uint32_t kDescHigh = (1024u >> 4) | (1u << 14) | (2u << 29);
+__device__ __forceinline__ uint32_t desc_low(uint32_t addr) { return ((addr >> 4) & 0x3FFFu) | (1u << 16); }
+__device__ __forceinline__ uint32_t desc_low_v(uint32_t addr) {
+  return ((addr >> 4) & 0x3FFFu) | ((uint32_t)(kKeys * 128 >> 4) << 16);
+}
+// Four MMAs along a swizzled column: 64 elements of K, 32 bytes each apart.
+__device__ __forceinline__ void mma_ss4(uint32_t lead, uint32_t d, uint32_t a, uint32_t b, uint32_t idesc,
+                                        uint32_t accumulate) {
   asm volatile(
-      "{\n .reg .pred p;\n setp.ne.b32 p, %4, 0;\n"
-      " tcgen05.mma.cta_group::1.kind::f16 [%0], %1, %2, %3, p;\n}" ::"r"(d),
-      "l"(a), "l"(b), "r"(idesc), "r"(accumulate)
+      "{\n .reg .pred l, p, q;\n .reg .b32 x, y;\n .reg .b64 a, b;\n"
+      " setp.ne.b32 l, %0, 0;\n setp.ne.b32 p, %5, 0;\n setp.eq.b32 q, 0, 0;\n"
+      " mov.b64 a, {%2, %6};\n mov.b64 b, {%3, %6};\n"
+      " @l tcgen05.mma.cta_group::1.kind::f16 [%1], a, b, %4, p;\n"
+      " add.u32 x, %2, 2;\n add.u32 y, %3, 2;\n mov.b64 a, {x, %6};\n mov.b64 b, {y, %6};\n"
+      " @l tcgen05.mma.cta_group::1.kind::f16 [%1], a, b, %4, q;\n"
+      " add.u32 x, %2, 4;\n add.u32 y, %3, 4;\n mov.b64 a, {x, %6};\n mov.b64 b, {y, %6};\n"
+      " @l tcgen05.mma.cta_group::1.kind::f16 [%1], a, b, %4, q;\n"
+      " add.u32 x, %2, 6;\n add.u32 y, %3, 6;\n mov.b64 a, {x, %6};\n mov.b64 b, {y, %6};\n"
+      " @l tcgen05.mma.cta_group::1.kind::f16 [%1], a, b, %4, q;\n}" ::"r"(lead),
+      "r"(d), "r"(a), "r"(b), "r"(idesc), "r"(accumulate), "r"(kDescHigh)
       : "memory");
 }
-__device__ __forceinline__ void mma_ts(uint32_t d, uint32_t a, uint64_t b, uint32_t idesc, uint32_t accumulate) {
+// Four MMAs along 64 keys: P in TMEM, 16 keys in 8 columns; V 16 rows of 128 bytes apart.  Of
+// them the first `steps`.
+__device__ __forceinline__ void mma_ts4(uint32_t lead, uint32_t d, uint32_t a, uint32_t b, uint32_t idesc,
+                                        uint32_t accumulate, int steps) {
   asm volatile(
-      "{\n .reg .pred p;\n setp.ne.b32 p, %4, 0;\n"
-      " tcgen05.mma.cta_group::1.kind::f16 [%0], [%1], %2, %3, p;\n}" ::"r"(d),
-      "r"(a), "l"(b), "r"(idesc), "r"(accumulate)
+      "{\n .reg .pred l, m, p, q;\n .reg .b32 x, y;\n .reg .b64 b;\n"
+      " setp.ne.b32 l, %0, 0;\n setp.ne.b32 p, %5, 0;\n setp.eq.b32 q, 0, 0;\n"
+      " setp.gt.and.s32 m, %7, 0, l;\n mov.b64 b, {%3, %6};\n"
+      " @m tcgen05.mma.cta_group::1.kind::f16 [%1], [%2], b, %4, p;\n"
+      " setp.gt.and.s32 m, %7, 1, l;\n add.u32 x, %2, 8;\n add.u32 y, %3, 128;\n mov.b64 b, {y, %6};\n"
+      " @m tcgen05.mma.cta_group::1.kind::f16 [%1], [x], b, %4, q;\n"
+      " setp.gt.and.s32 m, %7, 2, l;\n add.u32 x, %2, 16;\n add.u32 y, %3, 256;\n mov.b64 b, {y, %6};\n"
+      " @m tcgen05.mma.cta_group::1.kind::f16 [%1], [x], b, %4, q;\n"
+      " setp.gt.and.s32 m, %7, 3, l;\n add.u32 x, %2, 24;\n add.u32 y, %3, 384;\n mov.b64 b, {y, %6};\n"
+      " @m tcgen05.mma.cta_group::1.kind::f16 [%1], [x], b, %4, q;\n}" ::"r"(lead),
+      "r"(d), "r"(a), "r"(b), "r"(idesc), "r"(accumulate), "r"(kDescHigh), "r"(steps)
       : "memory");
-}
-// V as B: 64-element columns of 128 keys 16 KB apart (leading), 8-key groups 1 KB apart
-// (stride), 128-byte swizzle.
-__device__ __forceinline__ uint64_t desc_v(uint32_t addr) {
-  return (uint64_t)((addr >> 4) & 0x3FFFu) | ((uint64_t)(kKeys * 128 >> 4) << 16) | ((uint64_t)(1024 >> 4) << 32) |
-         ((uint64_t)1 << 46) | ((uint64_t)2 << 61);
 }
 __device__ __forceinline__ void tmem_store(uint32_t taddr, const uint32_t (&v)[16]) {
   asm volatile(
@@ -190,6 +225,11 @@ __device__ __forceinline__ float exp2_approx(float x) {  // 2^-22 relative; 0 fo
   float y;
   asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"(x));
   return y;
+}
+__device__ __forceinline__ float max3(float a, float b, float c) {
+  float d;
+  asm("max.f32 %0, %1, %2, %3;" : "=f"(d) : "f"(a), "f"(b), "f"(c));
+  return d;
 }
 __device__ __forceinline__ uint64_t fma2(uint64_t a, uint64_t b, uint64_t c) {
   uint64_t d;
@@ -205,6 +245,9 @@ __device__ __forceinline__ uint32_t to_bf16x2(float lo, float hi) {
   const __nv_bfloat162 b = __floats2bfloat162_rn(lo, hi);
   return *reinterpret_cast<const uint32_t*>(&b);
 }
+// A value that all lanes hold, so that the compiler knows: what is computed from it goes to
+// the tensor core without a detour through each lane's registers.
+__device__ __forceinline__ int uniform(int x) { return __shfl_sync(0xFFFFFFFFu, x, 0); }
 // All softmax threads: true if `ok` holds for all of them (so they leave together).
 __device__ __forceinline__ bool softmax_agree(bool ok) {
   uint32_t r;
@@ -246,7 +289,9 @@ attention_kernel(const __grid_constant__ CUtensorMap map_q, const __grid_constan
   uint32_t* const tmem_slot = reinterpret_cast<uint32_t*>(sums + kWarps + 1);
   volatile uint32_t* abort = tmem_slot + 1;
   int& start_seq = reinterpret_cast<int*>(tmem_slot)[2];
-  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+  // (uniform: a role's code is then known not to diverge, and its instructions' addresses and
+  // descriptors stay in uniform registers)
+  const int warp = uniform((int)threadIdx.x >> 5), lane = threadIdx.x & 31;
 
   if (q_smem & 1023u) {  // (the swizzled tiles need it; the declaration asks for it)
     nvfp4::report(p.dev_status, NVFP4_ERR_ALIGN);
@@ -288,31 +333,38 @@ attention_kernel(const __grid_constant__ CUtensorMap map_q, const __grid_constan
   const int s0 = min(p.batch, (int)threadIdx.x * run), s1 = min(p.batch, s0 + run);
   int64_t mine = 0;
   for (int s = s0; s < s1; ++s) {
-    mine += p.kv_heads * Line<NQ>(sequence(p, s), p.group).length;
-    if (blockIdx.x == 0 && !consistent(p, s)) nvfp4::report(p.dev_status, NVFP4_ERR_INDEX);
+    bool consistent;
+    mine += p.kv_heads * Line<NQ>(sequence(p, s, &consistent), p.group).length;
+    if (blockIdx.x == 0 && !consistent) nvfp4::report(p.dev_status, NVFP4_ERR_INDEX);
   }
   int64_t upto = mine;
+  if (p.batch > 1) {
 #pragma unroll
-  for (int d = 1; d < 32; d <<= 1) {
-    const int64_t o = __shfl_up_sync(0xFFFFFFFFu, upto, d);
-    if (lane >= d) upto += o;
+    for (int d = 1; d < 32; d <<= 1) {
+      const int64_t o = __shfl_up_sync(0xFFFFFFFFu, upto, d);
+      if (lane >= d) upto += o;
+    }
   }
-  if (lane == 31) sums[warp] = upto;
+  if (lane == (p.batch > 1 ? 31 : 0)) sums[warp] = upto;
   if (threadIdx.x == 0) start_seq = p.batch;
   tc_fence_before();
   __syncthreads();
   tc_fence_after();
-  const uint32_t tmem = *tmem_slot;
+  // all of the SM's columns: they start at 0 (a constant for the MMAs' addresses)
+  constexpr uint32_t tmem = 0;
+  if (*tmem_slot != tmem) nvfp4::report(p.dev_status, NVFP4_ERR_CUDA);
   int64_t total = 0;
 #pragma unroll
   for (int w = 0; w < kWarps; ++w) {
     if (w == warp) upto += total;
     total += sums[w];
   }
+  // total = shares * each + rest: the first `rest` shares are one longer
   const int64_t wanted = total / kMinShare;
   const int shares = (int)(wanted < 1 ? 1 : wanted < gridDim.x ? wanted : gridDim.x);
-  const int64_t x0 = (int)blockIdx.x < shares ? total * blockIdx.x / shares : total;
-  const int64_t x1 = (int)blockIdx.x < shares ? total * (blockIdx.x + 1) / shares : total;
+  const int64_t each = quotient(total, shares), rest = total - each * shares;
+  auto border = [&](int c) -> int64_t { return c < shares ? c * each + min((int64_t)c, rest) : total; };
+  const int64_t x0 = border((int)blockIdx.x), x1 = border((int)blockIdx.x + 1);
   if (x0 < x1 && upto > x0 && upto - mine <= x0) {
     int64_t at = upto - mine;
     int s = s0;
@@ -328,16 +380,15 @@ attention_kernel(const __grid_constant__ CUtensorMap map_q, const __grid_constan
 
   const int per_tile = kRows / p.group;  // tokens of a tile of rows
   int issued = 0, q_issued = 0;          // units and Q loads issued (TMA warps)
+  const uint32_t lead = elect_one();     // the lane that issues for a warp
 
   // NQ = 2: the softmax's threads take registers that the others have no use for
   // (256 x 208 + 128 x 88 = 384 x 168, what the block was launched with).
   if (NQ == 2 && warp >= kSoftmaxWarps) asm volatile("setmaxnreg.dec.sync.aligned.u32 88;");
   if (warp == 9) {
     // ------------------------------------------------- schedule, K and V loads
-    // (all lanes together; a lane per box of a unit issues)
+    // (all lanes together; lane i knows the page of a tile's box i)
     const int boxes = kKeys / p.box;
-    const int sub = lane / kBlocks, block = lane % kBlocks;
-    const bool loads = sub < boxes;
     bool ok = true;
     int seq = start_seq, head = 0, t = 0;
     Sequence q{}, next_q{};
@@ -345,7 +396,7 @@ attention_kernel(const __grid_constant__ CUtensorMap map_q, const __grid_constan
     if (seq < p.batch) {
       q = sequence(p, seq);
       const Line<NQ> line(q, p.group);
-      head = (int)((x0 - start_at) / line.length);
+      head = (int)quotient(x0 - start_at, line.length);
       head_at = start_at + head * line.length;
       int lo = 0, hi = line.items;  // the item that x0 lies in
       while (hi - lo > 1) {
@@ -402,51 +453,67 @@ attention_kernel(const __grid_constant__ CUtensorMap map_q, const __grid_constan
         r.row = seq * p.ld_table;
         r.begin = q.begin;
         if (a == 0 && b < tiles) {
-          const int64_t last_tile = at + (int64_t)(tiles - 1) * kKeys;
-          r.record = (int)(((last_tile + 1) * shares - 1) / total) - (int)blockIdx.x + 1;
+          const int64_t last_tile = at + (int64_t)(tiles - 1) * kKeys, longer = rest * (each + 1);
+          const int owner = (int)(last_tile < longer ? quotient(last_tile, each + 1) : rest + quotient(last_tile - longer, each));
+          r.record = owner - (int)blockIdx.x + 1;
         }
         break;
       }
       return r;
     };
-    // The page of this lane's box of a tile; past the cache (zeros) where no row sees it.
-    auto page_of = [&](const Part& r, int tile) -> int {
-      const int j = tile * kKeys + sub * p.box;
-      if (!loads || j >= r.it.end) return p.pages;
-      if (p.table == nullptr) return 0;
-      const int id = ld_ro(p.table + r.row + j / p.page_size);
-      if (id < 0 || id >= p.pages) {
-        nvfp4::report(p.dev_status, NVFP4_ERR_INDEX);
-        return p.pages;
-      }
-      return id;
+    // Where this lane's box of a tile lies: its page, and its first token there; how many boxes
+    // some row sees.  The others are not loaded: their scores are masked whatever they are, and
+    // P V stops before them.  (Boxes outside the cache, read as zeros, take the TMA unit about 1 us
+    // each.)
+    struct Place {
+      int page, token, count;
+    };
+    auto place_of = [&](const Part& r, int tile) -> Place {
+      const int j = tile * kKeys + lane * p.box;
+      const int count = min(max((r.it.end - tile * kKeys + p.box - 1) / p.box, 0), boxes);
+      if (lane >= count) return Place{0, 0, count};
+      if (p.table == nullptr) return Place{0, r.begin + j, count};
+      const int entry = p.page_shift >= 0 ? j >> p.page_shift : j / p.page_size;
+      const int id = ld_ro(p.table + r.row + entry);
+      return Place{id, j - entry * p.page_size, count};
     };
     int unit = 0;
-    auto load_unit = [&](const CUtensorMap* map, const Part& r, int tile, int page, int u) {
-      const int s = unit % kStages;
-      if (unit >= kStages) ok = ok && mbar_wait(empty(s), (unit / kStages - 1) & 1, abort, p.dev_status);
-      ok = __all_sync(0xFFFFFFFFu, ok);
-      if (!ok) return;
-      issued = unit + 1;
-      const bool withheld = nvfp4::kWithhold && blockIdx.x == 0 && unit == 0;  // test build: never issued
-      ++unit;
-      if (withheld) return;
-      if (lane == 0) mbar_arrive_expect_tx(full(s), L::kUnitBytes);
-      __syncwarp();
-      if (loads) {
-        const int j = tile * kKeys + sub * p.box;
-        const int token = p.table == nullptr ? r.begin + j : j % p.page_size;
-        tma_load_4d(ring + (uint32_t)(s * L::kUnitBytes + block * (kKeys * 128) + sub * p.box * 128), map,
-                    u * L::kUnitDims + block * 64, r.it.head, token, page, full(s));
+    auto load_tile = [&](const CUtensorMap* map, const Part& r, const Place& at) {
+      int page = at.page;
+      if (page < 0 || page >= p.pages) {
+        nvfp4::report(p.dev_status, NVFP4_ERR_INDEX);
+        page = p.pages;
+      }
+      const int head = uniform(r.it.head), count = uniform(at.count);
+#pragma unroll
+      for (int u = 0; u < kUnits; ++u) {
+        const int s = unit % kStages;
+        if (unit >= kStages) ok = ok && mbar_wait(empty(s), (unit / kStages - 1) & 1, abort, p.dev_status);
+        ok = __all_sync(0xFFFFFFFFu, ok);
+        if (!ok) return;
+        issued = unit + 1;
+        const bool withheld = nvfp4::kWithhold && blockIdx.x == 0 && unit == 0;  // test build: never issued
+        ++unit;
+        if (withheld) continue;
+        if (lead) mbar_arrive_expect_tx(full(s), (uint32_t)(count * p.box * 128 * kBlocks));
+        __syncwarp();
+        const uint32_t dst = ring + (uint32_t)(s * L::kUnitBytes);
+#pragma unroll
+        for (int i = 0; i < 8; ++i) {
+          if (i >= count) break;
+          const int pg = __shfl_sync(0xFFFFFFFFu, page, i), tk = __shfl_sync(0xFFFFFFFFu, at.token, i);
+#pragma unroll
+          for (int b = 0; b < kBlocks; ++b)
+            tma_load_4d(lead, dst + (uint32_t)(b * (kKeys * 128) + i * p.box * 128), map, u * L::kUnitDims + b * 64, head, tk,
+                        pg, full(s));
+        }
       }
     };
-    auto load_tile = [&](const CUtensorMap* map, const Part& r, int tile, int page) {
-      for (int u = 0; u < kUnits && ok; ++u) load_unit(map, r, tile, page, u);
-    };
-    Part cur = advance();
-    int page = cur.it.rows ? page_of(cur, cur.it.first) : 0;
-    Part prev{};
-    int prev_tile = -1, prev_page = 0, count = 0, record = 0;
+    Part cur = advance(), prev{};
+    Place at{}, prev_at{};
+    if (cur.it.rows) at = place_of(cur, cur.it.first);
+    bool behind = false;  // a V is still to come
+    int count = 0, record = 0;
     Part recorded{};
     while (ok) {
       const int i = count % kDescs;
@@ -464,28 +531,33 @@ attention_kernel(const __grid_constant__ CUtensorMap map_q, const __grid_constan
         record = cur.record;
         recorded = cur;
       }
-      const Part next = advance();
-      int next_first = 0;
-      if (next.it.rows) next_first = page_of(next, next.it.first);
+      Part next{};
       for (int tile = cur.it.first; tile < cur.it.last && ok; ++tile) {
-        const int next_page = tile + 1 < cur.it.last ? page_of(cur, tile + 1) : next_first;
-        load_tile(&map_k, cur, tile, page);
+        load_tile(&map_k, cur, at);
+        // the next tile's pages are on their way while this one's are loaded
+        Place next_at{};
+        if (tile + 1 < cur.it.last) {
+          next_at = place_of(cur, tile + 1);
+        } else {
+          next = advance();
+          if (next.it.rows) next_at = place_of(next, next.it.first);
+        }
         if constexpr (NQ == 2) {
-          load_tile(&map_v, cur, tile, page);
+          if (ok) load_tile(&map_v, cur, at);
         } else {
           // V one tile behind K, as the MMAs take them
-          if (prev_tile >= 0) load_tile(&map_v, prev, prev_tile, prev_page);
+          if (ok && behind) load_tile(&map_v, prev, prev_at);
+          behind = true;
           prev = cur;
-          prev_tile = tile;
-          prev_page = page;
+          prev_at = at;
         }
-        page = next_page;
+        at = next_at;
       }
       cur = next;
     }
-    if (NQ == 1 && ok && prev_tile >= 0) {
+    if (NQ == 1 && ok && behind) {
       unit += kUnits;  // the place of a K that does not come: V's is the same for every tile
-      load_tile(&map_v, prev, prev_tile, prev_page);
+      load_tile(&map_v, prev, prev_at);
     }
     if (lane == 0) {
       Record* rec = reinterpret_cast<Record*>(p.ws + (size_t)blockIdx.x * 64);
@@ -493,21 +565,25 @@ attention_kernel(const __grid_constant__ CUtensorMap map_q, const __grid_constan
     }
   } else if (warp == 10) {
     // ------------------------------------------------------------------ Q loads
-    if (lane == 0) {
-      for (int count = 0;; ++count) {
-        const int i = count % kDescs;
-        if (!mbar_wait(item_full(i), (count / kDescs) & 1, abort, p.dev_status)) break;
-        const Item it = items[i];
-        mbar_arrive(item_empty(i));
-        if (it.rows == 0) break;
-        if (count > 0 && !mbar_wait(q_empty, (count - 1) & 1, abort, p.dev_status)) break;
-        q_issued = count + 1;
-        mbar_arrive_expect_tx(q_full, (uint32_t)(NQ * (D / 64) * per_tile * p.group * 128));
-        for (int t = 0; t < NQ; ++t)
-          for (int b = 0; b < D / 64; ++b)
-            tma_load_4d(q_smem + (uint32_t)(t * L::kQTile + b * (kRows * 128)), &map_q, b * 64, 0, it.head,
-                        it.row0 + t * per_tile, q_full);
-      }
+    for (int count = 0;; ++count) {
+      const int i = count % kDescs;
+      bool ok = mbar_wait(item_full(i), (count / kDescs) & 1, abort, p.dev_status);
+      if (!__all_sync(0xFFFFFFFFu, ok)) break;
+      const int rows = uniform(items[i].rows), row0 = uniform(items[i].row0), head = uniform(items[i].head);
+      __syncwarp();
+      if (lane == 0) mbar_arrive(item_empty(i));
+      if (rows == 0) break;
+      ok = count == 0 || mbar_wait(q_empty, (count - 1) & 1, abort, p.dev_status);
+      if (!__all_sync(0xFFFFFFFFu, ok)) break;
+      q_issued = count + 1;
+      if (lead) mbar_arrive_expect_tx(q_full, (uint32_t)(NQ * (D / 64) * per_tile * p.group * 128));
+      __syncwarp();
+#pragma unroll
+      for (int t = 0; t < NQ; ++t)
+#pragma unroll
+        for (int b = 0; b < D / 64; ++b)
+          tma_load_4d(lead, q_smem + (uint32_t)(t * L::kQTile + b * (kRows * 128)), &map_q, b * 64, 0, head,
+                      row0 + t * per_tile, q_full);
     }
   } else if (warp == 8) {
     // --------------------------------------------------------------------- MMAs
@@ -525,11 +601,11 @@ attention_kernel(const __grid_constant__ CUtensorMap map_q, const __grid_constan
       ok = mbar_wait(item_full(i), (c.count / kDescs) & 1, abort, p.dev_status);
       ok = __all_sync(0xFFFFFFFFu, ok);
       if (!ok) return;
-      const Item it = items[i];
-      c.rows = it.rows;
-      c.tile = c.first = it.first;
-      c.last = it.last;
-      c.end = it.end;
+      const Item& it = items[i];
+      c.rows = uniform(it.rows);
+      c.tile = c.first = uniform(it.first);
+      c.last = uniform(it.last);
+      c.end = uniform(it.end);
       c.row_tile = 0;
       ++c.count;
       __syncwarp();
@@ -563,22 +639,15 @@ attention_kernel(const __grid_constant__ CUtensorMap map_q, const __grid_constan
         if (NQ == 1 || cs.row_tile == 0) wait_unit(u0 + u);
         if (!ok) return;
         tc_fence_after();
-        const uint64_t a = smem_desc(q_smem + (uint32_t)(cs.row_tile * L::kQTile + u * kBlocks * (kRows * 128)));
-        const uint64_t b = smem_desc(ring + (uint32_t)((u0 + u) % kStages * L::kUnitBytes));
-        if (elect_one()) {
+        const uint32_t a = desc_low(q_smem + (uint32_t)(cs.row_tile * L::kQTile + u * kBlocks * (kRows * 128)));
+        const uint32_t b = desc_low(ring + (uint32_t)((u0 + u) % kStages * L::kUnitBytes));
 #pragma unroll
-          for (int kk = 0; kk < L::kUnitDims / 16; ++kk) {
-            const uint64_t at = (uint64_t)((kk / 4) * (kRows * 128 >> 4) + (kk % 4) * 2);
-            mma_ss(d, a + at, b + at, kIdescS, (u > 0 || kk > 0) ? 1u : 0u);
-          }
-          if (last_use) mma_commit(empty((u0 + u) % kStages));
-          if (u == kUnits - 1) {
-            mma_commit(s_full(gs & 1));
-            if (last_use && cs.tile + 1 == cs.last) mma_commit(q_empty);
-          }
-        }
-        __syncwarp();
+        for (int c = 0; c < kBlocks; ++c)
+          mma_ss4(lead, d, a + c * (kRows * 128 >> 4), b + c * (kKeys * 128 >> 4), kIdescS, (u > 0 || c > 0) ? 1u : 0u);
+        if (u == kUnits - 1) commit(lead, s_full(gs & 1));
+        if (last_use) commit(lead, empty((u0 + u) % kStages));
       }
+      if (last_use && cs.tile + 1 == cs.last) commit(lead, q_empty);
       ++gs;
       step(cs, false);
     };
@@ -598,15 +667,13 @@ attention_kernel(const __grid_constant__ CUtensorMap map_q, const __grid_constan
         if (NQ == 1 || cp.row_tile == 0) wait_unit(u0 + u);
         if (!ok) return;
         tc_fence_after();
-        const uint64_t b = desc_v(ring + (uint32_t)((u0 + u) % kStages * L::kUnitBytes));
-        if (elect_one()) {
-          for (int kk = 0; kk < steps; ++kk)
-            mma_ts(o + (uint32_t)(u * L::kUnitDims), a + (uint32_t)(8 * kk), b + (uint64_t)(kk * (16 * 128 >> 4)), kIdescO,
-                   (cp.tile > cp.first || kk > 0) ? 1u : 0u);
-          if (last_use) mma_commit(empty((u0 + u) % kStages));
-          if (u == kUnits - 1) mma_commit(pv_done(gp & 1));
-        }
-        __syncwarp();
+        const uint32_t b = desc_low_v(ring + (uint32_t)((u0 + u) % kStages * L::kUnitBytes));
+#pragma unroll
+        for (int h = 0; h < 2; ++h)
+          mma_ts4(lead, o + (uint32_t)(u * L::kUnitDims), a + 32 * h, b + 512 * h, kIdescO,
+                  (cp.tile > cp.first || h > 0) ? 1u : 0u, steps - 4 * h);
+        if (u == kUnits - 1) commit(lead, pv_done(gp & 1));
+        if (last_use) commit(lead, empty((u0 + u) % kStages));
       }
       ++gp;
       step(cp, true);
@@ -649,7 +716,7 @@ attention_kernel(const __grid_constant__ CUtensorMap map_q, const __grid_constan
       if (it.rows == 0) break;
       const bool valid = token < per_tile && t * per_tile + token < it.rows;
       const bool busy = __any_sync(0xFFFFFFFFu, valid);  // this warp has rows
-      const int limit = valid ? it.pos0 + t * per_tile + token + 1 : 0;  // keys that the row sees
+      const int limit = valid ? it.pos0 + t * per_tile + token + 1 : 0x7FFFFFFF;  // keys that the row sees
       float m = -INFINITY, l = 0.0f;
       for (int tile = it.first; tile < it.last; ++tile, ++x) {
         const int b = NQ == 2 ? t : x & 1;
@@ -682,9 +749,10 @@ attention_kernel(const __grid_constant__ CUtensorMap map_q, const __grid_constan
           for (int i = 0; i < kCols; i += 8)
 #pragma unroll
             for (int e = 0; e < 4; ++e)
-              top4[e] = fmaxf(top4[e], fmaxf(__uint_as_float(s[(i + 2 * e) / 32][(i + 2 * e) % 32]),
-                                             __uint_as_float(s[(i + 2 * e + 1) / 32][(i + 2 * e + 1) % 32])));
-          top = fmaxf(fmaxf(top4[0], top4[1]), fmaxf(top4[2], top4[3]));
+              top4[e] = max3(top4[e], __uint_as_float(s[(i + 2 * e) / 32][(i + 2 * e) % 32]),
+                             __uint_as_float(s[(i + 2 * e + 1) / 32][(i + 2 * e + 1) % 32]));
+          top = max3(fmaxf(top4[0], top4[1]), top4[2], top4[3]);
+          if (!valid) top = 0.0f;  // (no row: whatever S holds there, O is not rescaled for it)
         }
         if constexpr (NQ == 1) {
           float* at = xch + (exchanges & 1) * 2 * kRows + r;
@@ -697,7 +765,7 @@ attention_kernel(const __grid_constant__ CUtensorMap map_q, const __grid_constan
         if (busy) {
           // the reference maximum: raised for the whole warp once a row needs it
           const float raised = fmaxf(m, top);
-          const bool grow = m == -INFINITY ? raised > m : (raised - m) * scale > kRescale;
+          const bool grow = (raised - m) * scale > kRescale;  // (no key seen yet, neither before: not a number)
           if (__any_sync(0xFFFFFFFFu, grow)) {
             const float keep = m == -INFINITY ? 0.0f : exp2_approx((m - raised) * scale);
             l *= keep;
@@ -835,7 +903,7 @@ attention_kernel(const __grid_constant__ CUtensorMap map_q, const __grid_constan
       for (int u = issued > kStages ? issued - kStages : 0; u < issued; ++u)
         mbar_drain(full(u % kStages), (uint32_t)(u / kStages) & 1u, p.dev_status);
     if (warp == 10 && lane == 0 && q_issued > 0) mbar_drain(q_full, (uint32_t)(q_issued - 1) & 1u, p.dev_status);
-    if (warp == 8 && elect_one()) {
+    if (warp == 8 && lead) {
       mma_commit(drain_bar);
       mbar_drain(drain_bar, 0u, p.dev_status);
     }
@@ -850,66 +918,94 @@ attention_kernel(const __grid_constant__ CUtensorMap map_q, const __grid_constan
 
 // ------------------------------------------------------------------- join
 //
-// One block per (CTA whose share begins an item that others finish, group of rows): a warp
-// per row and slice of the parts, then over the slices, all in the order of the keys.
+// For each CTA whose share begins an item that others finish: out = sum_k w_k O_k / sum_k w_k l_k,
+// w_k = exp2(m_k - max m), over the parts k in the order of the keys.  Few parts: a warp a row;
+// many (few rows over a long axis): a block a row, a slice of the parts each warp, the slices
+// added in order.  The weights come first, so that the sums' loads wait for nothing.
 
 constexpr int kJoinWarps = 8;
+constexpr int kJoinFew = 8;  // parts that one warp takes
 
 template <int D, int NQ>
 __global__ void __launch_bounds__(32 * kJoinWarps) attention_join_kernel(const __grid_constant__ Params p) {
-  constexpr int E = D / 32;  // of a lane
-  __shared__ float acc[kJoinWarps][D];
-  __shared__ float2 stats[kJoinWarps];
+  constexpr int E = D / 64;  // float2 of a lane
+  __shared__ float2 acc[kJoinWarps][D / 2];
+  __shared__ float weights[ATTENTION_MAX_CTAS];
   nvfp4::wait_for_previous_kernel();
   const int c = blockIdx.x, warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
   const Record rec = *reinterpret_cast<const Record*>(p.ws + (size_t)c * 64);
-  if (rec.parts <= 0) return;
-  const int per_tile = kRows / p.group, rows = rec.rows * p.group;
-  const float* slots = reinterpret_cast<const float*>(p.ws + kRecordBytes);
-  const int first = rec.parts * warp / kJoinWarps, last = rec.parts * (warp + 1) / kJoinWarps;
-  for (int i = blockIdx.y; i < rows; i += gridDim.y) {
+  const int parts = rec.parts, rows = rec.rows * p.group;
+  if (parts <= 0) return;
+  const int per_tile = kRows / p.group;
+  const bool few = parts <= kJoinFew;
+  const float* slots = reinterpret_cast<const float*>(p.ws + kRecordBytes) + 2 * (int64_t)c * slot_floats(D, NQ);
+  // part 0 is the first CTA's second place, the others are the next CTAs' first
+  auto slot_of = [&](int k) { return slots + (k == 0 ? 1 : 2 * k) * slot_floats(D, NQ); };
+  const int first = few ? 0 : parts * warp / kJoinWarps, last = few ? parts : parts * (warp + 1) / kJoinWarps;
+  const int row0 = few ? (int)blockIdx.y * kJoinWarps + warp : (int)blockIdx.y;
+  const int step = few ? (int)gridDim.y * kJoinWarps : (int)gridDim.y;
+  for (int i = row0; i < rows; i += step) {
     const int token = i / p.group, g = i - token * p.group;
     const int row = token / per_tile * kRows + token % per_tile * p.group + g;
-    float m = -INFINITY, l = 0.0f, o[E];
+    // (every warp forms all weights: lane k those of parts k, k + 32, ...)
+    constexpr int kMost = (ATTENTION_MAX_CTAS + 31) / 32;
+    float2 ml[kMost];
+    float top = -INFINITY;
 #pragma unroll
-    for (int e = 0; e < E; ++e) o[e] = 0.0f;
+    for (int j = 0; j < kMost; ++j) {
+      ml[j] = make_float2(-INFINITY, 0.0f);
+      if (lane + 32 * j < parts) ml[j] = *reinterpret_cast<const float2*>(slot_of(lane + 32 * j) + 2 * row);
+      top = fmaxf(top, ml[j].x);
+    }
+#pragma unroll
+    for (int d = 16; d; d >>= 1) top = fmaxf(top, __shfl_xor_sync(0xFFFFFFFFu, top, d));
+    float total = 0.0f, w0 = 0.0f;
+#pragma unroll
+    for (int j = 0; j < kMost; ++j) {
+      // (a part of which the row sees no key has l = 0, and O that may be anything)
+      const float w = ml[j].y == 0.0f ? 0.0f : exp2_approx((ml[j].x - top) * p.scale);
+      if (j == 0) w0 = w;
+      if (!few && warp == 0 && lane + 32 * j < parts) weights[lane + 32 * j] = w;
+      total += ml[j].y * w;
+    }
+#pragma unroll
+    for (int d = 16; d; d >>= 1) total += __shfl_xor_sync(0xFFFFFFFFu, total, d);
+    if (!few) __syncthreads();
+    float2 o[E];
+#pragma unroll
+    for (int e = 0; e < E; ++e) o[e] = make_float2(0.0f, 0.0f);
+#pragma unroll 4
     for (int k = first; k < last; ++k) {
-      const float* slot = slots + (2 * (int64_t)(c + k) + (k == 0 ? 1 : 0)) * slot_floats(D, NQ);
-      const float2 ml = *reinterpret_cast<const float2*>(slot + 2 * row);
-      float v[E];
+      const float w = few ? __shfl_sync(0xFFFFFFFFu, w0, k) : weights[k];
+      const float2* src = reinterpret_cast<const float2*>(slot_of(k) + 2 * NQ * kRows + (int64_t)row * D) + lane;
 #pragma unroll
-      for (int e = 0; e < E; ++e) v[e] = slot[2 * NQ * kRows + (int64_t)row * D + lane + 32 * e];
-      if (ml.y == 0.0f) continue;  // (sees none of this part's keys)
-      const float top = fmaxf(m, ml.x);
-      const float a = m == -INFINITY ? 0.0f : exp2_approx((m - top) * p.scale), b = exp2_approx((ml.x - top) * p.scale);
-      m = top;
-      l = l * a + ml.y * b;
-#pragma unroll
-      for (int e = 0; e < E; ++e) o[e] = o[e] * a + v[e] * b;
-    }
-#pragma unroll
-    for (int e = 0; e < E; ++e) acc[warp][lane + 32 * e] = o[e];
-    if (lane == 0) stats[warp] = make_float2(m, l);
-    __syncthreads();
-    if (threadIdx.x < D / 2) {
-      float top = -INFINITY, total = 0.0f;
-      float2 sum = make_float2(0.0f, 0.0f);
-#pragma unroll
-      for (int w = 0; w < kJoinWarps; ++w) top = fmaxf(top, stats[w].x);
-#pragma unroll
-      for (int w = 0; w < kJoinWarps; ++w) {
-        if (stats[w].y == 0.0f) continue;
-        const float b = exp2_approx((stats[w].x - top) * p.scale);
-        total += stats[w].y * b;
-        const float2 v = *reinterpret_cast<const float2*>(&acc[w][2 * threadIdx.x]);
-        sum.x += v.x * b;
-        sum.y += v.y * b;
+      for (int e = 0; e < E; ++e) {
+        const float2 v = src[32 * e];
+        o[e].x += w != 0.0f ? v.x * w : 0.0f;
+        o[e].y += w != 0.0f ? v.y * w : 0.0f;
       }
-      const float norm = 1.0f / total;
-      __nv_bfloat16* out = p.out + (int64_t)(rec.row0 + token) * p.ld_token + (rec.head * p.group + g) * p.ld_head;
-      reinterpret_cast<uint32_t*>(out)[threadIdx.x] = total != 0.0f ? to_bf16x2(sum.x * norm, sum.y * norm) : 0u;
     }
-    __syncthreads();
+    const float norm = 1.0f / total;
+    uint32_t* out = reinterpret_cast<uint32_t*>(p.out + (int64_t)(rec.row0 + token) * p.ld_token +
+                                                (rec.head * p.group + g) * p.ld_head);
+    if (few) {
+#pragma unroll
+      for (int e = 0; e < E; ++e) out[lane + 32 * e] = total != 0.0f ? to_bf16x2(o[e].x * norm, o[e].y * norm) : 0u;
+    } else {
+#pragma unroll
+      for (int e = 0; e < E; ++e) acc[warp][lane + 32 * e] = o[e];
+      __syncthreads();
+      if (threadIdx.x < D / 2) {
+        float2 sum = make_float2(0.0f, 0.0f);
+#pragma unroll
+        for (int w = 0; w < kJoinWarps; ++w) {
+          sum.x += acc[w][threadIdx.x].x;
+          sum.y += acc[w][threadIdx.x].y;
+        }
+        out[threadIdx.x] = total != 0.0f ? to_bf16x2(sum.x * norm, sum.y * norm) : 0u;
+      }
+      __syncthreads();
+    }
   }
 }
 
@@ -940,6 +1036,9 @@ int launch(const paged_attention_input& in, const attn_rows& out, void* workspac
   p.kv_heads = (int)in.kv_heads;
   p.group = (int)(in.heads / in.kv_heads);
   p.page_size = (int)in.page_size;
+  p.page_shift = -1;
+  for (int i = 4; i < 17; ++i)
+    if (in.page_size == (int64_t)1 << i) p.page_shift = i;
   p.pages = (int)in.pages;
   p.box = kKeys;
   if (in.block_table != nullptr)
@@ -971,7 +1070,7 @@ int launch(const paged_attention_input& in, const attn_rows& out, void* workspac
   if (nvfp4::launch_dependent(kern, dim3(grid), dim3(kThreads), L::kSmemBytes, stream, 1, args) != cudaSuccess)
     return NVFP4_ERR_CUDA;
   void* join_args[] = {&p};
-  if (nvfp4::launch_dependent((const void*)attention_join_kernel<D, NQ>, dim3(grid, 8), dim3(32 * kJoinWarps), 0, stream, 1,
+  if (nvfp4::launch_dependent((const void*)attention_join_kernel<D, NQ>, dim3(grid, 8 * NQ), dim3(32 * kJoinWarps), 0, stream, 1,
                               join_args) != cudaSuccess)
     return NVFP4_ERR_CUDA;
   return NVFP4_OK;
