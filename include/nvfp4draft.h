@@ -638,7 +638,7 @@ typedef struct prompt_attention_input {
  * another query of its sequence sees must be finite.  Other sequences' may be anything.
  * Sums are split over SMs by a rule on the lengths and joined in a fixed order: the same
  * call gives the same bits.
- * Workspace: ATTENTION_WS_BYTES, 16-byte aligned; nothing need be in it, nothing is kept
+ * Workspace: ATTENTION_WS_BYTES, 32-byte aligned; nothing need be in it, nothing is kept
  * there.  Waits inside the kernel are bounded; one that runs out writes NVFP4_ERR_TIMEOUT
  * to dev_status and leaves the output incomplete.
  */

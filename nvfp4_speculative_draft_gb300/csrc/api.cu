@@ -201,7 +201,8 @@ int attention(const paged_attention_input& in, const attn_rows* out, const nvfp4
     return NVFP4_ERR_SHAPE;
   if (!rows_aligned(in.q) || !pages_aligned(in.k) || !pages_aligned(in.v) || !rows_aligned(*out) || !aligned4(in.cu))
     return NVFP4_ERR_ALIGN;
-  if (ex == nullptr || ex->workspace == nullptr || ex->workspace_bytes < ATTENTION_WS_BYTES || !aligned16(ex->workspace))
+  if (ex == nullptr || ex->workspace == nullptr || ex->workspace_bytes < ATTENTION_WS_BYTES ||
+      (reinterpret_cast<uintptr_t>(ex->workspace) & 31u))
     return NVFP4_ERR_WORKSPACE;
   return launch_attention(&in, out, ex->workspace, status_of(ex), stream_of(ex));
 }

@@ -22,9 +22,9 @@
 //          warpgroups work on the same tile, half of its keys each, and exchange the
 //          rows' maxima through shared memory; S is double buffered.
 //   warps 0..7  softmax; they rescale and finish O as well
-//   warp 8      allocates TMEM, issues the MMAs: S two steps ahead of the P V it waits for
-//   warp 9      schedules the items and loads K and V (TMA) into a ring
-//   warp 10     loads Q
+//   warp 8      allocates TMEM, issues the MMAs (NQ = 2: warps 8 and 11, a tile of rows each)
+//   warp 9      schedules the items and loads K (TMA)
+//   warp 10     loads Q and V
 //
 // Schedule: the items of all sequences and heads are laid end to end on a line, a tile of
 // keys 128 units long and an item's start kItemCost, and every CTA takes an equal share of
@@ -38,6 +38,8 @@
 // other sequences or unused slots, does not matter.
 #include <cuda_bf16.h>
 
+#include <type_traits>
+
 #include "tc.cuh"
 
 namespace {
@@ -48,31 +50,34 @@ using nvfp4::ld_ro;
 constexpr int kRows = 128;                    // MMA rows of a tile of queries
 constexpr int kKeys = 128;                    // keys of a tile
 constexpr int kSoftmaxWarps = 8;
-constexpr int kWarps = kSoftmaxWarps + 4;     // (three of the last four work)
-constexpr int kThreads = 32 * kWarps;
+constexpr int kThreads = 32 * (kSoftmaxWarps + 4);  // (three of the last four work)
 constexpr int kDescs = 4;                     // item descriptors in flight
 constexpr int kItemCost = kKeys;              // an item's fixed cost, in keys
-constexpr int kMinShare = 2 * kKeys + kItemCost;  // of a CTA, where there are that few
+constexpr int kMinShare = 160;                // of a CTA, where there is that little
 constexpr float kRescale = 8.0f;              // log2 of what the maximum may lag behind
 constexpr float kLog2e = 1.4426950408889634f;
 
 template <int D, int NQ>
 struct Tile {
-  static constexpr int kUnitDims = D < 128 ? D : 128;  // of a unit of the ring: 128 keys of as many dims
-  static constexpr int kUnits = D / kUnitDims;         // of a tile of K, and of V
-  static constexpr int kBlocks = kUnitDims / 64;       // swizzled columns of 128 bytes
-  static constexpr int kUnitBytes = kKeys * kUnitDims * 2;
+  // Units of the rings: 128 keys of as many dims.
+  static constexpr int kDimsK = D < 128 ? D : 128, kDimsV = kDimsK;
+  static constexpr int kUnitsK = D / kDimsK, kUnitsV = D / kDimsV;  // of a tile
+  static constexpr int kBytesK = kKeys * kDimsK * 2, kBytesV = kKeys * kDimsV * 2;
   static constexpr int kQTile = kRows * D * 2;
   static constexpr int kQBytes = NQ * kQTile;
   static constexpr int kXchBytes = NQ == 1 ? 2 * 2 * kRows * 4 : 0;
-  static constexpr int kDescBytes = kDescs * 64;
-  static constexpr int kRest = kXchBytes + kDescBytes + 512;
-  static constexpr int kFit = (227 * 1024 - kQBytes - kRest) / kUnitBytes;
-  static constexpr int kStages = kFit < 10 ? kFit : 10;
-  static constexpr size_t kSmemBytes = (size_t)kQBytes + (size_t)kStages * kUnitBytes + kRest;
   static constexpr int kCols = NQ == 2 ? kKeys : kKeys / 2;  // of S, a softmax thread's
   static constexpr int kOut = NQ == 2 ? D : D / 2;           // of O, a softmax thread's
-  static_assert(kStages >= 5 && kStages > kUnits, "ring");
+  static constexpr int kDescBytes = kDescs * 64;
+  static constexpr int kRest = kXchBytes + kDescBytes + 512;
+  static constexpr int kFit = 227 * 1024 - kQBytes - kRest;
+  static constexpr int kStagesV = D == 64 ? 5 : 3;
+  static constexpr int kLeft = (kFit - kStagesV * kBytesV) / kBytesK;
+  static constexpr int kStagesK = kLeft < 5 ? kLeft : 5;
+  static constexpr int kStages = kStagesK + kStagesV, kRing = kStagesK * kBytesK + kStagesV * kBytesV;
+  static constexpr size_t kSmemBytes = (size_t)kQBytes + kRing + kRest;
+  static_assert(kStagesK >= 2 && kStagesK >= kUnitsK && kStagesV > kUnitsV, "rings");
+  static_assert(kBytesK % 1024 == 0 && kBytesV % 1024 == 0, "swizzled tiles start on 1 KB");
   static_assert(2 * kKeys + NQ * D <= 512, "TMEM");
 };
 
@@ -82,6 +87,7 @@ struct Params {
   const int32_t* table;
   int64_t ld_table, capacity;  // tokens of a table row
   int tokens, batch, kv_heads, group;
+  int per_tile, per_item;      // tokens of a tile of rows, and of an item
   int page_size, page_shift;   // tokens of a page; log2 of it, or -1
   int box;                     // tokens of a TMA box
   int pages;
@@ -89,13 +95,13 @@ struct Params {
   int negative;
   __nv_bfloat16* out;
   int64_t ld_token, ld_head;
+  bool wide;                   // rows of the output start on 32 bytes
   unsigned char* ws;
   int32_t* dev_status;
 };
 
 struct Sequence {
   int begin, n;  // rows of q
-  int len;       // keys
   int off;       // position of the first query (may be negative)
 };
 
@@ -105,6 +111,8 @@ struct __align__(16) Item {
   int pos0, end;    // position of the first; keys that some row sees
   int head, first;  // key head; first tile of this part
   int last, slot;   // past its last tile; -1: the whole item, else the part's place
+  int64_t table;    // of its sequence: the block table's row,
+  int begin;        // the first token of packed prompts
 };
 
 // An item cut by a share's border, for the kernel that joins its parts.
@@ -115,15 +123,21 @@ struct Record {
 __host__ __device__ constexpr int64_t slot_floats(int d, int nq) { return (int64_t)nq * kRows * (d + 2); }
 constexpr size_t kRecordBytes = (size_t)ATTENTION_MAX_CTAS * 64;
 
-__device__ __forceinline__ Sequence sequence(const Params& p, int s, bool* consistent = nullptr) {
-  const int a = ld_ro(p.cu + s), b = ld_ro(p.cu + s + 1);
-  const int64_t cached = p.kv_lens != nullptr ? ld_ro(p.kv_lens + s) : 0;
+// Offsets and length as they are in memory, and what they come to within the tensors.
+struct Raw {
+  int a, b, cached;
+};
+__device__ __forceinline__ Raw load_raw(const Params& p, int s) {
+  return Raw{ld_ro(p.cu + s), ld_ro(p.cu + s + 1), p.kv_lens != nullptr ? ld_ro(p.kv_lens + s) : 0};
+}
+__device__ __forceinline__ bool consistent(const Params& p, const Raw& r) {
+  return r.a >= 0 && r.b <= p.tokens && r.a <= r.b && r.cached <= p.capacity;
+}
+__device__ __forceinline__ Sequence sequence(const Params& p, const Raw& r) {
   Sequence q;
-  q.begin = min(max(a, 0), p.tokens);
-  q.n = max(min(max(b, 0), p.tokens) - q.begin, 0);
-  q.len = p.kv_lens != nullptr ? (int)min(max(cached, (int64_t)0), p.capacity) : q.n;
-  q.off = q.len - q.n;
-  if (consistent != nullptr) *consistent = a >= 0 && b <= p.tokens && a <= b && cached <= p.capacity;
+  q.begin = min(max(r.a, 0), p.tokens);
+  q.n = max(min(max(r.b, 0), p.tokens) - q.begin, 0);
+  q.off = (p.kv_lens != nullptr ? (int)min((int64_t)max(r.cached, 0), p.capacity) : q.n) - q.n;
   return q;
 }
 // (64-bit division takes several times a 32-bit one's time)
@@ -132,20 +146,21 @@ __device__ __forceinline__ int64_t quotient(int64_t a, int64_t b) {
 }
 
 // The line: item t of a (sequence, head) starts `before(t)` behind its head's start.
-template <int NQ>
 struct Line {
   int per;       // tokens of an item
-  int64_t base;  // length of item 0
   int items;
+  int64_t base;  // length of item 0
   int64_t length;
-  __device__ __forceinline__ Line(const Sequence& q, int group) {
-    per = NQ * (kRows / group);
-    items = (q.n + per - 1) / per;
-    const int64_t cached = max(q.off, 0);
-    base = cached + per + kItemCost;
+  __device__ __forceinline__ Line(const Sequence& q, int per_item) {
+    per = per_item;
+    items = q.n <= per ? (q.n > 0) : (q.n + per - 1) / per;
+    const int cached = max(q.off, 0);
+    base = (int64_t)cached + per + kItemCost;
     length = items > 0 ? before(items - 1) + cached + q.n + kItemCost : 0;
   }
-  __device__ __forceinline__ int64_t before(int64_t t) const { return t * base + per * (t * (t - 1) / 2); }
+  __device__ __forceinline__ int64_t before(int t) const {
+    return t * base + (int64_t)per * ((int64_t)t * (t - 1) / 2);
+  }
 };
 
 // TMA and MMA instructions are issued by one lane of a converged warp, by predicate and not
@@ -195,7 +210,7 @@ __device__ __forceinline__ void mma_ss4(uint32_t lead, uint32_t d, uint32_t a, u
       "r"(d), "r"(a), "r"(b), "r"(idesc), "r"(accumulate), "r"(kDescHigh)
       : "memory");
 }
-// Four MMAs along 64 keys: P in TMEM, 16 keys in 8 columns; V 16 rows of 128 bytes apart.  Of
+// Four MMAs along 64 keys (a half of P): 16 keys in 8 columns; V 16 rows of 128 bytes apart.  Of
 // them the first `steps`.
 __device__ __forceinline__ void mma_ts4(uint32_t lead, uint32_t d, uint32_t a, uint32_t b, uint32_t idesc,
                                         uint32_t accumulate, int steps) {
@@ -219,6 +234,12 @@ __device__ __forceinline__ void tmem_store(uint32_t taddr, const uint32_t (&v)[1
       "r"(v[0]), "r"(v[1]), "r"(v[2]), "r"(v[3]), "r"(v[4]), "r"(v[5]), "r"(v[6]), "r"(v[7]), "r"(v[8]), "r"(v[9]),
       "r"(v[10]), "r"(v[11]), "r"(v[12]), "r"(v[13]), "r"(v[14]), "r"(v[15])
       : "memory");
+}
+// 32 bytes to one address: whole sectors
+__device__ __forceinline__ void store32(void* p, const uint32_t* v) {
+  asm volatile("st.global.v8.b32 [%0], {%1, %2, %3, %4, %5, %6, %7, %8};" ::"l"(p), "r"(v[0]), "r"(v[1]), "r"(v[2]),
+               "r"(v[3]), "r"(v[4]), "r"(v[5]), "r"(v[6]), "r"(v[7])
+               : "memory");
 }
 __device__ __forceinline__ void tmem_store_wait() { asm volatile("tcgen05.wait::st.sync.aligned;" ::: "memory"); }
 __device__ __forceinline__ float exp2_approx(float x) {  // 2^-22 relative; 0 for -inf
@@ -266,15 +287,21 @@ __global__ void __launch_bounds__(kThreads, 1)
 attention_kernel(const __grid_constant__ CUtensorMap map_q, const __grid_constant__ CUtensorMap map_k,
                  const __grid_constant__ CUtensorMap map_v, const __grid_constant__ Params p) {
   using L = Tile<D, NQ>;
-  constexpr int kStages = L::kStages, kUnits = L::kUnits, kBlocks = L::kBlocks;
+  constexpr int kStages = L::kStages, kUnitsK = L::kUnitsK, kUnitsV = L::kUnitsV;
+  constexpr int kMmaWarp = kSoftmaxWarps, kWarpK = kMmaWarp + 1, kWarpV = kMmaWarp + 2;
   extern __shared__ __align__(1024) unsigned char smem[];
   unsigned char* const ring_ptr = smem + L::kQBytes;
-  float* const xch = reinterpret_cast<float*>(ring_ptr + kStages * L::kUnitBytes);
+  float* const xch = reinterpret_cast<float*>(ring_ptr + L::kRing);
   Item* const items = reinterpret_cast<Item*>(reinterpret_cast<unsigned char*>(xch) + L::kXchBytes);
-  const uint32_t q_smem = smem_u32(smem), ring = q_smem + L::kQBytes;
+  const uint32_t q_smem = smem_u32(smem), ring = q_smem + L::kQBytes;  // K's, then V's
   const uint32_t bars = smem_u32(items) + L::kDescBytes;
+  // stages of the two rings: K's, then V's
+  constexpr int kK = L::kStagesK, kV = L::kStagesV;
   auto full = [&](int s) { return bars + 8u * s; };
   auto empty = [&](int s) { return bars + 8u * (kStages + s); };
+  auto stage_k = [&](int unit) { return unit % kK; };
+  auto stage_v = [&](int unit) { return kK + unit % kV; };
+  auto offset = [&](int s) { return (uint32_t)(s < kK ? s * L::kBytesK : kK * L::kBytesK + (s - kK) * L::kBytesV); };
   auto item_full = [&](int i) { return bars + 8u * (2 * kStages + i); };
   auto item_empty = [&](int i) { return bars + 8u * (2 * kStages + kDescs + i); };
   constexpr int kFixed = 2 * kStages + 2 * kDescs;
@@ -283,12 +310,9 @@ attention_kernel(const __grid_constant__ CUtensorMap map_q, const __grid_constan
   auto p_full = [&](int b) { return bars + 8u * (kFixed + 4 + b); };
   auto pv_done = [&](int t) { return bars + 8u * (kFixed + 6 + t); };
   const uint32_t drain_bar = bars + 8u * (kFixed + 8);
-  static_assert(8 * (kFixed + 9 + kWarps + 1) + 12 <= 512, "shared memory behind the items");
-  int64_t* const sums = reinterpret_cast<int64_t*>(reinterpret_cast<unsigned char*>(items) + L::kDescBytes + 8 * (kFixed + 9));
-  int64_t& start_at = sums[kWarps];
-  uint32_t* const tmem_slot = reinterpret_cast<uint32_t*>(sums + kWarps + 1);
+  static_assert(8 * (kFixed + 9) + 8 <= 512, "shared memory behind the items");
+  uint32_t* const tmem_slot = reinterpret_cast<uint32_t*>(reinterpret_cast<unsigned char*>(items) + L::kDescBytes + 8 * (kFixed + 9));
   volatile uint32_t* abort = tmem_slot + 1;
-  int& start_seq = reinterpret_cast<int*>(tmem_slot)[2];
   // (uniform: a role's code is then known not to diverge, and its instructions' addresses and
   // descriptors stay in uniform registers)
   const int warp = uniform((int)threadIdx.x >> 5), lane = threadIdx.x & 31;
@@ -310,95 +334,145 @@ attention_kernel(const __grid_constant__ CUtensorMap map_q, const __grid_constan
     mbar_init(q_empty, 1);
     for (int b = 0; b < 2; ++b) {
       mbar_init(s_full(b), 1);
-      mbar_init(p_full(b), NQ == 2 ? kSoftmaxWarps / 2 : kSoftmaxWarps);
+      mbar_init(p_full(b), kSoftmaxWarps / NQ);
       mbar_init(pv_done(b), 1);
     }
     mbar_init(drain_bar, 1);
     *abort = 0u;
     asm volatile("fence.mbarrier_init.release.cluster;" ::: "memory");
   }
-  if (warp == 8) {
+  if (warp == kMmaWarp) {
     asm volatile("tcgen05.alloc.cta_group::1.sync.aligned.shared::cta.b32 [%0], %1;" ::"r"(smem_u32(tmem_slot)), "r"(512)
                  : "memory");
     asm volatile("tcgen05.relinquish_alloc_permit.cta_group::1.sync.aligned;" ::: "memory");
   }
-  if (threadIdx.x >= 288 && threadIdx.x < 291) {
-    const CUtensorMap* m = threadIdx.x == 288 ? &map_q : threadIdx.x == 289 ? &map_k : &map_v;
+  if (warp == kWarpK && lane < 3) {
+    const CUtensorMap* m = lane == 0 ? &map_q : lane == 1 ? &map_k : &map_v;
     asm volatile("prefetch.tensormap [%0];" ::"l"(reinterpret_cast<uint64_t>(m)) : "memory");
   }
-  nvfp4::wait_for_previous_kernel();
-
-  // This CTA's share [x0, x1) of the line, and the sequence that x0 lies in.
-  const int run = (p.batch + kThreads - 1) / kThreads;
-  const int s0 = min(p.batch, (int)threadIdx.x * run), s1 = min(p.batch, s0 + run);
-  int64_t mine = 0;
-  for (int s = s0; s < s1; ++s) {
-    bool consistent;
-    mine += p.kv_heads * Line<NQ>(sequence(p, s, &consistent), p.group).length;
-    if (blockIdx.x == 0 && !consistent) nvfp4::report(p.dev_status, NVFP4_ERR_INDEX);
-  }
-  int64_t upto = mine;
-  if (p.batch > 1) {
-#pragma unroll
-    for (int d = 1; d < 32; d <<= 1) {
-      const int64_t o = __shfl_up_sync(0xFFFFFFFFu, upto, d);
-      if (lane >= d) upto += o;
-    }
-  }
-  if (lane == (p.batch > 1 ? 31 : 0)) sums[warp] = upto;
-  if (threadIdx.x == 0) start_seq = p.batch;
   tc_fence_before();
   __syncthreads();
   tc_fence_after();
   // all of the SM's columns: they start at 0 (a constant for the MMAs' addresses)
   constexpr uint32_t tmem = 0;
   if (*tmem_slot != tmem) nvfp4::report(p.dev_status, NVFP4_ERR_CUDA);
-  int64_t total = 0;
-#pragma unroll
-  for (int w = 0; w < kWarps; ++w) {
-    if (w == warp) upto += total;
-    total += sums[w];
-  }
-  // total = shares * each + rest: the first `rest` shares are one longer
-  const int64_t wanted = total / kMinShare;
-  const int shares = (int)(wanted < 1 ? 1 : wanted < gridDim.x ? wanted : gridDim.x);
-  const int64_t each = quotient(total, shares), rest = total - each * shares;
-  auto border = [&](int c) -> int64_t { return c < shares ? c * each + min((int64_t)c, rest) : total; };
-  const int64_t x0 = border((int)blockIdx.x), x1 = border((int)blockIdx.x + 1);
-  if (x0 < x1 && upto > x0 && upto - mine <= x0) {
-    int64_t at = upto - mine;
-    int s = s0;
-    for (; s + 1 < s1; ++s) {
-      const int64_t len = p.kv_heads * Line<NQ>(sequence(p, s), p.group).length;
-      if (at + len > x0) break;
-      at += len;
-    }
-    start_seq = s;
-    start_at = at;
-  }
-  __syncthreads();
-
-  const int per_tile = kRows / p.group;  // tokens of a tile of rows
+  const int per_tile = p.per_tile;
   int issued = 0, q_issued = 0;          // units and Q loads issued (TMA warps)
   const uint32_t lead = elect_one();     // the lane that issues for a warp
+  nvfp4::wait_for_previous_kernel();
 
-  // NQ = 2: the softmax's threads take registers that the others have no use for
-  // (256 x 208 + 128 x 88 = 384 x 168, what the block was launched with).
-  if (NQ == 2 && warp >= kSoftmaxWarps) asm volatile("setmaxnreg.dec.sync.aligned.u32 88;");
-  if (warp == 9) {
-    // ------------------------------------------------- schedule, K and V loads
-    // (all lanes together; lane i knows the page of a tile's box i)
+  // Loads of K and V, a warp each, all lanes together.  Where this lane's box of a tile
+  // lies: its page, and its first token there; how many boxes some row sees (the others are not
+  // loaded: their scores are masked whatever they are, and P V stops before them).
+  struct Place {
+    int page, token, count;
+  };
+  auto place_of = [&](const Item& it, int tile) -> Place {
     const int boxes = kKeys / p.box;
+    const int j = tile * kKeys + lane * p.box;
+    const int count = min(max((it.end - tile * kKeys + p.box - 1) / p.box, 0), boxes);
+    if (lane >= count) return Place{0, 0, count};
+    if (p.table == nullptr) return Place{0, it.begin + j, count};
+    const int entry = p.page_shift >= 0 ? j >> p.page_shift : j / p.page_size;
+    const int id = ld_ro(p.table + it.table + entry);
+    return Place{id, j - entry * p.page_size, count};
+  };
+  auto load_tile = [&](const CUtensorMap* map, auto dims, int first_stage, int stages, int key_head, const Place& at) -> bool {
+    constexpr int kDims = decltype(dims)::value, kBlocks = kDims / 64;  // swizzled columns of 128 bytes
+    int page = at.page;
+    if (page < 0 || page >= p.pages) {
+      nvfp4::report(p.dev_status, NVFP4_ERR_INDEX);
+      page = p.pages;  // (read as zeros)
+    }
+    const int head = uniform(key_head), count = uniform(at.count);
+#pragma unroll
+    for (int u = 0; u < D / kDims; ++u) {
+      const int s = first_stage + issued % stages;
+      const bool ok = issued < stages || mbar_wait(empty(s), (issued / stages - 1) & 1, abort, p.dev_status);
+      if (!__all_sync(0xFFFFFFFFu, ok)) return false;
+      const bool withheld = nvfp4::kWithhold && blockIdx.x == 0 && first_stage == 0 && issued == 0;  // (test build)
+      ++issued;
+      if (withheld) continue;
+      if (lead) mbar_arrive_expect_tx(full(s), (uint32_t)(count * p.box * 128 * kBlocks));
+      __syncwarp();
+      const uint32_t dst = ring + offset(s);
+#pragma unroll
+      for (int i = 0; i < 8; ++i) {
+        if (i >= count) break;
+        const int pg = __shfl_sync(0xFFFFFFFFu, page, i), tk = __shfl_sync(0xFFFFFFFFu, at.token, i);
+#pragma unroll
+        for (int b = 0; b < kBlocks; ++b)
+          tma_load_4d(lead, dst + (uint32_t)(b * (kKeys * 128) + i * p.box * 128), map, u * kDims + b * 64, head, tk, pg,
+                      full(s));
+      }
+    }
+    return true;
+  };
+
+  if (warp == kWarpK) {
+    // ------------------------------------------------------- schedule, K loads
     bool ok = true;
-    int seq = start_seq, head = 0, t = 0;
-    Sequence q{}, next_q{};
+    // This CTA's share [x0, x1) of the line: a lane a sequence.  (By this warp alone: the others
+    // get their items from it, and a pass over 32 sequences takes less than the block's barriers
+    // and loads up to some hundreds of them.)
+    int64_t total = 0, chunk = 0;  // of all sequences; this lane's of the first 32
+    Sequence q{};
+    for (int s = lane; s < p.batch; s += 32) {
+      const Raw raw = load_raw(p, s);
+      const Sequence x = sequence(p, raw);
+      const int64_t length = p.kv_heads * Line(x, p.per_item).length;
+      if (blockIdx.x == 0 && !consistent(p, raw)) nvfp4::report(p.dev_status, NVFP4_ERR_INDEX);
+      if (s < 32) {
+        q = x;
+        chunk = length;
+      }
+      total += length;
+    }
+    if (p.batch == 1) {
+      total = __shfl_sync(0xFFFFFFFFu, total, 0);
+    } else {
+#pragma unroll
+      for (int d = 16; d; d >>= 1) total += __shfl_xor_sync(0xFFFFFFFFu, total, d);
+    }
+    // total = shares * each + rest: the first `rest` shares are one longer
+    const int shares = total >= (int64_t)kMinShare * gridDim.x ? (int)gridDim.x : max((int)((uint32_t)total / kMinShare), 1);
+    const int64_t each = quotient(total, shares), rest = total - each * shares;
+    auto border = [&](int c) -> int64_t { return c < shares ? c * each + min((int64_t)c, rest) : total; };
+    const int64_t x0 = border((int)blockIdx.x), x1 = border((int)blockIdx.x + 1);
+    int seq = p.batch, head = 0, t = 0;
     int64_t head_at = 0;
-    if (seq < p.batch) {
-      q = sequence(p, seq);
-      const Line<NQ> line(q, p.group);
-      head = (int)quotient(x0 - start_at, line.length);
-      head_at = start_at + head * line.length;
-      int lo = 0, hi = line.items;  // the item that x0 lies in
+    if (x0 < x1) {  // the sequence, head and item that x0 lies in
+      int64_t at = 0;
+      int who = 0;
+      for (int base = 0; base < p.batch; base += 32) {
+        if (base > 0) {
+          q = base + lane < p.batch ? sequence(p, load_raw(p, base + lane)) : Sequence{};
+          chunk = p.kv_heads * Line(q, p.per_item).length;
+        }
+        int64_t upto = chunk;
+        if (p.batch > 1) {
+#pragma unroll
+          for (int d = 1; d < 32; d <<= 1) {
+            const int64_t o = __shfl_up_sync(0xFFFFFFFFu, upto, d);
+            if (lane >= d) upto += o;
+          }
+        }
+        const unsigned past = __ballot_sync(0xFFFFFFFFu, at + upto > x0);
+        if (past != 0u) {
+          who = __ffs((int)past) - 1;
+          seq = base + who;
+          at += __shfl_sync(0xFFFFFFFFu, upto - chunk, who);
+          break;
+        }
+        at += __shfl_sync(0xFFFFFFFFu, upto, 31);
+      }
+      q.begin = __shfl_sync(0xFFFFFFFFu, q.begin, who);
+      q.n = __shfl_sync(0xFFFFFFFFu, q.n, who);
+      q.off = __shfl_sync(0xFFFFFFFFu, q.off, who);
+      const Line line(q, p.per_item);
+      head = (int)quotient(x0 - at, line.length);
+      head_at = at + head * line.length;
+      int lo = 0, hi = line.items;
       while (hi - lo > 1) {
         const int mid = (lo + hi) >> 1;
         if (head_at + line.before(mid) <= x0)
@@ -407,29 +481,30 @@ attention_kernel(const __grid_constant__ CUtensorMap map_q, const __grid_constan
           hi = mid;
       }
       t = lo;
-      if (seq + 1 < p.batch) next_q = sequence(p, seq + 1);
     }
-    // The next part of this CTA's share, or rows = 0.  `row` is its table row, `begin` its
-    // first token in packed prompts.
+    Raw next_raw{};  // of sequence seq + 1, once `fetched`: on its way while seq's items are loaded
+    bool fetched = false;
+    // The next part of this CTA's share, or rows = 0.
     struct Part {
       Item it;
-      int64_t row;
-      int begin;
       int record;  // parts of the whole item, where this is the first of several
     };
     auto advance = [&]() -> Part {
       Part r{};
       r.it.rows = 0;
       while (seq < p.batch) {
-        const Line<NQ> line(q, p.group);
+        const Line line(q, p.per_item);
         if (t >= line.items) {
           t = 0;
           head_at += line.length;
           if (q.n == 0 || ++head >= p.kv_heads) {
             head = 0;
-            ++seq;
-            q = next_q;
-            if (seq + 1 < p.batch) next_q = sequence(p, seq + 1);
+            if (++seq < p.batch) {
+              if (!fetched) next_raw = load_raw(p, seq);
+              q = sequence(p, next_raw);
+              fetched = seq + 1 < p.batch;
+              if (fetched) next_raw = load_raw(p, seq + 1);
+            }
           }
           continue;
         }
@@ -438,8 +513,9 @@ attention_kernel(const __grid_constant__ CUtensorMap map_q, const __grid_constan
         const int row = t * line.per, rows = min(line.per, q.n - row);
         const int end = max(q.off + row + rows, 0);
         const int tiles = max((end + kKeys - 1) / kKeys, 1);
-        const int64_t a = at >= x0 ? 0 : (x0 - at + kKeys - 1) / kKeys;
-        const int64_t b = at >= x1 ? 0 : (x1 - at + kKeys - 1) / kKeys;
+        const int64_t a = at >= x0 ? 0 : (x0 - at + kKeys - 1) >> 7;
+        const int64_t b = at >= x1 ? 0 : (x1 - at + kKeys - 1) >> 7;
+        static_assert(kKeys == 1 << 7, "shift");
         ++t;
         if (a >= tiles || b <= a) continue;
         r.it.row0 = q.begin + row;
@@ -450,8 +526,8 @@ attention_kernel(const __grid_constant__ CUtensorMap map_q, const __grid_constan
         r.it.first = (int)a;
         r.it.last = (int)min(b, (int64_t)tiles);
         r.it.slot = a > 0 ? 0 : b < tiles ? 1 : -1;
-        r.row = seq * p.ld_table;
-        r.begin = q.begin;
+        r.it.table = seq * p.ld_table;
+        r.it.begin = q.begin;
         if (a == 0 && b < tiles) {
           const int64_t last_tile = at + (int64_t)(tiles - 1) * kKeys, longer = rest * (each + 1);
           const int owner = (int)(last_tile < longer ? quotient(last_tile, each + 1) : rest + quotient(last_tile - longer, each));
@@ -461,61 +537,12 @@ attention_kernel(const __grid_constant__ CUtensorMap map_q, const __grid_constan
       }
       return r;
     };
-    // Where this lane's box of a tile lies: its page, and its first token there; how many boxes
-    // some row sees.  The others are not loaded: their scores are masked whatever they are, and
-    // P V stops before them.  (Boxes outside the cache, read as zeros, take the TMA unit about 1 us
-    // each.)
-    struct Place {
-      int page, token, count;
-    };
-    auto place_of = [&](const Part& r, int tile) -> Place {
-      const int j = tile * kKeys + lane * p.box;
-      const int count = min(max((r.it.end - tile * kKeys + p.box - 1) / p.box, 0), boxes);
-      if (lane >= count) return Place{0, 0, count};
-      if (p.table == nullptr) return Place{0, r.begin + j, count};
-      const int entry = p.page_shift >= 0 ? j >> p.page_shift : j / p.page_size;
-      const int id = ld_ro(p.table + r.row + entry);
-      return Place{id, j - entry * p.page_size, count};
-    };
-    int unit = 0;
-    auto load_tile = [&](const CUtensorMap* map, const Part& r, const Place& at) {
-      int page = at.page;
-      if (page < 0 || page >= p.pages) {
-        nvfp4::report(p.dev_status, NVFP4_ERR_INDEX);
-        page = p.pages;
-      }
-      const int head = uniform(r.it.head), count = uniform(at.count);
-#pragma unroll
-      for (int u = 0; u < kUnits; ++u) {
-        const int s = unit % kStages;
-        if (unit >= kStages) ok = ok && mbar_wait(empty(s), (unit / kStages - 1) & 1, abort, p.dev_status);
-        ok = __all_sync(0xFFFFFFFFu, ok);
-        if (!ok) return;
-        issued = unit + 1;
-        const bool withheld = nvfp4::kWithhold && blockIdx.x == 0 && unit == 0;  // test build: never issued
-        ++unit;
-        if (withheld) continue;
-        if (lead) mbar_arrive_expect_tx(full(s), (uint32_t)(count * p.box * 128 * kBlocks));
-        __syncwarp();
-        const uint32_t dst = ring + (uint32_t)(s * L::kUnitBytes);
-#pragma unroll
-        for (int i = 0; i < 8; ++i) {
-          if (i >= count) break;
-          const int pg = __shfl_sync(0xFFFFFFFFu, page, i), tk = __shfl_sync(0xFFFFFFFFu, at.token, i);
-#pragma unroll
-          for (int b = 0; b < kBlocks; ++b)
-            tma_load_4d(lead, dst + (uint32_t)(b * (kKeys * 128) + i * p.box * 128), map, u * L::kUnitDims + b * 64, head, tk,
-                        pg, full(s));
-        }
-      }
-    };
-    Part cur = advance(), prev{};
-    Place at{}, prev_at{};
-    if (cur.it.rows) at = place_of(cur, cur.it.first);
-    bool behind = false;  // a V is still to come
-    int count = 0, record = 0;
+    Part cur = advance();
+    Place at{};
+    if (cur.it.rows) at = place_of(cur.it, cur.it.first);
+    int record = 0;
     Part recorded{};
-    while (ok) {
+    for (int count = 0; ok; ++count) {
       const int i = count % kDescs;
       if (count >= kDescs) ok = mbar_wait(item_empty(i), (count / kDescs - 1) & 1, abort, p.dev_status);
       ok = __all_sync(0xFFFFFFFFu, ok);
@@ -525,7 +552,6 @@ attention_kernel(const __grid_constant__ CUtensorMap map_q, const __grid_constan
         mbar_arrive(item_full(i));
       }
       __syncwarp();
-      ++count;
       if (cur.it.rows == 0) break;
       if (cur.record) {
         record = cur.record;
@@ -533,46 +559,35 @@ attention_kernel(const __grid_constant__ CUtensorMap map_q, const __grid_constan
       }
       Part next{};
       for (int tile = cur.it.first; tile < cur.it.last && ok; ++tile) {
-        load_tile(&map_k, cur, at);
+        ok = load_tile(&map_k, std::integral_constant<int, L::kDimsK>(), 0, kK, cur.it.head, at);
         // the next tile's pages are on their way while this one's are loaded
-        Place next_at{};
         if (tile + 1 < cur.it.last) {
-          next_at = place_of(cur, tile + 1);
+          at = place_of(cur.it, tile + 1);
         } else {
           next = advance();
-          if (next.it.rows) next_at = place_of(next, next.it.first);
+          if (next.it.rows) at = place_of(next.it, next.it.first);
         }
-        if constexpr (NQ == 2) {
-          if (ok) load_tile(&map_v, cur, at);
-        } else {
-          // V one tile behind K, as the MMAs take them
-          if (ok && behind) load_tile(&map_v, prev, prev_at);
-          behind = true;
-          prev = cur;
-          prev_at = at;
-        }
-        at = next_at;
       }
       cur = next;
-    }
-    if (NQ == 1 && ok && behind) {
-      unit += kUnits;  // the place of a K that does not come: V's is the same for every tile
-      load_tile(&map_v, prev, prev_at);
     }
     if (lane == 0) {
       Record* rec = reinterpret_cast<Record*>(p.ws + (size_t)blockIdx.x * 64);
       *rec = Record{record, recorded.it.row0, recorded.it.rows, recorded.it.head};
     }
-  } else if (warp == 10) {
-    // ------------------------------------------------------------------ Q loads
+  } else if (warp == kWarpV) {
+    // ------------------------------------------------------------ Q and V loads
     for (int count = 0;; ++count) {
       const int i = count % kDescs;
       bool ok = mbar_wait(item_full(i), (count / kDescs) & 1, abort, p.dev_status);
       if (!__all_sync(0xFFFFFFFFu, ok)) break;
-      const int rows = uniform(items[i].rows), row0 = uniform(items[i].row0), head = uniform(items[i].head);
+      Item it = items[i];
+      it.row0 = uniform(it.row0);
+      it.head = uniform(it.head);
+      it.last = uniform(it.last);
       __syncwarp();
       if (lane == 0) mbar_arrive(item_empty(i));
-      if (rows == 0) break;
+      if (uniform(it.rows) == 0) break;
+      Place at = place_of(it, it.first);
       ok = count == 0 || mbar_wait(q_empty, (count - 1) & 1, abort, p.dev_status);
       if (!__all_sync(0xFFFFFFFFu, ok)) break;
       q_issued = count + 1;
@@ -582,21 +597,30 @@ attention_kernel(const __grid_constant__ CUtensorMap map_q, const __grid_constan
       for (int t = 0; t < NQ; ++t)
 #pragma unroll
         for (int b = 0; b < D / 64; ++b)
-          tma_load_4d(lead, q_smem + (uint32_t)(t * L::kQTile + b * (kRows * 128)), &map_q, b * 64, 0, head,
-                      row0 + t * per_tile, q_full);
+          tma_load_4d(lead, q_smem + (uint32_t)(t * L::kQTile + b * (kRows * 128)), &map_q, b * 64, 0, it.head,
+                      it.row0 + t * per_tile, q_full);
+      for (int tile = uniform(it.first); tile < it.last && ok; ++tile) {
+        const Place next = tile + 1 < it.last ? place_of(it, tile + 1) : Place{};
+        ok = load_tile(&map_v, std::integral_constant<int, L::kDimsV>(), kK, kV, it.head, at);
+        at = next;
+      }
+      if (!ok) break;
     }
-  } else if (warp == 8) {
+  } else if (warp == kMmaWarp) {
     // --------------------------------------------------------------------- MMAs
     // Steps g = 0, 1, ... over all items: NQ = 2: tile of keys g / 2, rows g % 2; NQ = 1: tile
-    // g.  S of step g into buffer g % 2.  Two cursors, S's two steps ahead.
-    constexpr uint32_t kIdescS = idesc_bf16(kKeys, false), kIdescO = idesc_bf16(L::kUnitDims, true);
+    // g.  S of step g into buffer g % 2.  Two cursors, S's two steps ahead: S of step g + 2 is
+    // issued behind P V of step g, which reads the same buffer.  (One warp for both tiles of rows:
+    // two fell into step, both softmaxes at once, then both products; 1.5 -> 2.2 ms.)
+    const uint32_t idesc_s = idesc_bf16(kKeys, false) | (p.negative ? 1u << 13 : 0u);  // (-Q: a negative scale)
+    constexpr uint32_t kIdescO = idesc_bf16(L::kDimsV, true);
     bool ok = true;
     struct Cursor {
-      int count, tile, first, last, end, rows, x;  // item, tile of it; tiles of the CTA before
-      int row_tile;
+      int count, tile, first, last, end, rows;  // items fetched; of the last of them
+      int x, row, g;                            // tiles before; tile of rows; step
     };
-    Cursor cs{}, cp{};
-    auto fetch = [&](Cursor& c, bool release) {  // the cursor's next item
+    Cursor cs{}, cp{};  // of S, of P V
+    auto fetch = [&](Cursor& c, bool release) {
       const int i = c.count % kDescs;
       ok = mbar_wait(item_full(i), (c.count / kDescs) & 1, abort, p.dev_status);
       ok = __all_sync(0xFFFFFFFFu, ok);
@@ -606,76 +630,65 @@ attention_kernel(const __grid_constant__ CUtensorMap map_q, const __grid_constan
       c.tile = c.first = uniform(it.first);
       c.last = uniform(it.last);
       c.end = uniform(it.end);
-      c.row_tile = 0;
       ++c.count;
       __syncwarp();
       if (release && lane == 0) mbar_arrive(item_empty(i));
     };
+    auto wait = [&](uint32_t bar, uint32_t phase) {
+      ok = ok && mbar_wait(bar, phase, abort, p.dev_status);
+      ok = __all_sync(0xFFFFFFFFu, ok);
+    };
     auto step = [&](Cursor& c, bool release) {
-      if (NQ == 2 && c.row_tile == 0) {
-        c.row_tile = 1;
+      ++c.g;
+      if (NQ == 2 && c.row == 0) {
+        c.row = 1;
         return;
       }
-      c.row_tile = 0;
+      c.row = 0;
       ++c.x;
       if (++c.tile == c.last) fetch(c, release);
     };
-    auto wait_unit = [&](int unit) {
-      ok = ok && mbar_wait(full(unit % kStages), (unit / kStages) & 1, abort, p.dev_status);
-      ok = __all_sync(0xFFFFFFFFu, ok);
-    };
-    int gs = 0;
     auto issue_s = [&]() {
-      if (cs.tile == cs.first && cs.row_tile == 0) {
-        ok = mbar_wait(q_full, (cs.count - 1) & 1, abort, p.dev_status);
-        ok = __all_sync(0xFFFFFFFFu, ok);
-        if (!ok) return;
-      }
-      const int u0 = NQ == 2 ? 2 * cs.x * kUnits : cs.x == 0 ? 0 : (2 * cs.x - 1) * kUnits;
-      const uint32_t d = tmem + (uint32_t)(gs & 1) * kKeys;
-      const bool last_use = NQ == 1 || cs.row_tile == 1;
+      if (cs.tile == cs.first && cs.row == 0) wait(q_full, (cs.count - 1) & 1);
+      const uint32_t d = tmem + (uint32_t)(cs.g & 1) * kKeys;
+      const bool last_use = cs.row == NQ - 1;
 #pragma unroll
-      for (int u = 0; u < kUnits; ++u) {
-        if (NQ == 1 || cs.row_tile == 0) wait_unit(u0 + u);
+      for (int u = 0; u < kUnitsK; ++u) {
+        const int unit = cs.x * kUnitsK + u, s = stage_k(unit);
+        if (cs.row == 0) wait(full(s), (unit / kK) & 1);
         if (!ok) return;
         tc_fence_after();
-        const uint32_t a = desc_low(q_smem + (uint32_t)(cs.row_tile * L::kQTile + u * kBlocks * (kRows * 128)));
-        const uint32_t b = desc_low(ring + (uint32_t)((u0 + u) % kStages * L::kUnitBytes));
+        constexpr int kBlocks = L::kDimsK / 64;
+        const uint32_t a = desc_low(q_smem + (uint32_t)(cs.row * L::kQTile + u * kBlocks * (kRows * 128)));
+        const uint32_t b = desc_low(ring + offset(s));
 #pragma unroll
         for (int c = 0; c < kBlocks; ++c)
-          mma_ss4(lead, d, a + c * (kRows * 128 >> 4), b + c * (kKeys * 128 >> 4), kIdescS, (u > 0 || c > 0) ? 1u : 0u);
-        if (u == kUnits - 1) commit(lead, s_full(gs & 1));
-        if (last_use) commit(lead, empty((u0 + u) % kStages));
+          mma_ss4(lead, d, a + c * (kRows * 128 >> 4), b + c * (kKeys * 128 >> 4), idesc_s, (u > 0 || c > 0) ? 1u : 0u);
+        if (u == kUnitsK - 1) commit(lead, s_full(cs.g & 1));
+        if (last_use) commit(lead, empty(s));
       }
       if (last_use && cs.tile + 1 == cs.last) commit(lead, q_empty);
-      ++gs;
       step(cs, false);
     };
-    int gp = 0;
     auto issue_pv = [&]() {
-      ok = mbar_wait(p_full(gp & 1), (gp >> 1) & 1, abort, p.dev_status);
-      ok = __all_sync(0xFFFFFFFFu, ok);
-      if (!ok) return;
-      const int u0 = NQ == 2 ? (2 * cp.x + 1) * kUnits : (2 * cp.x + 2) * kUnits;
-      const int seen = min(max(cp.end - cp.tile * kKeys, 1), kKeys);
-      const int steps = (seen + 15) / 16;  // of 16 keys
-      const uint32_t a = tmem + (uint32_t)(gp & 1) * kKeys;
-      const uint32_t o = tmem + 2 * kKeys + (uint32_t)(cp.row_tile * D);
-      const bool last_use = NQ == 1 || cp.row_tile == 1;
+      const int steps = (min(max(cp.end - cp.tile * kKeys, 1), kKeys) + 15) / 16;  // of 16 keys
+      const uint32_t a = tmem + (uint32_t)(cp.g & 1) * kKeys, o = tmem + 2 * kKeys + (uint32_t)(cp.row * D);
+      const bool last_use = cp.row == NQ - 1;
+      wait(p_full(cp.g & 1), (cp.g >> 1) & 1);
 #pragma unroll
-      for (int u = 0; u < kUnits; ++u) {
-        if (NQ == 1 || cp.row_tile == 0) wait_unit(u0 + u);
+      for (int u = 0; u < kUnitsV; ++u) {
+        const int unit = cp.x * kUnitsV + u, s = stage_v(unit);
+        if (cp.row == 0) wait(full(s), (unit / kV) & 1);
         if (!ok) return;
         tc_fence_after();
-        const uint32_t b = desc_low_v(ring + (uint32_t)((u0 + u) % kStages * L::kUnitBytes));
+        const uint32_t b = desc_low_v(ring + offset(s));
 #pragma unroll
         for (int h = 0; h < 2; ++h)
-          mma_ts4(lead, o + (uint32_t)(u * L::kUnitDims), a + 32 * h, b + 512 * h, kIdescO,
+          mma_ts4(lead, o + (uint32_t)(u * L::kDimsV), a + (NQ == 2 ? kKeys / 4 : kKeys / 2) * h, b + 512 * h, kIdescO,
                   (cp.tile > cp.first || h > 0) ? 1u : 0u, steps - 4 * h);
-        if (u == kUnits - 1) commit(lead, pv_done(gp & 1));
-        if (last_use) commit(lead, empty((u0 + u) % kStages));
+        if (u == kUnitsV - 1) commit(lead, pv_done(cp.g & 1));
+        if (last_use) commit(lead, empty(s));
       }
-      ++gp;
       step(cp, true);
     };
     fetch(cs, false);
@@ -687,15 +700,15 @@ attention_kernel(const __grid_constant__ CUtensorMap map_q, const __grid_constan
     }
   } else if (warp < kSoftmaxWarps) {
     // ------------------------------------------------------------------ softmax
-    if constexpr (NQ == 2) asm volatile("setmaxnreg.inc.sync.aligned.u32 208;");
-    constexpr int kCols = L::kCols, kOut = L::kOut;
-    const int group_of = warp >> 2;                                  // warpgroup
+    // NQ = 2: a row of one tile a thread.  NQ = 1: a row and half of the keys, and of O's columns.
+    constexpr int kCols = L::kCols, kOut = L::kOut, kChunks = kCols / 32;
+    const int half = warp >> 2;                                      // warpgroup
+    const int t = NQ == 2 ? half : 0;                                // tile of rows
     const int r = (warp & 3) * 32 + lane;                            // row of the tile
     const uint32_t lanes = tmem + ((uint32_t)((warp & 3) * 32) << 16);
-    const int t = NQ == 2 ? group_of : 0;
-    const int c0 = NQ == 2 ? 0 : group_of * kCols;
+    const int key0 = NQ == 2 ? 0 : half * kCols;  // first key of the thread's
     const int token = r / p.group, g = r - token * p.group;
-    const uint32_t o_addr = lanes + 2 * kKeys + (uint32_t)(t * D + (NQ == 1 ? group_of * kOut : 0));
+    const uint32_t o_addr = lanes + 2 * kKeys + (uint32_t)(NQ == 2 ? t * D : half * kOut);
     const float scale = p.scale;
     const uint64_t scale2 = pack2(__float_as_uint(scale), __float_as_uint(scale));
     // P V of the CTA's tile i is complete.  A barrier per buffer of S: the wait before last on
@@ -705,10 +718,25 @@ attention_kernel(const __grid_constant__ CUtensorMap map_q, const __grid_constan
     };
     bool ok = true;
     int x = 0, exchanges = 0;
-    for (int count = 0;; ++count) {  // (NQ = 1: the warps leave together, at an exchange)
+    // Whether to go on: NQ = 1: all warps alike, so that they leave together, at a barrier.
+    auto agree = [&]() {
+      if constexpr (NQ == 1)
+        ok = softmax_agree(ok);
+      else
+        ok = __all_sync(0xFFFFFFFFu, ok);
+    };
+    // NQ = 1: the other half's value of the row (two places in turn)
+    auto exchange = [&](float own) -> float {
+      float* at = xch + (exchanges & 1) * 2 * kRows + r;
+      ++exchanges;
+      at[half * kRows] = own;
+      agree();
+      return at[(half ^ 1) * kRows];
+    };
+    for (int count = 0;; ++count) {
       const int di = count % kDescs;
       ok = ok && mbar_wait(item_full(di), (count / kDescs) & 1, abort, p.dev_status);
-      ok = NQ == 1 ? softmax_agree(ok) : (bool)__all_sync(0xFFFFFFFFu, ok);
+      agree();
       if (!ok) break;
       const Item it = items[di];
       __syncwarp();
@@ -717,86 +745,66 @@ attention_kernel(const __grid_constant__ CUtensorMap map_q, const __grid_constan
       const bool valid = token < per_tile && t * per_tile + token < it.rows;
       const bool busy = __any_sync(0xFFFFFFFFu, valid);  // this warp has rows
       const int limit = valid ? it.pos0 + t * per_tile + token + 1 : 0x7FFFFFFF;  // keys that the row sees
-      float m = -INFINITY, l = 0.0f;
+      float m = -INFINITY, l = 0.0f, top = -INFINITY;
       for (int tile = it.first; tile < it.last; ++tile, ++x) {
         const int b = NQ == 2 ? t : x & 1;
         ok = ok && mbar_wait(s_full(b), (NQ == 2 ? x : x >> 1) & 1, abort, p.dev_status);
         if (NQ == 2) {
-          ok = __all_sync(0xFFFFFFFFu, ok);
+          agree();
           if (!ok) break;
         }
         tc_fence_after();
-        const uint32_t s_addr = lanes + (uint32_t)(b * kKeys + c0);
-        uint32_t s[kCols / 32][32];
-        float top = -INFINITY;
+        const uint32_t s_addr = lanes + (uint32_t)(b * kKeys + key0);  // (P goes over it, packed)
+        const int seen = limit - tile * kKeys - key0;
+        uint32_t s[kChunks][32];
+        top = -INFINITY;
         if (busy) {
 #pragma unroll
-          for (int c = 0; c < kCols / 32; ++c) tmem_issue(s_addr + 32 * c, s[c]);
+          for (int c = 0; c < kChunks; ++c) tmem_issue(s_addr + 32 * c, s[c]);
 #pragma unroll
-          for (int c = 0; c < kCols / 32; ++c) tmem_wait(s[c]);
-          if (p.negative) {
-#pragma unroll
-            for (int i = 0; i < kCols; ++i) s[i / 32][i % 32] ^= 0x80000000u;
-          }
-          const int seen = limit - tile * kKeys - c0;
+          for (int c = 0; c < kChunks; ++c) tmem_wait(s[c]);
           if (__any_sync(0xFFFFFFFFu, seen < kCols)) {
+            // (a bit a key, and only the 32s that some row does not see all of)
 #pragma unroll
-            for (int i = 0; i < kCols; ++i)
-              if (i >= seen) s[i / 32][i % 32] = 0xFF800000u;
+            for (int c = 0; c < kChunks; ++c) {
+              const int n = seen - 32 * c;
+              if (__any_sync(0xFFFFFFFFu, n < 32)) {
+                const uint32_t keep = n >= 32 ? 0xFFFFFFFFu : n <= 0 ? 0u : (1u << n) - 1u;
+#pragma unroll
+                for (int i = 0; i < 32; ++i)
+                  if (!(keep >> i & 1u)) s[c][i] = 0xFF800000u;
+              }
+            }
           }
-          float top4[4] = {-INFINITY, -INFINITY, -INFINITY, -INFINITY};
+          float most[4] = {-INFINITY, -INFINITY, -INFINITY, -INFINITY};
 #pragma unroll
           for (int i = 0; i < kCols; i += 8)
 #pragma unroll
             for (int e = 0; e < 4; ++e)
-              top4[e] = max3(top4[e], __uint_as_float(s[(i + 2 * e) / 32][(i + 2 * e) % 32]),
+              most[e] = max3(most[e], __uint_as_float(s[(i + 2 * e) / 32][(i + 2 * e) % 32]),
                              __uint_as_float(s[(i + 2 * e + 1) / 32][(i + 2 * e + 1) % 32]));
-          top = max3(fmaxf(top4[0], top4[1]), top4[2], top4[3]);
-          if (!valid) top = 0.0f;  // (no row: whatever S holds there, O is not rescaled for it)
+          // (no row: whatever S holds there, O is not rescaled for it)
+          top = valid ? max3(fmaxf(most[0], most[1]), most[2], most[3]) : 0.0f;
         }
         if constexpr (NQ == 1) {
-          float* at = xch + (exchanges & 1) * 2 * kRows + r;
-          ++exchanges;
-          at[group_of * kRows] = top;
-          ok = softmax_agree(ok);
+          top = fmaxf(top, exchange(top));
           if (!ok) break;
-          top = fmaxf(top, at[(group_of ^ 1) * kRows]);
         }
         if (busy) {
           // the reference maximum: raised for the whole warp once a row needs it
           const float raised = fmaxf(m, top);
-          const bool grow = (raised - m) * scale > kRescale;  // (no key seen yet, neither before: not a number)
-          if (__any_sync(0xFFFFFFFFu, grow)) {
-            const float keep = m == -INFINITY ? 0.0f : exp2_approx((m - raised) * scale);
+          const bool raise = __any_sync(0xFFFFFFFFu, (raised - m) * scale > kRescale);  // (no key seen: not a number)
+          float keep = 1.0f;
+          if (raise) {
+            keep = m == -INFINITY ? 0.0f : exp2_approx((m - raised) * scale);
             l *= keep;
             m = raised;
-            if (tile > it.first) {
-              ok = ok && wait_pv(x - 1);
-              ok = __all_sync(0xFFFFFFFFu, ok);
-              tc_fence_after();
-              const uint64_t keep2 = pack2(__float_as_uint(keep), __float_as_uint(keep));
-#pragma unroll 1
-              for (int c = 0; c < kOut; c += 16) {
-                uint32_t o[16];
-                tmem_issue(o_addr + c, o);
-                tmem_wait(o);
-#pragma unroll
-                for (int i = 0; i < 16; i += 2) {
-                  float lo, hi;
-                  unpack2(fma2(pack2(o[i], o[i + 1]), keep2, 0ull), lo, hi);
-                  o[i] = __float_as_uint(lo);
-                  o[i + 1] = __float_as_uint(hi);
-                }
-                tmem_store(o_addr + c, o);
-              }
-            }
           }
           const float shift = m == -INFINITY ? 0.0f : -m * scale;
           const uint64_t shift2 = pack2(__float_as_uint(shift), __float_as_uint(shift));
           uint64_t sum[2] = {0ull, 0ull};
-          const uint32_t p_addr = lanes + (uint32_t)(b * kKeys + c0 / 2);
 #pragma unroll
-          for (int c = 0; c < kCols / 32; ++c) {
+          for (int c = 0; c < kChunks; ++c) {
             uint32_t w[16];
 #pragma unroll
             for (int i = 0; i < 16; ++i) {
@@ -807,29 +815,53 @@ attention_kernel(const __grid_constant__ CUtensorMap map_q, const __grid_constan
               sum[i & 1] = add2(sum[i & 1], pack2(__float_as_uint(lo), __float_as_uint(hi)));
               w[i] = to_bf16x2(lo, hi);
             }
-            tmem_store(p_addr + 16 * c, w);
+            tmem_store(s_addr + 16 * c, w);
           }
           float s0f, s1f;
           unpack2(add2(sum[0], sum[1]), s0f, s1f);
           l += s0f + s1f;
+          if (raise && tile > it.first) {
+            ok = ok && wait_pv(x - 1);
+            ok = __all_sync(0xFFFFFFFFu, ok);
+            tc_fence_after();
+            const uint64_t keep2 = pack2(__float_as_uint(keep), __float_as_uint(keep));
+#pragma unroll 1
+            for (int c = 0; c < kOut; c += 32) {
+              uint32_t o[2][16];
+              tmem_issue(o_addr + c, o[0]);
+              tmem_issue(o_addr + c + 16, o[1]);
+              tmem_wait(o[0]);
+              tmem_wait(o[1]);
+#pragma unroll
+              for (int i = 0; i < 32; i += 2) {
+                float lo, hi;
+                unpack2(fma2(pack2(o[i / 16][i % 16], o[i / 16][i % 16 + 1]), keep2, 0ull), lo, hi);
+                o[i / 16][i % 16] = __float_as_uint(lo);
+                o[i / 16][i % 16 + 1] = __float_as_uint(hi);
+              }
+              tmem_store(o_addr + c, o[0]);
+              tmem_store(o_addr + c + 16, o[1]);
+            }
+          }
           tmem_store_wait();
         }
         // Values behind the last key that any row sees may be anything: zeros for those of
-        // them that the last 16 keys of P V take in.
-        if (tile * kKeys + kKeys > it.end && (NQ == 1 || t == 0)) {
+        // them that the last 16 keys of P V take in.  (NQ = 2: by the first tile of rows' threads:
+        // the second's P V is issued behind theirs.)
+        if (tile * kKeys + kKeys > it.end && t == 0) {
           const int from = max(it.end - tile * kKeys, 0), to = (max(from, 1) + 15) / 16 * 16;
-          const int u0 = NQ == 2 ? (2 * x + 1) * kUnits : (2 * x + 2) * kUnits;
-          const int threads = NQ == 2 ? 128 : 256, me = threadIdx.x % threads;
+          constexpr int threads = 32 * kSoftmaxWarps / NQ;
           // A stage's barrier tells this load from the one before only once that one is complete:
-          // it is S's or an earlier tile's, but with two units a tile and five stages V's of the
-          // tile before.
-          static_assert(kUnits == 1 || NQ == 1, "stages");
-          if (kUnits == 2 && x > 0) ok = ok && wait_pv(x - 1);
-          for (int u = 0; u < kUnits; ++u) {
-            ok = ok && mbar_wait(full((u0 + u) % kStages), ((u0 + u) / kStages) & 1, abort, p.dev_status);
-            unsigned char* v = ring_ptr + (u0 + u) % kStages * L::kUnitBytes;
+          // V's of three tiles before is, from S of this tile; with two units a tile and three
+          // stages it may be the tile's before.
+          if (kUnitsV == 2 && x > 0) ok = ok && wait_pv(x - 1);
+          constexpr int kBlocks = L::kDimsV / 64;
+          for (int u = 0; u < kUnitsV; ++u) {
+            const int unit = x * kUnitsV + u, sv = stage_v(unit);
+            ok = ok && mbar_wait(full(sv), (unit / kV) & 1, abort, p.dev_status);
+            unsigned char* v = ring_ptr + offset(sv);
             if (ok)
-              for (int i = from * 8 * kBlocks + me; i < to * 8 * kBlocks; i += threads) {
+              for (int i = from * 8 * kBlocks + (int)threadIdx.x; i < to * 8 * kBlocks; i += threads) {
                 const int key = i / (8 * kBlocks), piece = i % (8 * kBlocks);
                 *reinterpret_cast<uint4*>(v + piece / 8 * (kKeys * 128) + key * 128 + piece % 8 * 16) = make_uint4(0, 0, 0, 0);
               }
@@ -842,15 +874,11 @@ attention_kernel(const __grid_constant__ CUtensorMap map_q, const __grid_constan
       }
       if (NQ == 2 && !ok) break;
       // the part's end: O / l to the output, or (m, l, O) to the workspace
+      ok = ok && wait_pv(x - 1);
       if constexpr (NQ == 1) {
-        float* at = xch + (exchanges & 1) * 2 * kRows + r;
-        ++exchanges;
-        at[group_of * kRows] = l;
-        ok = softmax_agree(ok);
+        l += exchange(l);
         if (!ok) break;
-        l += at[(group_of ^ 1) * kRows];
       }
-      ok = wait_pv(x - 1);
       ok = __all_sync(0xFFFFFFFFu, ok);
       tc_fence_after();
       if (busy && ok) {
@@ -860,35 +888,46 @@ attention_kernel(const __grid_constant__ CUtensorMap map_q, const __grid_constan
         if (it.slot < 0) {
           norm = 1.0f / l;
           out = p.out + (int64_t)(it.row0 + t * per_tile + token) * p.ld_token + (it.head * p.group + g) * p.ld_head +
-                (NQ == 1 ? group_of * kOut : 0);
+                (NQ == 1 ? half * kOut : 0);
         } else {
           float* slot = reinterpret_cast<float*>(p.ws + kRecordBytes) + (2 * (int64_t)blockIdx.x + it.slot) * slot_floats(D, NQ);
           const int row = t * kRows + r;
-          if (valid && (NQ == 2 || group_of == 0)) *reinterpret_cast<float2*>(slot + 2 * row) = make_float2(m, l);
-          part = slot + 2 * NQ * kRows + (int64_t)row * D + (NQ == 1 ? group_of * kOut : 0);
+          if (valid && (NQ == 2 || half == 0)) *reinterpret_cast<float2*>(slot + 2 * row) = make_float2(m, l);
+          // eight columns of all rows, then the next eight: a warp's store is contiguous
+          part = slot + 2 * NQ * kRows + ((NQ == 1 ? half * (kOut / 8) * NQ * kRows : 0) + row) * 8;
         }
+        constexpr int kStep = kOut < 64 ? kOut : 64;
 #pragma unroll 1
-        for (int c = 0; c < kOut; c += 32) {
-          uint32_t o[32];
-          tmem_issue(o_addr + c, o);
-          tmem_wait(o);
+        for (int c0 = 0; c0 < kOut; c0 += kStep) {
+          uint32_t o[kStep / 32][32];
+#pragma unroll
+          for (int c = 0; c < kStep / 32; ++c) tmem_issue(o_addr + c0 + 32 * c, o[c]);
+#pragma unroll
+          for (int c = 0; c < kStep / 32; ++c) tmem_wait(o[c]);
           if (!valid) continue;
           if (part != nullptr) {
 #pragma unroll
-            for (int i = 0; i < 32; i += 4)
-              *reinterpret_cast<uint4*>(part + c + i) = make_uint4(o[i], o[i + 1], o[i + 2], o[i + 3]);
-          } else {
+            for (int c = 0; c < kStep; c += 8) store32(part + (c0 + c) * NQ * kRows, &o[c / 32][c % 32]);
+            continue;
+          }
 #pragma unroll
-            for (int i = 0; i < 32; i += 8) {
-              uint32_t w[4];
+          for (int c = 0; c < kStep / 32; ++c) {
+            uint32_t w[16];
 #pragma unroll
-              for (int e = 0; e < 4; ++e) {
-                // (a row that sees nothing: 0, whatever O holds)
-                const float lo = l != 0.0f ? __uint_as_float(o[i + 2 * e]) * norm : 0.0f;
-                const float hi = l != 0.0f ? __uint_as_float(o[i + 2 * e + 1]) * norm : 0.0f;
-                w[e] = to_bf16x2(lo, hi);
-              }
-              *reinterpret_cast<uint4*>(out + c + i) = make_uint4(w[0], w[1], w[2], w[3]);
+            for (int i = 0; i < 16; ++i) {
+              // (a row that sees nothing: 0, whatever O holds)
+              const float lo = l != 0.0f ? __uint_as_float(o[c][2 * i]) * norm : 0.0f;
+              const float hi = l != 0.0f ? __uint_as_float(o[c][2 * i + 1]) * norm : 0.0f;
+              w[i] = to_bf16x2(lo, hi);
+            }
+            __nv_bfloat16* dst = out + c0 + 32 * c;
+            if (p.wide) {
+              store32(dst, w);
+              store32(dst + 16, w + 8);
+            } else {
+#pragma unroll
+              for (int i = 0; i < 16; i += 4)
+                *reinterpret_cast<uint4*>(dst + 2 * i) = make_uint4(w[i], w[i + 1], w[i + 2], w[i + 3]);
             }
           }
         }
@@ -899,17 +938,21 @@ attention_kernel(const __grid_constant__ CUtensorMap map_q, const __grid_constan
   __syncthreads();
   if (*abort) {
     // A wait ran out: what is in flight lands (bounded) before TMEM and shared memory go.
-    if (warp == 9 && lane == 0)
-      for (int u = issued > kStages ? issued - kStages : 0; u < issued; ++u)
-        mbar_drain(full(u % kStages), (uint32_t)(u / kStages) & 1u, p.dev_status);
-    if (warp == 10 && lane == 0 && q_issued > 0) mbar_drain(q_full, (uint32_t)(q_issued - 1) & 1u, p.dev_status);
-    if (warp == 8 && lead) {
+    if (warp == kWarpK && lane == 0)
+      for (int u = issued > kK ? issued - kK : 0; u < issued; ++u)
+        mbar_drain(full(stage_k(u)), (uint32_t)(u / kK) & 1u, p.dev_status);
+    if (warp == kWarpV && lane == 0) {
+      for (int u = issued > kV ? issued - kV : 0; u < issued; ++u)
+        mbar_drain(full(stage_v(u)), (uint32_t)(u / kV) & 1u, p.dev_status);
+      if (q_issued > 0) mbar_drain(q_full, (uint32_t)(q_issued - 1) & 1u, p.dev_status);
+    }
+    if (warp == kMmaWarp && lead) {
       mma_commit(drain_bar);
       mbar_drain(drain_bar, 0u, p.dev_status);
     }
     __syncthreads();
   }
-  if (warp == 8) {
+  if (warp == kMmaWarp) {
     __syncwarp();
     tc_fence_after();
     asm volatile("tcgen05.dealloc.cta_group::1.sync.aligned.b32 %0, %1;" ::"r"(tmem), "r"(512) : "memory");
@@ -928,15 +971,15 @@ constexpr int kJoinFew = 8;  // parts that one warp takes
 
 template <int D, int NQ>
 __global__ void __launch_bounds__(32 * kJoinWarps) attention_join_kernel(const __grid_constant__ Params p) {
-  constexpr int E = D / 64;  // float2 of a lane
-  __shared__ float2 acc[kJoinWarps][D / 2];
+  constexpr int kQuads = D / 4, E = (kQuads + 31) / 32;  // float4 of a row, of a lane
+  __shared__ float4 acc[kJoinWarps][kQuads];
   __shared__ float weights[ATTENTION_MAX_CTAS];
   nvfp4::wait_for_previous_kernel();
   const int c = blockIdx.x, warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
   const Record rec = *reinterpret_cast<const Record*>(p.ws + (size_t)c * 64);
   const int parts = rec.parts, rows = rec.rows * p.group;
   if (parts <= 0) return;
-  const int per_tile = kRows / p.group;
+  const int per_tile = p.per_tile;
   const bool few = parts <= kJoinFew;
   const float* slots = reinterpret_cast<const float*>(p.ws + kRecordBytes) + 2 * (int64_t)c * slot_floats(D, NQ);
   // part 0 is the first CTA's second place, the others are the next CTAs' first
@@ -971,38 +1014,47 @@ __global__ void __launch_bounds__(32 * kJoinWarps) attention_join_kernel(const _
 #pragma unroll
     for (int d = 16; d; d >>= 1) total += __shfl_xor_sync(0xFFFFFFFFu, total, d);
     if (!few) __syncthreads();
-    float2 o[E];
+    float4 o[E];
 #pragma unroll
-    for (int e = 0; e < E; ++e) o[e] = make_float2(0.0f, 0.0f);
+    for (int e = 0; e < E; ++e) o[e] = make_float4(0.0f, 0.0f, 0.0f, 0.0f);
+    auto add = [](float4& a, const float4& v, float w) {
+      a.x += v.x * w;
+      a.y += v.y * w;
+      a.z += v.z * w;
+      a.w += v.w * w;
+    };
 #pragma unroll 4
     for (int k = first; k < last; ++k) {
       const float w = few ? __shfl_sync(0xFFFFFFFFu, w0, k) : weights[k];
-      const float2* src = reinterpret_cast<const float2*>(slot_of(k) + 2 * NQ * kRows + (int64_t)row * D) + lane;
+      const float* src = slot_of(k) + 2 * NQ * kRows + row * 8;
 #pragma unroll
       for (int e = 0; e < E; ++e) {
-        const float2 v = src[32 * e];
-        o[e].x += w != 0.0f ? v.x * w : 0.0f;
-        o[e].y += w != 0.0f ? v.y * w : 0.0f;
+        const int quad = lane + 32 * e;  // (half of eight columns)
+        float4 v = make_float4(0.0f, 0.0f, 0.0f, 0.0f);
+        if (quad < kQuads && w != 0.0f)
+          v = *reinterpret_cast<const float4*>(src + (int64_t)(quad / 2) * (NQ * kRows * 8) + quad % 2 * 4);
+        add(o[e], v, w);
       }
     }
     const float norm = 1.0f / total;
-    uint32_t* out = reinterpret_cast<uint32_t*>(p.out + (int64_t)(rec.row0 + token) * p.ld_token +
-                                                (rec.head * p.group + g) * p.ld_head);
+    uint2* out = reinterpret_cast<uint2*>(p.out + (int64_t)(rec.row0 + token) * p.ld_token + (rec.head * p.group + g) * p.ld_head);
+    auto finish = [&](const float4& v) {
+      return total != 0.0f ? make_uint2(to_bf16x2(v.x * norm, v.y * norm), to_bf16x2(v.z * norm, v.w * norm)) : make_uint2(0u, 0u);
+    };
     if (few) {
 #pragma unroll
-      for (int e = 0; e < E; ++e) out[lane + 32 * e] = total != 0.0f ? to_bf16x2(o[e].x * norm, o[e].y * norm) : 0u;
+      for (int e = 0; e < E; ++e)
+        if (lane + 32 * e < kQuads) out[lane + 32 * e] = finish(o[e]);
     } else {
 #pragma unroll
-      for (int e = 0; e < E; ++e) acc[warp][lane + 32 * e] = o[e];
+      for (int e = 0; e < E; ++e)
+        if (lane + 32 * e < kQuads) acc[warp][lane + 32 * e] = o[e];
       __syncthreads();
-      if (threadIdx.x < D / 2) {
-        float2 sum = make_float2(0.0f, 0.0f);
+      if (threadIdx.x < kQuads) {
+        float4 sum = make_float4(0.0f, 0.0f, 0.0f, 0.0f);
 #pragma unroll
-        for (int w = 0; w < kJoinWarps; ++w) {
-          sum.x += acc[w][threadIdx.x].x;
-          sum.y += acc[w][threadIdx.x].y;
-        }
-        out[threadIdx.x] = total != 0.0f ? to_bf16x2(sum.x * norm, sum.y * norm) : 0u;
+        for (int w = 0; w < kJoinWarps; ++w) add(sum, acc[w][threadIdx.x], 1.0f);
+        out[threadIdx.x] = finish(sum);
       }
       __syncthreads();
     }
@@ -1035,6 +1087,8 @@ int launch(const paged_attention_input& in, const attn_rows& out, void* workspac
   p.batch = (int)in.batch;
   p.kv_heads = (int)in.kv_heads;
   p.group = (int)(in.heads / in.kv_heads);
+  p.per_tile = kRows / p.group;
+  p.per_item = NQ * p.per_tile;
   p.page_size = (int)in.page_size;
   p.page_shift = -1;
   for (int i = 4; i < 17; ++i)
@@ -1049,6 +1103,7 @@ int launch(const paged_attention_input& in, const attn_rows& out, void* workspac
   p.out = static_cast<__nv_bfloat16*>(out.data);
   p.ld_token = out.ld_token;
   p.ld_head = out.ld_head;
+  p.wide = reinterpret_cast<uintptr_t>(out.data) % 32 == 0 && out.ld_token % 16 == 0 && out.ld_head % 16 == 0;
   p.ws = static_cast<unsigned char*>(workspace);
   p.dev_status = dev_status;
 
