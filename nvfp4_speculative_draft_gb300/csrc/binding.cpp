@@ -452,10 +452,28 @@ int64_t number(PyObject* o) {
   if (x == -1 && PyErr_Occurred()) throw python_error();
   return x;
 }
-// An int32 vector, given or made.
-Tensor vector_or_new(PyObject* o, const char* name, at::Device dev, int64_t n) {
-  return o != Py_None ? need_vector(o, name, at::kInt, dev, n) : make({n}, at::kInt, dev);
-}
+// int32 vectors, given or made: those that are made share one allocation, 64 bytes aligned.
+struct Vectors {
+  static constexpr int64_t kAlign = 16;
+  int64_t words = 0;
+  Tensor all;
+  int64_t add(PyObject* o, const char* name, at::Device dev, int64_t n) {
+    if (o != Py_None) {
+      need_vector(o, name, at::kInt, dev, n);
+      return -1;
+    }
+    const int64_t at = words;
+    words += (n + kAlign - 1) / kAlign * kAlign;
+    return at;
+  }
+  Tensor get(PyObject* o, int64_t at, int64_t n) const {
+    if (at < 0) return *tensor_of(o);
+    Tensor t = at::detail::make_tensor<c10::TensorImpl>(c10::Storage(all.storage()), all.key_set(), all.dtype());
+    t.unsafeGetTensorImpl()->set_storage_offset(at);
+    t.unsafeGetTensorImpl()->set_sizes_contiguous({n});
+    return t;
+  }
+};
 
 // plan(lens, num_new, block_table, free_pages, free_count, page_size, tokens, held | None,
 //      cu_new | None, kv_lens | None, positions | None, slots | None, held_out | None,
@@ -485,12 +503,15 @@ PyObject* plan(PyObject*, PyObject* const* a, Py_ssize_t nargs) {
   if (in.tokens < 0 || in.tokens > 0x7FFFFFFF) throw Refusal("tokens must be in 0 .. 2^31 - 1");
   if (a[7] != Py_None) in.held = need_vector(a[7], "held", at::kInt, dev, in.batch).data_ptr<int32_t>();
   const Call call(dev, a[14], a[15]);
-  const Tensor cu = vector_or_new(a[8], "cu_new", dev, in.batch + 1);
-  const Tensor kv = vector_or_new(a[9], "kv_lens", dev, in.batch);
-  const Tensor positions = vector_or_new(a[10], "positions", dev, in.tokens);
-  const Tensor slots = vector_or_new(a[11], "slots", dev, in.tokens);
-  const Tensor held = vector_or_new(a[12], "held_out", dev, in.batch);
-  const Tensor count = vector_or_new(a[13], "free_count_out", dev, 1);
+  const char* names[6] = {"cu_new", "kv_lens", "positions", "slots", "held_out", "free_count_out"};
+  const int64_t sizes[6] = {in.batch + 1, in.batch, in.tokens, in.tokens, in.batch, 1};
+  Vectors made;
+  int64_t where[6];
+  for (int i = 0; i < 6; ++i) where[i] = made.add(a[8 + i], names[i], dev, sizes[i]);
+  if (made.words > 0) made.all = make({made.words}, at::kInt, dev);
+  Tensor v[6];
+  for (int i = 0; i < 6; ++i) v[i] = made.get(a[8 + i], where[i], sizes[i]);
+  const Tensor &cu = v[0], &kv = v[1], &positions = v[2], &slots = v[3], &held = v[4], &count = v[5];
   const kv_plan_output out{cu.data_ptr<int32_t>(),    kv.data_ptr<int32_t>(),   positions.data_ptr<int32_t>(),
                            slots.data_ptr<int32_t>(), held.data_ptr<int32_t>(), count.data_ptr<int32_t>()};
   const int rc = lib.plan(&in, &out, &call.ex);

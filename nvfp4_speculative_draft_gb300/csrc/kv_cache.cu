@@ -17,13 +17,17 @@ namespace cg = cooperative_groups;
 // of one cluster for itself, in shared memory, and tokens and pages are then shared
 // out evenly, each finding its sequence by bisection.  All reads that an in-place call
 // overwrites come before the cluster's barrier, all writes behind it.
+//
+// What bounds it is the chain of dependent steps (launch, the lengths' load, two prefix
+// sums, bisection, the table's load), not the bytes.
 
-constexpr int kPlanThreads = 512;
+constexpr int kPlanThreads = 1024;
 constexpr int kPlanWarps = kPlanThreads / 32;
 
 struct PlanParams {
   kv_plan_input in;
   kv_plan_output out;
+  int page_shift;  // log2 of the page size, or -1
   int32_t* dev_status;
 };
 
@@ -40,15 +44,29 @@ __device__ __forceinline__ T block_scan(T v, T* warp_sums, T& total) {
   __syncthreads();  // the sums of the scan before are read
   if (lane == 31) warp_sums[warp] = sum;
   __syncthreads();
-  T before = 0;
-  total = 0;
+  T before = lane < kPlanWarps ? warp_sums[lane] : 0;  // (every warp sums the warps' sums)
+  total = before;
 #pragma unroll
-  for (int w = 0; w < kPlanWarps; ++w) {
-    const T x = warp_sums[w];
-    if (w < warp) before += x;
-    total += x;
+  for (int d = 1; d < 32; d <<= 1) {
+    const T o = __shfl_up_sync(0xFFFFFFFFu, total, d);
+    if (lane >= d) total += o;
   }
+  before = __shfl_sync(0xFFFFFFFFu, total - before, warp);
+  total = __shfl_sync(0xFFFFFFFFu, total, 31);
   return before + sum - v;
+}
+
+// The smallest of the CTA's values.
+__device__ __forceinline__ int64_t block_min(int64_t v, int64_t* warp_values) {
+#pragma unroll
+  for (int d = 16; d; d >>= 1) v = min(v, (int64_t)__shfl_xor_sync(0xFFFFFFFFu, v, d));
+  __syncthreads();
+  if ((threadIdx.x & 31) == 0) warp_values[threadIdx.x >> 5] = v;
+  __syncthreads();
+  v = warp_values[threadIdx.x & 31];
+#pragma unroll
+  for (int d = 16; d; d >>= 1) v = min(v, (int64_t)__shfl_xor_sync(0xFFFFFFFFu, v, d));
+  return v;
 }
 
 // Last s in [0, batch) with start[s] <= i (start ascends, start[0] <= i).
@@ -64,16 +82,20 @@ __device__ __forceinline__ int find_sequence(const int32_t* start, int batch, in
   return lo;
 }
 
-__global__ void __launch_bounds__(kPlanThreads) kv_plan_kernel(const __grid_constant__ PlanParams p) {
+static_assert(kPlanWarps == 32, "a lane a warp");
+
+__global__ void __launch_bounds__(kPlanThreads, 1) kv_plan_kernel(const __grid_constant__ PlanParams p) {
   extern __shared__ int32_t plan_smem[];
   __shared__ int64_t sums64[kPlanWarps];
   const int batch = (int)p.in.batch, page = (int)p.in.page_size;
   const int64_t tokens = p.in.tokens, width = p.in.max_pages;
-  // per sequence: first token, first extra page, cached length, held pages; -1 - held where refused
+  // per sequence: first token, first extra page, cached length, held pages; -1 - held where
+  // refused (until then: new tokens, need, cached length, held pages)
   int32_t* const s_token = plan_smem;
   int32_t* const s_page = plan_smem + batch;
   int32_t* const s_len = plan_smem + 2 * batch;
   int32_t* const s_held = plan_smem + 3 * batch;
+  auto pages_of = [&](uint32_t n) { return p.page_shift >= 0 ? n >> p.page_shift : n / (uint32_t)page; };
   nvfp4::wait_for_previous_kernel();
 
   cg::cluster_group cluster = cg::this_cluster();
@@ -88,57 +110,54 @@ __global__ void __launch_bounds__(kPlanThreads) kv_plan_kernel(const __grid_cons
   const int run = (batch + kPlanThreads - 1) / kPlanThreads;
   const int first = min(batch, (int)threadIdx.x * run), last = min(batch, first + run);
   int64_t mine = 0;
-  for (int s = first; s < last; ++s) mine += max(nvfp4::ld_ro(p.in.num_new + s), 0);
+  for (int s = first; s < last; ++s) {
+    const int32_t n = max(nvfp4::ld_ro(p.in.num_new + s), 0), len = max(nvfp4::ld_ro(p.in.lens + s), 0);
+    const int32_t given = p.in.held != nullptr ? max(nvfp4::ld_ro(p.in.held + s), 0) : 0;
+    const int64_t have = p.in.held != nullptr ? given : pages_of((uint32_t)len + (uint32_t)page - 1u);
+    s_token[s] = n;
+    s_len[s] = len;
+    s_held[s] = (int32_t)min(have, width);
+    mine += n;
+  }
   int64_t total;
   int64_t at = block_scan<int64_t>(mine, sums64, total);
   const int32_t used = (int32_t)min(total, tokens);
-  // pages wanted by the sequences that fit their table's row and the tokens
-  auto wanted = [&](int s, int64_t start, int32_t& n, int32_t& len, int32_t& held, bool& fits) -> int64_t {
-    n = max(nvfp4::ld_ro(p.in.num_new + s), 0);
-    len = max(nvfp4::ld_ro(p.in.lens + s), 0);
-    const int64_t least = ((int64_t)len + page - 1) / page;
-    const int64_t have = p.in.held != nullptr ? max(nvfp4::ld_ro(p.in.held + s), 0) : least;
-    held = (int32_t)min(have, width);
-    const int64_t need = n > 0 ? ((int64_t)len + n + page - 1) / page : 0;
-    fits = n == 0 || (need <= width && start + n <= tokens && (int64_t)len + n <= 0x7FFFFFFF);
-    return fits && need > held ? need - held : 0;
-  };
+  // pages wanted by the sequences that fit their table's row and the tokens; -1: does not fit
   int64_t extra = 0;
   {
     int64_t start = at;
     for (int s = first; s < last; ++s) {
-      int32_t n, len, held;
-      bool fits;
-      extra += wanted(s, start, n, len, held, fits);
-      start += n;
+      const int32_t n = s_token[s], held = s_held[s];
+      int32_t want = 0;
+      if (n > 0) {
+        const uint32_t length = (uint32_t)s_len[s] + (uint32_t)n;  // (two int32: no overflow)
+        const int64_t need = length <= 0x7FFFFFFFu ? pages_of(length + (uint32_t)page - 1u) : (int64_t)width + 1;
+        want = need > width || start + n > tokens ? -1 : (int32_t)max(need - held, (int64_t)0);
+        start += n;
+      }
+      s_page[s] = want;
+      if (want > 0) extra += want;
     }
   }
   int64_t all_extra;
   int64_t upto = block_scan<int64_t>(extra, sums64, all_extra);
   int64_t taken = 0;  // pages taken by this thread's run, counted from the stack's top
   for (int s = first; s < last; ++s) {
-    int32_t n, len, held;
-    bool fits;
-    const int64_t e = wanted(s, at, n, len, held, fits);
-    const bool ok = fits && (e == 0 || upto + e <= left);
+    const int32_t want = s_page[s], n = s_token[s], e = max(want, 0);
+    const bool ok = want >= 0 && (e == 0 || upto + e <= left);
     s_token[s] = (int32_t)min(at, tokens);
     s_page[s] = (int32_t)min(upto, left);
-    s_len[s] = len;
-    s_held[s] = ok ? held : -1 - held;
-    if (!ok) error = NVFP4_ERR_PAGES;
+    if (!ok) {
+      s_held[s] = -1 - s_held[s];
+      error = NVFP4_ERR_PAGES;
+    }
     at += n;
     upto += e;
     if (ok && e > 0) taken = upto;
   }
   if (error) nvfp4::report(p.dev_status, error);
   // the most that any sequence took up to (its prefix counts those before it, which all got theirs)
-  __syncthreads();
-  __shared__ unsigned long long most;
-  if (threadIdx.x == 0) most = 0ull;
-  __syncthreads();
-  if (taken > 0) atomicMax(&most, (unsigned long long)taken);
-  __syncthreads();
-  taken = (int64_t)most;
+  taken = -block_min(-taken, sums64);
   cluster.sync();
 
   const int me = rank * kPlanThreads + (int)threadIdx.x, step = ranks * kPlanThreads;
@@ -146,7 +165,7 @@ __global__ void __launch_bounds__(kPlanThreads) kv_plan_kernel(const __grid_cons
     const int32_t next = s + 1 < batch ? s_token[s + 1] : used;
     const int32_t held = s_held[s] < 0 ? -1 - s_held[s] : s_held[s];
     const int64_t n = s_held[s] < 0 ? 0 : next - s_token[s];
-    const int64_t kv = s_len[s] + n, need = n > 0 ? (kv + page - 1) / page : 0;
+    const int64_t kv = s_len[s] + n, need = n > 0 ? pages_of((uint32_t)kv + (uint32_t)page - 1u) : 0;
     p.out.cu_new[s + 1] = next;
     p.out.kv_lens[s] = (int32_t)kv;
     if (p.out.held != nullptr) p.out.held[s] = (int32_t)max((int64_t)held, need);
@@ -168,10 +187,10 @@ __global__ void __launch_bounds__(kPlanThreads) kv_plan_kernel(const __grid_cons
       position = (int32_t)min(at_kv, (int64_t)0x7FFFFFFF);
       const int32_t held = s_held[s];
       if (held >= 0) {
-        const int32_t entry = position / page;
+        const int32_t entry = (int32_t)pages_of((uint32_t)position);
         const int32_t id = entry < held ? p.in.block_table[s * p.in.ld_table + entry]
                                         : top[-((int64_t)s_page[s] + entry - held)];
-        const int64_t where = (int64_t)id * page + position % page;
+        const int64_t where = (int64_t)id * page + (position - entry * page);
         if (id >= 0 && where <= 0x7FFFFFFF)
           slot = (int32_t)where;
         else
@@ -193,7 +212,6 @@ __global__ void __launch_bounds__(kPlanThreads) kv_plan_kernel(const __grid_cons
 // rounding to BF16.
 
 constexpr int kRopeThreads = 256;
-constexpr int kRopeTokens = 4;  // tokens of a CTA
 
 struct RopeParams {
   rope_kv_input in;
@@ -230,16 +248,53 @@ __device__ __forceinline__ void rotate(uint4& a, uint4& b, const float2* cs) {
   b = make_uint4(y[0], y[1], y[2], y[3]);
 }
 
+// A CTA takes TOKENS tokens (and a share of their vectors), a thread the same vectors of all of
+// them: their loads are in flight together, the first ones while the sines are formed.
+template <int TOKENS>
 __global__ void __launch_bounds__(kRopeThreads) rope_kv_kernel(const __grid_constant__ RopeParams p) {
-  __shared__ float2 angles[kRopeTokens][ROPE_MAX_DIM / 2];
-  __shared__ int64_t k_at[kRopeTokens], v_at[kRopeTokens];
+  __shared__ __align__(16) float2 angles[TOKENS][ROPE_MAX_DIM / 2];
+  __shared__ int64_t k_at[TOKENS], v_at[TOKENS];
   const rope_kv_input& in = p.in;
   const int half = (int)in.rot_dim / 2, dim = (int)in.dim;
-  const int64_t t0 = (int64_t)blockIdx.x * kRopeTokens;
-  const int count = (int)min(in.tokens - t0, (int64_t)kRopeTokens);
+  const int64_t t0 = (int64_t)blockIdx.x * TOKENS;
+  const int count = (int)min(in.tokens - t0, (int64_t)TOKENS);
+  const bool cached = in.k_cache.data != nullptr;
+  // items: 16 elements of a (token, head): the two ends of eight pairs, or two neighbouring vectors
+  const int per_head = dim / 16, rot_items = half / 8;
+  const int q_heads = (int)in.heads, k_heads = q_heads + (int)in.kv_heads;
+  const int all = k_heads + (cached ? (int)in.kv_heads : 0);
+  const int items = all * per_head, step = kRopeThreads * (int)gridDim.y;
+
+  const __nv_bfloat16* src = nullptr;  // of token t0
+  int64_t ld_src = 0;
+  int h = 0, i = 0, lo = 0, hi = 0;
+  uint4 a[TOKENS], b[TOKENS];
+  auto locate = [&](int w) {
+    h = w / per_head;
+    i = w - h * per_head;
+    const bool turn = i < rot_items && h < k_heads;
+    lo = turn ? 8 * i : h < k_heads ? 2 * half + 16 * (i - rot_items) : 16 * i;
+    hi = lo + (turn ? half : 8);
+    const attn_rows& r = h < q_heads ? in.q : h < k_heads ? in.k : in.v;
+    const int head = h < q_heads ? h : h < k_heads ? h - q_heads : h - k_heads;
+    ld_src = r.ld_token;
+    src = (const __nv_bfloat16*)r.data + t0 * ld_src + head * r.ld_head;
+  };
+  auto load = [&]() {
+#pragma unroll
+    for (int t = 0; t < TOKENS; ++t) {
+      if (t < count) {
+        a[t] = load16(src + t * ld_src + lo);
+        b[t] = load16(src + t * ld_src + hi);
+      }
+    }
+  };
+  int w = (int)blockIdx.y * kRopeThreads + (int)threadIdx.x;
+  if (w < items) locate(w);
   nvfp4::wait_for_previous_kernel();
-  for (int i = threadIdx.x; i < count * half; i += kRopeThreads) {
-    const int t = i / half, j = i - t * half;
+  if (w < items) load();
+  for (int x = threadIdx.x; x < count * half; x += kRopeThreads) {
+    const int t = x / half, j = x - t * half;
     const int axis = in.axis != nullptr ? in.axis[j] : 0;
     const int64_t position = nvfp4::ld_ro(in.positions + (axis < in.axes ? axis : 0) * in.ld_positions + t0 + t);
     const uint64_t turns = (uint64_t)position * in.turns[j];
@@ -247,7 +302,6 @@ __global__ void __launch_bounds__(kRopeThreads) rope_kv_kernel(const __grid_cons
     sincospif((float)(int32_t)(turns >> 32) * 0x1p-31f, &s, &c);
     angles[t][j] = make_float2(c, s);
   }
-  const bool cached = in.k_cache.data != nullptr;
   if (cached && (int)threadIdx.x < count) {
     const int32_t slot = nvfp4::ld_ro(in.slots + t0 + threadIdx.x);
     const int32_t page = slot / (int32_t)in.page_size, off = slot - page * (int32_t)in.page_size;
@@ -257,51 +311,37 @@ __global__ void __launch_bounds__(kRopeThreads) rope_kv_kernel(const __grid_cons
     v_at[threadIdx.x] = ok ? page * in.v_cache.ld_page + off * in.v_cache.ld_token : -1;
   }
   __syncthreads();
-  // items: 16 elements of a (token, head): the two ends of eight pairs, or two neighbouring vectors
-  const int per_head = dim / 16, rot_items = half / 8;
-  const int q_heads = (int)in.heads, k_heads = q_heads + (int)in.kv_heads;
-  const int all = k_heads + (in.v.data != nullptr && cached ? (int)in.kv_heads : 0);
-  const int per_token = all * per_head;
-  for (int t = 0; t < count; ++t) {
-    const int64_t token = t0 + t;
-    for (int w = (int)blockIdx.y * kRopeThreads + (int)threadIdx.x; w < per_token; w += kRopeThreads * (int)gridDim.y) {
-      const int h = w / per_head, i = w - h * per_head;
-      const bool turn = i < rot_items && h < k_heads;
-      int lo, hi;
-      if (turn) {
-        lo = 8 * i;
-        hi = half + 8 * i;
-      } else {
-        lo = h < k_heads ? 2 * half + 16 * (i - rot_items) : 16 * i;
-        hi = lo + 8;
-      }
-      const __nv_bfloat16* src;
-      __nv_bfloat16 *dst = nullptr, *cache = nullptr;
-      if (h < q_heads) {
-        src = (const __nv_bfloat16*)in.q.data + token * in.q.ld_token + h * in.q.ld_head;
-        dst = (__nv_bfloat16*)p.out.q.data + token * p.out.q.ld_token + h * p.out.q.ld_head;
-      } else if (h < k_heads) {
-        const int kh = h - q_heads;
-        src = (const __nv_bfloat16*)in.k.data + token * in.k.ld_token + kh * in.k.ld_head;
-        if (p.out.k.data != nullptr) dst = (__nv_bfloat16*)p.out.k.data + token * p.out.k.ld_token + kh * p.out.k.ld_head;
-        if (cached && k_at[t] >= 0) cache = (__nv_bfloat16*)in.k_cache.data + k_at[t] + kh * in.k_cache.ld_head;
-      } else {
-        const int vh = h - k_heads;
-        src = (const __nv_bfloat16*)in.v.data + token * in.v.ld_token + vh * in.v.ld_head;
-        if (v_at[t] >= 0) cache = (__nv_bfloat16*)in.v_cache.data + v_at[t] + vh * in.v_cache.ld_head;
-      }
-      if (!turn && dst == src) dst = nullptr;  // in place: what is not rotated stays
-      if (dst == nullptr && cache == nullptr) continue;
-      uint4 a = load16(src + lo), b = load16(src + hi);
-      if (turn) rotate(a, b, &angles[t][8 * i]);
+  while (w < items) {
+    const bool turn = i < rot_items && h < k_heads;
+    // where it goes: a tensor's rows (not what an in-place call leaves as it is), the cache's pages
+    const attn_rows& r = h < q_heads ? p.out.q : p.out.k;
+    const int head = h < q_heads ? h : h < k_heads ? h - q_heads : h - k_heads;
+    __nv_bfloat16* dst = nullptr;
+    if (h < k_heads && r.data != nullptr) {
+      dst = (__nv_bfloat16*)r.data + t0 * r.ld_token + head * r.ld_head;
+      if (!turn && dst == src) dst = nullptr;
+    }
+    const kv_pages& c = h < k_heads ? in.k_cache : in.v_cache;
+    const int64_t* slots = h < k_heads ? k_at : v_at;
+    const bool caching = cached && h >= q_heads;
+#pragma unroll
+    for (int t = 0; t < TOKENS; ++t) {
+      if (t >= count) continue;
+      if (turn) rotate(a[t], b[t], &angles[t][8 * i]);
       if (dst != nullptr) {
-        store16(dst + lo, a);
-        store16(dst + hi, b);
+        store16(dst + t * r.ld_token + lo, a[t]);
+        store16(dst + t * r.ld_token + hi, b[t]);
       }
-      if (cache != nullptr) {
-        store16(cache + lo, a);
-        store16(cache + hi, b);
+      if (caching && slots[t] >= 0) {
+        __nv_bfloat16* at = (__nv_bfloat16*)c.data + slots[t] + head * c.ld_head;
+        store16(at + lo, a[t]);
+        store16(at + hi, b[t]);
       }
+    }
+    w += step;
+    if (w < items) {
+      locate(w);
+      load();
     }
   }
 }
@@ -309,7 +349,9 @@ __global__ void __launch_bounds__(kRopeThreads) rope_kv_kernel(const __grid_cons
 }  // namespace
 
 int launch_kv_plan(const kv_plan_input* in, const kv_plan_output* out, int32_t* dev_status, cudaStream_t stream) {
-  PlanParams p{*in, *out, dev_status};
+  PlanParams p{*in, *out, -1, dev_status};
+  for (int i = 0; i < 17; ++i)
+    if (in->page_size == (int64_t)1 << i) p.page_shift = i;
   const size_t smem = (size_t)in->batch * 16;
   if (nvfp4::occupancy((const void*)kv_plan_kernel, kPlanThreads, smem) < 1) return NVFP4_ERR_CUDA;
   // one CTA while each thread has a few tokens at most, else a cluster of eight
@@ -324,11 +366,18 @@ int launch_kv_plan(const kv_plan_input* in, const kv_plan_output* out, int32_t* 
 int launch_rope_kv_write(const rope_kv_input* in, const rope_kv_output* out, int32_t* dev_status,
                          cudaStream_t stream) {
   RopeParams p{*in, *out, dev_status};
-  const int64_t groups = nvfp4::cdiv(in->tokens, kRopeTokens);
+  // Four tokens a CTA where that leaves each SM four CTAs; fewer tokens one by one, their vectors
+  // over several CTAs.
+  const int sms = nvfp4::sm_count();
+  const bool many = in->tokens >= (int64_t)16 * sms;
+  const int64_t groups = many ? nvfp4::cdiv(in->tokens, 4) : in->tokens;
   if (groups > 0x7FFFFFFF) return NVFP4_ERR_SHAPE;
+  const int64_t items = (in->heads + (in->k_cache.data != nullptr ? 2 : 1) * in->kv_heads) * (in->dim / 16);
+  const int64_t parts = many ? 1 : nvfp4::cdiv(items, kRopeThreads);
   void* args[] = {&p};
-  return nvfp4::launch_dependent((const void*)rope_kv_kernel, dim3((unsigned)groups), dim3(kRopeThreads), 0, stream, 1,
-                                 args) == cudaSuccess
+  const void* kern = many ? (const void*)rope_kv_kernel<4> : (const void*)rope_kv_kernel<1>;
+  return nvfp4::launch_dependent(kern, dim3((unsigned)groups, (unsigned)(parts < 64 ? parts : 64)), dim3(kRopeThreads), 0,
+                                 stream, 1, args) == cudaSuccess
              ? NVFP4_OK
              : NVFP4_ERR_CUDA;
 }
