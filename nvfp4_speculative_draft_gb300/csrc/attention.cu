@@ -53,7 +53,7 @@ constexpr int kSoftmaxWarps = 8;
 constexpr int kThreads = 32 * (kSoftmaxWarps + 4);  // (three of the last four work)
 constexpr int kDescs = 4;                     // item descriptors in flight
 constexpr int kItemCost = kKeys;              // an item's fixed cost, in keys
-constexpr int kMinShare = 160;                // of a CTA, where there is that little
+constexpr int kMinShare = kKeys;              // of a CTA, where there is that little
 constexpr float kRescale = 8.0f;              // log2 of what the maximum may lag behind
 constexpr float kLog2e = 1.4426950408889634f;
 
