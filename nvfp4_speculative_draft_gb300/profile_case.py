@@ -12,7 +12,11 @@ workspace),
 weight variant of the 151936 x 5120 head); the verify step: ``fp8b_quantize``
 (17408 x 5120), ``fp8b_rmsnorm`` (8192 x 5120 with residual), ``fp8b_gemm`` (M=--m
 below 65 against 5120 x 10240, else against 17408 x 5120), ``spec_verify``
-(64 sequences, 4 drafts, 151936 FP32 probabilities).  Inputs are prepared first (their kernels run
+(64 sequences, 4 drafts, 151936 FP32 probabilities); the attention step:
+``kv_plan`` (1000 requests), ``rope_kv_write`` (8192 tokens, 40 + 2 x 8 heads of 128),
+``prompt_attention`` (one prompt of 4096 tokens, 32 / 8 heads of 128), ``paged_attention``
+(32 sequences of 4000 cached tokens, --m new ones each, 32 / 8 heads of 128, pages of
+16).  Inputs are prepared first (their kernels run
 before the measured calls, so ``ncu -k regex:<kernel> -s <n>`` can skip them),
 then the call runs --iters times and the process exits 0.
 """
@@ -34,7 +38,8 @@ def main():
     ap.add_argument("--case", required=True,
                     choices=["lm_head", "propose", "propose_fp8", "fc", "gemm", "gemm_f16", "quantize",
                              "quantize_fp8", "fp8b_quantize", "fp8b_rmsnorm", "fp8b_gemm",
-                             "spec_verify"])
+                             "spec_verify", "kv_plan", "rope_kv_write", "prompt_attention",
+                             "paged_attention"])
     ap.add_argument("--m", type=int, default=1)
     ap.add_argument("--iters", type=int, default=3)
     args = ap.parse_args()
@@ -123,6 +128,41 @@ def main():
         torch.cuda.synchronize()
         for _ in range(args.iters):
             nd.spec_verify(p, tok, u, r, draft_probs=q)
+    elif args.case == "kv_plan":
+        g = torch.Generator(device=dev).manual_seed(1)
+        b, page = 1000, 16
+        lens = torch.randint(1, 16000, (b,), generator=g, device=dev, dtype=torch.int32)
+        new = torch.randint(0, 50, (b,), generator=g, device=dev, dtype=torch.int32)
+        table = torch.zeros((b, 1010), dtype=torch.int32, device=dev)
+        free, count = torch.arange(8000, dtype=torch.int32, device=dev), torch.full((1,), 8000, dtype=torch.int32, device=dev)
+        tokens = int(new.sum())
+        torch.cuda.synchronize()
+        for _ in range(args.iters):
+            nd.kv_plan(lens, new, table, free, count, page, tokens)
+    elif args.case == "rope_kv_write":
+        t, hq, hk, d = 8192, 40, 8, 128
+        q, k, v = torch.randn((t, hq + 2 * hk, d), device=dev).to(torch.bfloat16).split([hq, hk, hk], 1)
+        kc, vc = (torch.zeros((t // 16, 16, hk, d), dtype=torch.bfloat16, device=dev) for _ in range(2))
+        pos, table = torch.arange(t, dtype=torch.int32, device=dev), nd.rotary_table(d, device=dev)
+        torch.cuda.synchronize()
+        for _ in range(args.iters):
+            nd.rope_kv_write(q, k, v, pos, table, kc, vc, pos)
+    elif args.case == "prompt_attention":
+        q, k, v = (torch.randn((4096, h, 128), device=dev).to(torch.bfloat16) for h in (32, 8, 8))
+        cu = torch.tensor([0, 4096], dtype=torch.int32, device=dev)
+        torch.cuda.synchronize()
+        for _ in range(args.iters):
+            nd.prompt_attention(q, k, v, cu)
+    elif args.case == "paged_attention":
+        b, kv, page = 32, 4000, 16
+        kc, vc = (torch.randn((b * kv // page, page, 8, 128), device=dev).to(torch.bfloat16) for _ in range(2))
+        table = torch.randperm(b * kv // page, device=dev).to(torch.int32).view(b, -1)
+        q = torch.randn((b * args.m, 32, 128), device=dev).to(torch.bfloat16)
+        cu = torch.arange(0, b * args.m + 1, args.m, dtype=torch.int32, device=dev)
+        lens = torch.full((b,), kv, dtype=torch.int32, device=dev)
+        torch.cuda.synchronize()
+        for _ in range(args.iters):
+            nd.paged_attention(q, kc, vc, table, lens, cu)
     else:
         c = workloads.prefill_gemm(m=128, device=dev)
         torch.cuda.synchronize()
