@@ -1109,6 +1109,8 @@ int launch(const paged_attention_input& in, const attn_rows& out, void* workspac
   void* args[] = {&mq, &mk, &mv, &p};
   if (nvfp4::launch_dependent(kern, dim3(grid), dim3(kThreads), L::kSmemBytes, stream, 1, args) != cudaSuccess)
     return NVFP4_ERR_CUDA;
+  // (an item of one tile of keys is no border's)
+  if ((in.block_table != nullptr ? capacity : in.tokens) <= kKeys) return NVFP4_OK;
   void* join_args[] = {&p};
   if (nvfp4::launch_dependent((const void*)attention_join_kernel<D, NQ>, dim3(grid, 8 * NQ), dim3(32 * kJoinWarps), 0, stream, 1,
                               join_args) != cudaSuccess)

@@ -233,12 +233,14 @@ __device__ __forceinline__ uint32_t pack_bf16(float lo, float hi) {
   return *reinterpret_cast<const uint32_t*>(&b);
 }
 
-// Eight pairs: a = elements i.., b = elements half + i..
-__device__ __forceinline__ void rotate(uint4& a, uint4& b, const float2* cs) {
+// Eight pairs: a = elements 8 i.., b = elements half + 8 i..; cs: cosines and sines of two of the
+// pairs, then of the next two `items` further on (so that neighbouring threads read neighbouring
+// words).
+__device__ __forceinline__ void rotate(uint4& a, uint4& b, const float4* cs, int items) {
   uint32_t x[4] = {a.x, a.y, a.z, a.w}, y[4] = {b.x, b.y, b.z, b.w};
 #pragma unroll
   for (int j = 0; j < 4; ++j) {
-    const float4 t = reinterpret_cast<const float4*>(cs)[j];  // cos, sin of two pairs
+    const float4 t = cs[j * items];
     const float x0 = __uint_as_float(x[j] << 16), x1 = __uint_as_float(x[j] & 0xFFFF0000u);
     const float y0 = __uint_as_float(y[j] << 16), y1 = __uint_as_float(y[j] & 0xFFFF0000u);
     x[j] = pack_bf16(x0 * t.x - y0 * t.y, x1 * t.z - y1 * t.w);
@@ -300,7 +302,7 @@ __global__ void __launch_bounds__(kRopeThreads) rope_kv_kernel(const __grid_cons
     const uint64_t turns = (uint64_t)position * in.turns[j];
     float s, c;
     sincospif((float)(int32_t)(turns >> 32) * 0x1p-31f, &s, &c);
-    angles[t][j] = make_float2(c, s);
+    angles[t][2 * (j % 8 / 2 * rot_items + j / 8) + j % 2] = make_float2(c, s);
   }
   if (cached && (int)threadIdx.x < count) {
     const int32_t slot = nvfp4::ld_ro(in.slots + t0 + threadIdx.x);
@@ -327,7 +329,7 @@ __global__ void __launch_bounds__(kRopeThreads) rope_kv_kernel(const __grid_cons
 #pragma unroll
     for (int t = 0; t < TOKENS; ++t) {
       if (t >= count) continue;
-      if (turn) rotate(a[t], b[t], &angles[t][8 * i]);
+      if (turn) rotate(a[t], b[t], reinterpret_cast<const float4*>(angles[t]) + i, rot_items);
       if (dst != nullptr) {
         store16(dst + t * r.ld_token + lo, a[t]);
         store16(dst + t * r.ld_token + hi, b[t]);
