@@ -60,9 +60,8 @@ constexpr float kLog2e = 1.4426950408889634f;
 template <int D, int NQ>
 struct Tile {
   // Units of the rings: 128 keys of as many dims.
-  static constexpr int kDimsK = D < 128 ? D : 128, kDimsV = kDimsK;
-  static constexpr int kUnitsK = D / kDimsK, kUnitsV = D / kDimsV;  // of a tile
-  static constexpr int kBytesK = kKeys * kDimsK * 2, kBytesV = kKeys * kDimsV * 2;
+  static constexpr int kDims = D < 128 ? D : 128, kUnits = D / kDims;  // (units of a tile)
+  static constexpr int kBytes = kKeys * kDims * 2;
   static constexpr int kQTile = kRows * D * 2;
   static constexpr int kQBytes = NQ * kQTile;
   static constexpr int kXchBytes = NQ == 1 ? 2 * 2 * kRows * 4 : 0;
@@ -72,12 +71,12 @@ struct Tile {
   static constexpr int kRest = kXchBytes + kDescBytes + 512;
   static constexpr int kFit = 227 * 1024 - kQBytes - kRest;
   static constexpr int kStagesV = D == 64 ? 5 : 3;
-  static constexpr int kLeft = (kFit - kStagesV * kBytesV) / kBytesK;
+  static constexpr int kLeft = kFit / kBytes - kStagesV;
   static constexpr int kStagesK = kLeft < 5 ? kLeft : 5;
-  static constexpr int kStages = kStagesK + kStagesV, kRing = kStagesK * kBytesK + kStagesV * kBytesV;
+  static constexpr int kStages = kStagesK + kStagesV, kRing = kStages * kBytes;
   static constexpr size_t kSmemBytes = (size_t)kQBytes + kRing + kRest;
-  static_assert(kStagesK >= 2 && kStagesK >= kUnitsK && kStagesV > kUnitsV, "rings");
-  static_assert(kBytesK % 1024 == 0 && kBytesV % 1024 == 0, "swizzled tiles start on 1 KB");
+  static_assert(kStagesK >= 2 && kStagesK >= kUnits && kStagesV > kUnits, "rings");
+  static_assert(kBytes % 1024 == 0, "swizzled tiles start on 1 KB");
   static_assert(2 * kKeys + NQ * D <= 512, "TMEM");
 };
 
@@ -235,9 +234,11 @@ __device__ __forceinline__ void tmem_store(uint32_t taddr, const uint32_t (&v)[1
       "r"(v[10]), "r"(v[11]), "r"(v[12]), "r"(v[13]), "r"(v[14]), "r"(v[15])
       : "memory");
 }
-// 32 bytes to one address: whole sectors
+// 32 bytes to one address: whole sectors.  Past the L1, where a warp's store of 32 rows would
+// take a line each: 8192 tokens 32/8/128 407 -> 389 us, 32/4/256 875 -> 839 us, packed prompts
+// 88 -> 80 us.
 __device__ __forceinline__ void store32(void* p, const uint32_t* v) {
-  asm volatile("st.global.v8.b32 [%0], {%1, %2, %3, %4, %5, %6, %7, %8};" ::"l"(p), "r"(v[0]), "r"(v[1]), "r"(v[2]),
+  asm volatile("st.global.L1::no_allocate.v8.b32 [%0], {%1, %2, %3, %4, %5, %6, %7, %8};" ::"l"(p), "r"(v[0]), "r"(v[1]), "r"(v[2]),
                "r"(v[3]), "r"(v[4]), "r"(v[5]), "r"(v[6]), "r"(v[7])
                : "memory");
 }
@@ -290,7 +291,7 @@ __global__ void __launch_bounds__(kThreads, 1)
 attention_kernel(const __grid_constant__ CUtensorMap map_q, const __grid_constant__ CUtensorMap map_k,
                  const __grid_constant__ CUtensorMap map_v, const __grid_constant__ Params p) {
   using L = Tile<D, NQ>;
-  constexpr int kStages = L::kStages, kUnitsK = L::kUnitsK, kUnitsV = L::kUnitsV;
+  constexpr int kStages = L::kStages, kUnits = L::kUnits;
   constexpr int kMmaWarp = kSoftmaxWarps, kWarpK = kMmaWarp + 1, kWarpV = kMmaWarp + 2;
   extern __shared__ __align__(1024) unsigned char smem[];
   unsigned char* const ring_ptr = smem + L::kQBytes;
@@ -304,7 +305,7 @@ attention_kernel(const __grid_constant__ CUtensorMap map_q, const __grid_constan
   auto empty = [&](int s) { return bars + 8u * (kStages + s); };
   auto stage_k = [&](int unit) { return unit % kK; };
   auto stage_v = [&](int unit) { return kK + unit % kV; };
-  auto offset = [&](int s) { return (uint32_t)(s < kK ? s * L::kBytesK : kK * L::kBytesK + (s - kK) * L::kBytesV); };
+  auto offset = [&](int s) { return (uint32_t)(s * L::kBytes); };
   auto item_full = [&](int i) { return bars + 8u * (2 * kStages + i); };
   auto item_empty = [&](int i) { return bars + 8u * (2 * kStages + kDescs + i); };
   constexpr int kFixed = 2 * kStages + 2 * kDescs;
@@ -360,13 +361,13 @@ attention_kernel(const __grid_constant__ CUtensorMap map_q, const __grid_constan
   constexpr uint32_t tmem = 0;
   if (*tmem_slot != tmem) nvfp4::report(p.dev_status, NVFP4_ERR_CUDA);
   const int per_tile = p.per_tile;
-  int issued = 0, q_issued = 0;          // units and Q loads issued (TMA warps)
+  int issued = 0, q_issued = 0;          // units and Q loads issued (the loading warps)
   const uint32_t lead = elect_one();     // the lane that issues for a warp
   nvfp4::wait_for_previous_kernel();
 
-  // Loads of K and V, a warp each, all lanes together.  Where this lane's box of a tile
-  // lies: its page, and its first token there; how many boxes some row sees (the others are not
-  // loaded: their scores are masked whatever they are, and P V stops before them).
+  // Where this lane's box of a tile lies: its page, and its first token there; how many boxes
+  // some row sees (the others are not loaded: their scores are masked whatever they are, and P V
+  // stops before them).
   struct Place {
     int page, token, count;
   };
@@ -380,46 +381,54 @@ attention_kernel(const __grid_constant__ CUtensorMap map_q, const __grid_constan
     const int id = ld_ro(p.table + it.table + entry);
     return Place{id, j - entry * p.page_size, count};
   };
-  auto load_tile = [&](const CUtensorMap* map, auto dims, int first_stage, int stages, int key_head, const Place& at) -> bool {
-    constexpr int kDims = decltype(dims)::value, kBlocks = kDims / 64;  // swizzled columns of 128 bytes
-    int page = at.page;
-    if (page < 0 || page >= p.pages) {
-      nvfp4::report(p.dev_status, NVFP4_ERR_INDEX);
-      page = p.pages;  // (read as zeros)
-    }
-    const int head = uniform(key_head), count = uniform(at.count);
-#pragma unroll
-    for (int u = 0; u < D / kDims; ++u) {
-      const int s = first_stage + issued % stages;
-      const bool ok = issued < stages || mbar_wait(empty(s), (issued / stages - 1) & 1, abort, p.dev_status);
-      if (!__all_sync(0xFFFFFFFFu, ok)) return false;
-      const bool withheld = nvfp4::kWithhold && blockIdx.x == 0 && first_stage == 0 && issued == 0;  // (test build)
-      ++issued;
-      if (withheld) continue;
-      if (lead) mbar_arrive_expect_tx(full(s), (uint32_t)(count * p.box * 128 * kBlocks));
-      __syncwarp();
-      const uint32_t dst = ring + offset(s);
-#pragma unroll 1
-      for (int i = 0; i < count; ++i) {
-        const int pg = __shfl_sync(0xFFFFFFFFu, page, i), tk = __shfl_sync(0xFFFFFFFFu, at.token, i);
-#pragma unroll
-        for (int b = 0; b < kBlocks; ++b)
-          tma_load_4d(lead, dst + (uint32_t)(b * (kKeys * 128) + i * p.box * 128), map, u * kDims + b * 64, head, tk, pg,
-                      full(s));
-      }
-    }
-    return true;
-  };
-
-  if (warp == kWarpK) {
-    // ------------------------------------------------------- schedule, K loads
+  if (warp == kWarpK || warp == kWarpV) {
+    // ----------------------------------------- K and V loads, a warp each, all lanes together;
+    // that of K finds the items, that of V loads their Q
+    const bool keys = warp == kWarpK;
+    const CUtensorMap* const map = keys ? &map_k : &map_v;
+    const int ring0 = keys ? 0 : kK, stages = keys ? kK : kV;
+    int slot = 0, phase = 1;  // of the warp's ring
     bool ok = true;
+    auto load_tile = [&](int key_head, const Place& at) {
+      int page = at.page;
+      if (page < 0 || page >= p.pages) {
+        nvfp4::report(p.dev_status, NVFP4_ERR_INDEX);
+        page = p.pages;  // (read as zeros)
+      }
+      const int head = uniform(key_head), count = uniform(at.count);
+      constexpr int kBlocks = L::kDims / 64;  // swizzled columns of 128 bytes
+#pragma unroll 1
+      for (int u = 0; u < kUnits; ++u) {
+        const int s = uniform(ring0 + slot);
+        ok = mbar_wait(empty(s), phase, abort, p.dev_status);  // (the first round passes: phase 1 is before 0)
+        ok = __all_sync(0xFFFFFFFFu, ok);
+        if (!ok) return;
+        if (++slot == stages) {
+          slot = 0;
+          phase ^= 1;
+        }
+        const bool withheld = nvfp4::kWithhold && blockIdx.x == 0 && keys && issued == 0;  // (test build)
+        ++issued;
+        if (withheld) continue;
+        if (lead) mbar_arrive_expect_tx(full(s), (uint32_t)(count * p.box * 128 * kBlocks));
+        __syncwarp();
+        const uint32_t dst = ring + offset(s);
+#pragma unroll 1
+        for (int i = 0; i < count; ++i) {
+          const int pg = __shfl_sync(0xFFFFFFFFu, page, i), tk = __shfl_sync(0xFFFFFFFFu, at.token, i);
+#pragma unroll
+          for (int b = 0; b < kBlocks; ++b)
+            tma_load_4d(lead, dst + (uint32_t)(b * (kKeys * 128) + i * p.box * 128), map, u * L::kDims + b * 64, head, tk,
+                        pg, full(s));
+        }
+      }
+    };
     // This CTA's share [x0, x1) of the line: a lane a sequence.  (By this warp alone: the others
     // get their items from it, and a pass over 32 sequences takes less than the block's barriers
     // and loads up to some hundreds of them.)
     int64_t total = 0, chunk = 0;  // of all sequences; this lane's of the first 32
     Sequence q{};
-    for (int s = lane; s < p.batch; s += 32) {
+    for (int s = lane; keys && s < p.batch; s += 32) {
       const Raw raw = load_raw(p, s);
       const Sequence x = sequence(p, raw);
       const int64_t length = p.kv_heads * Line(x, p.per_item).length;
@@ -443,7 +452,7 @@ attention_kernel(const __grid_constant__ CUtensorMap map_q, const __grid_constan
     const int64_t x0 = border((int)blockIdx.x), x1 = border((int)blockIdx.x + 1);
     int seq = p.batch, head = 0, t = 0;
     int64_t head_at = 0;
-    if (x0 < x1) {  // the sequence, head and item that x0 lies in
+    if (keys && x0 < x1) {  // the sequence, head and item that x0 lies in
       int64_t at = 0;
       int who = 0;
       for (int base = 0; base < p.batch; base += 32) {
@@ -539,19 +548,37 @@ attention_kernel(const __grid_constant__ CUtensorMap map_q, const __grid_constan
       }
       return r;
     };
-    Part cur{};
-    Place at{};
-    int record = 0, count = 0, tile = 0;
-    Part recorded{};
+    Part cur{}, recorded{};
+    int record = 0, count = 0, tile = 0;  // items; tile whose place comes next
+    Place at{};                           // of the tile before it, once there is one
+    bool have = false;
     for (;;) {
-      if (count > 0) {
-        ok = load_tile(&map_k, std::integral_constant<int, L::kDimsK>(), 0, kK, cur.it.head, at);
+      const bool more = tile < cur.it.last;
+      Place next{};  // (on its way while the tile before is loaded)
+      if (more) next = place_of(cur.it, tile++);
+      if (have) {
+        load_tile(cur.it.head, at);
         if (!ok) break;
+      } else if (!keys && more) {
+        if (count > 1) ok = mbar_wait(q_empty, count & 1, abort, p.dev_status);
+        if (!__all_sync(0xFFFFFFFFu, ok)) break;
+        q_issued = count;
+        if (lead) mbar_arrive_expect_tx(q_full, (uint32_t)(NQ * (D / 64) * per_tile * p.group * 128));
+        __syncwarp();
+        const int head = uniform(cur.it.head), row0 = uniform(cur.it.row0);
+#pragma unroll
+        for (int t = 0; t < NQ; ++t)
+#pragma unroll
+          for (int b = 0; b < D / 64; ++b)
+            tma_load_4d(lead, q_smem + (uint32_t)(t * L::kQTile + b * (kRows * 128)), &map_q, b * 64, 0, head,
+                        row0 + t * per_tile, q_full);
       }
-      if (count == 0 || ++tile == cur.it.last) {  // the next item
-        const int i = count % kDescs;
+      at = next;
+      have = more;
+      if (more) continue;
+      const int i = count % kDescs;  // the next item
+      if (keys) {
         cur = advance();
-        tile = cur.it.first;
         if (count >= kDescs) ok = mbar_wait(item_empty(i), (count / kDescs - 1) & 1, abort, p.dev_status);
         ok = __all_sync(0xFFFFFFFFu, ok);
         if (!ok) break;
@@ -560,50 +587,24 @@ attention_kernel(const __grid_constant__ CUtensorMap map_q, const __grid_constan
           mbar_arrive(item_full(i));
         }
         __syncwarp();
-        ++count;
-        if (cur.it.rows == 0) break;
         if (cur.record) {
           record = cur.record;
           recorded = cur;
         }
+      } else {
+        ok = mbar_wait(item_full(i), (count / kDescs) & 1, abort, p.dev_status);
+        if (!__all_sync(0xFFFFFFFFu, ok)) break;
+        cur.it = items[i];
+        __syncwarp();
+        if (lane == 0) mbar_arrive(item_empty(i));
       }
-      at = place_of(cur.it, tile);
+      ++count;
+      if (uniform(cur.it.rows) == 0) break;
+      tile = uniform(cur.it.first);
     }
-    if (lane == 0) {
+    if (keys && lane == 0) {
       Record* rec = reinterpret_cast<Record*>(p.ws + (size_t)blockIdx.x * 64);
       *rec = Record{record, recorded.it.row0, recorded.it.rows, recorded.it.head};
-    }
-  } else if (warp == kWarpV) {
-    // ------------------------------------------------------------ Q and V loads
-    for (int count = 0;; ++count) {
-      const int i = count % kDescs;
-      bool ok = mbar_wait(item_full(i), (count / kDescs) & 1, abort, p.dev_status);
-      if (!__all_sync(0xFFFFFFFFu, ok)) break;
-      Item it = items[i];
-      it.row0 = uniform(it.row0);
-      it.head = uniform(it.head);
-      it.last = uniform(it.last);
-      __syncwarp();
-      if (lane == 0) mbar_arrive(item_empty(i));
-      if (uniform(it.rows) == 0) break;
-      Place at = place_of(it, it.first);
-      ok = count == 0 || mbar_wait(q_empty, (count - 1) & 1, abort, p.dev_status);
-      if (!__all_sync(0xFFFFFFFFu, ok)) break;
-      q_issued = count + 1;
-      if (lead) mbar_arrive_expect_tx(q_full, (uint32_t)(NQ * (D / 64) * per_tile * p.group * 128));
-      __syncwarp();
-#pragma unroll
-      for (int t = 0; t < NQ; ++t)
-#pragma unroll
-        for (int b = 0; b < D / 64; ++b)
-          tma_load_4d(lead, q_smem + (uint32_t)(t * L::kQTile + b * (kRows * 128)), &map_q, b * 64, 0, it.head,
-                      it.row0 + t * per_tile, q_full);
-      for (int tile = uniform(it.first); tile < it.last && ok; ++tile) {
-        const Place next = tile + 1 < it.last ? place_of(it, tile + 1) : Place{};
-        ok = load_tile(&map_v, std::integral_constant<int, L::kDimsV>(), kK, kV, it.head, at);
-        at = next;
-      }
-      if (!ok) break;
     }
   } else if (warp == kMmaWarp) {
     // --------------------------------------------------------------------- MMAs
@@ -612,7 +613,7 @@ attention_kernel(const __grid_constant__ CUtensorMap map_q, const __grid_constan
     // issued behind P V of step g, which reads the same buffer.  (One warp for both tiles of rows:
     // two fell into step, both softmaxes at once, then both products; 1.5 -> 2.2 ms.)
     const uint32_t idesc_s = idesc_bf16(kKeys, false) | (p.negative ? 1u << 13 : 0u);  // (-Q: a negative scale)
-    constexpr uint32_t kIdescO = idesc_bf16(L::kDimsV, true);
+    constexpr uint32_t kIdescO = idesc_bf16(L::kDims, true);
     bool ok = true;
     struct Cursor {
       int count, tile, first, last, end, rows;  // items fetched; of the last of them
@@ -651,19 +652,19 @@ attention_kernel(const __grid_constant__ CUtensorMap map_q, const __grid_constan
       if (cs.tile == cs.first && cs.row == 0) wait(q_full, (cs.count - 1) & 1);
       const uint32_t d = tmem + (uint32_t)(cs.g & 1) * kKeys;
       const bool last_use = cs.row == NQ - 1;
-#pragma unroll
-      for (int u = 0; u < kUnitsK; ++u) {
-        const int unit = cs.x * kUnitsK + u, s = stage_k(unit);
+#pragma unroll 1
+      for (int u = 0; u < kUnits; ++u) {
+        const int unit = cs.x * kUnits + u, s = stage_k(unit);
         if (cs.row == 0) wait(full(s), (unit / kK) & 1);
         if (!ok) return;
         tc_fence_after();
-        constexpr int kBlocks = L::kDimsK / 64;
+        constexpr int kBlocks = L::kDims / 64;
         const uint32_t a = desc_low(q_smem + (uint32_t)(cs.row * L::kQTile + u * kBlocks * (kRows * 128)));
         const uint32_t b = desc_low(ring + offset(s));
 #pragma unroll
         for (int c = 0; c < kBlocks; ++c)
           mma_ss4(lead, d, a + c * (kRows * 128 >> 4), b + c * (kKeys * 128 >> 4), idesc_s, (u > 0 || c > 0) ? 1u : 0u);
-        if (u == kUnitsK - 1) commit(lead, s_full(cs.g & 1));
+        if (u == kUnits - 1) commit(lead, s_full(cs.g & 1));
         if (last_use) commit(lead, empty(s));
       }
       if (last_use && cs.tile + 1 == cs.last) commit(lead, q_empty);
@@ -674,18 +675,18 @@ attention_kernel(const __grid_constant__ CUtensorMap map_q, const __grid_constan
       const uint32_t a = tmem + (uint32_t)(cp.g & 1) * kKeys, o = tmem + 2 * kKeys + (uint32_t)(cp.row * D);
       const bool last_use = cp.row == NQ - 1;
       wait(p_full(cp.g & 1), (cp.g >> 1) & 1);
-#pragma unroll
-      for (int u = 0; u < kUnitsV; ++u) {
-        const int unit = cp.x * kUnitsV + u, s = stage_v(unit);
+#pragma unroll 1
+      for (int u = 0; u < kUnits; ++u) {
+        const int unit = cp.x * kUnits + u, s = stage_v(unit);
         if (cp.row == 0) wait(full(s), (unit / kV) & 1);
         if (!ok) return;
         tc_fence_after();
         const uint32_t b = desc_low_v(ring + offset(s));
 #pragma unroll
         for (int h = 0; h < 2; ++h)
-          mma_ts4(lead, o + (uint32_t)(u * L::kDimsV), a + (NQ == 2 ? kKeys / 4 : kKeys / 2) * h, b + 512 * h, kIdescO,
+          mma_ts4(lead, o + (uint32_t)(u * L::kDims), a + (NQ == 2 ? kKeys / 4 : kKeys / 2) * h, b + 512 * h, kIdescO,
                   (cp.tile > cp.first || h > 0) ? 1u : 0u, steps - 4 * h);
-        if (u == kUnitsV - 1) commit(lead, pv_done(cp.g & 1));
+        if (u == kUnits - 1) commit(lead, pv_done(cp.g & 1));
         if (last_use) commit(lead, empty(s));
       }
       step(cp, true);
@@ -851,10 +852,11 @@ attention_kernel(const __grid_constant__ CUtensorMap map_q, const __grid_constan
           // A stage's barrier tells this load from the one before only once that one is complete:
           // V's of three tiles before is, from S of this tile; with two units a tile and three
           // stages it may be the tile's before.
-          if (kUnitsV == 2 && x > 0) ok = ok && wait_pv(x - 1);
-          constexpr int kBlocks = L::kDimsV / 64;
-          for (int u = 0; u < kUnitsV; ++u) {
-            const int unit = x * kUnitsV + u, sv = stage_v(unit);
+          if (kUnits == 2 && x > 0) ok = ok && wait_pv(x - 1);
+          constexpr int kBlocks = L::kDims / 64;
+#pragma unroll 1
+          for (int u = 0; u < kUnits; ++u) {
+            const int unit = x * kUnits + u, sv = stage_v(unit);
             ok = ok && mbar_wait(full(sv), (unit / kV) & 1, abort, p.dev_status);
             unsigned char* v = ring_ptr + offset(sv);
             if (ok)
@@ -895,24 +897,26 @@ attention_kernel(const __grid_constant__ CUtensorMap map_q, const __grid_constan
         const float norm = it.slot < 0 ? 1.0f / l : 1.0f;
         const bool nothing = it.slot < 0 && l == 0.0f;
 #pragma unroll 1
-        for (int c = 0; c < kOut; c += 16) {
-          uint32_t o[16];
+        for (int c = 0; c < kOut; c += 32) {
+          uint32_t o[32];
           tmem_issue(o_addr + c, o);
           tmem_wait(o);
           if (!valid) continue;
           if (part != nullptr) {
-            store32(part + c * NQ * kRows, o);
-            store32(part + (c + 8) * NQ * kRows, o + 8);
-          } else {
-            uint32_t w[8];
 #pragma unroll
-            for (int i = 0; i < 8; ++i)
+            for (int i = 0; i < 32; i += 8) store32(part + (c + i) * NQ * kRows, o + i);
+          } else {
+            uint32_t w[16];
+#pragma unroll
+            for (int i = 0; i < 16; ++i)
               w[i] = nothing ? 0u : to_bf16x2(__uint_as_float(o[2 * i]) * norm, __uint_as_float(o[2 * i + 1]) * norm);
             if (p.wide) {
               store32(out + c, w);
+              store32(out + c + 16, w + 8);
             } else {
-              reinterpret_cast<uint4*>(out + c)[0] = make_uint4(w[0], w[1], w[2], w[3]);
-              reinterpret_cast<uint4*>(out + c)[1] = make_uint4(w[4], w[5], w[6], w[7]);
+#pragma unroll
+              for (int i = 0; i < 4; ++i)
+                reinterpret_cast<uint4*>(out + c)[i] = make_uint4(w[4 * i], w[4 * i + 1], w[4 * i + 2], w[4 * i + 3]);
             }
           }
         }
@@ -923,12 +927,10 @@ attention_kernel(const __grid_constant__ CUtensorMap map_q, const __grid_constan
   __syncthreads();
   if (*abort) {
     // A wait ran out: what is in flight lands (bounded) before TMEM and shared memory go.
-    if (warp == kWarpK && lane == 0)
-      for (int u = issued > kK ? issued - kK : 0; u < issued; ++u)
-        mbar_drain(full(stage_k(u)), (uint32_t)(u / kK) & 1u, p.dev_status);
-    if (warp == kWarpV && lane == 0) {
-      for (int u = issued > kV ? issued - kV : 0; u < issued; ++u)
-        mbar_drain(full(stage_v(u)), (uint32_t)(u / kV) & 1u, p.dev_status);
+    if ((warp == kWarpK || warp == kWarpV) && lane == 0) {
+      const int ring0 = warp == kWarpK ? 0 : kK, stages = warp == kWarpK ? kK : kV;
+      for (int u = issued > stages ? issued - stages : 0; u < issued; ++u)
+        mbar_drain(full(ring0 + u % stages), (uint32_t)(u / stages) & 1u, p.dev_status);
       if (q_issued > 0) mbar_drain(q_full, (uint32_t)(q_issued - 1) & 1u, p.dev_status);
     }
     if (warp == kMmaWarp && lead) {
