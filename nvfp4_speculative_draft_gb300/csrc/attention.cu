@@ -26,8 +26,8 @@
 //   warp 9      schedules the items and loads K (TMA)
 //   warp 10     loads Q and V
 //
-// Schedule: the items of all sequences and heads are laid end to end on a line, a tile of
-// keys 128 units long and an item's start kItemCost, and every CTA takes an equal share of
+// Schedule: the items of all sequences and heads are laid end to end on a line, item_cost units
+// for an item's start and end, then 128 for a tile of keys, and every CTA takes an equal share of
 // it, whatever the lengths: each finds its share from the lengths on the device.  An item
 // that a share's border cuts leaves the parts' (maximum, sum, O) in the workspace, FP32, and
 // a second kernel joins them in the order of the keys.  The borders depend on the lengths
@@ -52,7 +52,12 @@ constexpr int kKeys = 128;                    // keys of a tile
 constexpr int kSoftmaxWarps = 8;
 constexpr int kThreads = 32 * (kSoftmaxWarps + 4);  // (three of the last four work)
 constexpr int kDescs = 4;                     // item descriptors in flight
-constexpr int kItemCost = kKeys;              // an item's fixed cost, in keys
+// An item's start and end, in the keys that its products would take meanwhile.  With full tiles of
+// rows what was measured (us):              64    128    192    256    320    384    512    640
+//   heads of 128, 11 packed prompts        93     76     72     71     72     75     77     81
+//   heads of 256, 8192 tokens             864    825    772    722    690    650    639    641
+// and with few rows, where keys arrive no faster, no difference up to 256 and 1 % more at 512.
+constexpr int kItemCostFew = 128, kItemCost = 224, kItemCostWide = 512;
 constexpr int kMinShare = kKeys;              // of a CTA, where there is that little
 constexpr float kRescale = 8.0f;              // log2 of what the maximum may lag behind
 constexpr float kLog2e = 1.4426950408889634f;
@@ -89,6 +94,7 @@ struct Params {
   int per_tile, per_item;      // tokens of a tile of rows, and of an item
   int page_size, page_shift;   // tokens of a page; log2 of it, or -1
   int box;                     // tokens of a TMA box
+  bool full_tiles;             // most tiles of rows are full
   int pages;
   float scale;                 // |scale| log2 e, never 0
   int negative;
@@ -150,12 +156,12 @@ struct Line {
   int items;
   int64_t base;  // length of item 0
   int64_t length;
-  __device__ __forceinline__ Line(const Sequence& q, int per_item) {
+  __device__ __forceinline__ Line(const Sequence& q, int per_item, int item_cost) {
     per = per_item;
     items = q.n <= per ? (q.n > 0) : (q.n + per - 1) / per;
     const int cached = max(q.off, 0);
-    base = (int64_t)cached + per + kItemCost;
-    length = items > 0 ? before(items - 1) + cached + q.n + kItemCost : 0;
+    base = (int64_t)cached + per + item_cost;
+    length = items > 0 ? before(items - 1) + cached + q.n + item_cost : 0;
   }
   __device__ __forceinline__ int64_t before(int t) const {
     return t * base + (int64_t)per * ((int64_t)t * (t - 1) / 2);
@@ -407,7 +413,7 @@ attention_kernel(const __grid_constant__ CUtensorMap map_q, const __grid_constan
           slot = 0;
           phase ^= 1;
         }
-        const bool withheld = nvfp4::kWithhold && blockIdx.x == 0 && keys && issued == 0;  // (test build)
+        const bool withheld = nvfp4::kWithhold && keys && issued == 0;  // (test build: by each CTA)
         ++issued;
         if (withheld) continue;
         if (lead) mbar_arrive_expect_tx(full(s), (uint32_t)(count * p.box * 128 * kBlocks));
@@ -426,12 +432,13 @@ attention_kernel(const __grid_constant__ CUtensorMap map_q, const __grid_constan
     // This CTA's share [x0, x1) of the line: a lane a sequence.  (By this warp alone: the others
     // get their items from it, and a pass over 32 sequences takes less than the block's barriers
     // and loads up to some hundreds of them.)
+    const int item_cost = NQ == 2 ? kItemCost : D == 256 && p.full_tiles ? kItemCostWide : kItemCostFew;
     int64_t total = 0, chunk = 0;  // of all sequences; this lane's of the first 32
     Sequence q{};
     for (int s = lane; keys && s < p.batch; s += 32) {
       const Raw raw = load_raw(p, s);
       const Sequence x = sequence(p, raw);
-      const int64_t length = p.kv_heads * Line(x, p.per_item).length;
+      const int64_t length = p.kv_heads * Line(x, p.per_item, item_cost).length;
       if (blockIdx.x == 0 && !consistent(p, raw)) nvfp4::report(p.dev_status, NVFP4_ERR_INDEX);
       if (s < 32) {
         q = x;
@@ -458,7 +465,7 @@ attention_kernel(const __grid_constant__ CUtensorMap map_q, const __grid_constan
       for (int base = 0; base < p.batch; base += 32) {
         if (base > 0) {
           q = base + lane < p.batch ? sequence(p, load_raw(p, base + lane)) : Sequence{};
-          chunk = p.kv_heads * Line(q, p.per_item).length;
+          chunk = p.kv_heads * Line(q, p.per_item, item_cost).length;
         }
         int64_t upto = chunk;
         if (p.batch > 1) {
@@ -480,7 +487,7 @@ attention_kernel(const __grid_constant__ CUtensorMap map_q, const __grid_constan
       q.begin = __shfl_sync(0xFFFFFFFFu, q.begin, who);
       q.n = __shfl_sync(0xFFFFFFFFu, q.n, who);
       q.off = __shfl_sync(0xFFFFFFFFu, q.off, who);
-      const Line line(q, p.per_item);
+      const Line line(q, p.per_item, item_cost);
       head = (int)quotient(x0 - at, line.length);
       head_at = at + head * line.length;
       int lo = 0, hi = line.items;
@@ -504,7 +511,7 @@ attention_kernel(const __grid_constant__ CUtensorMap map_q, const __grid_constan
       Part r{};
       r.it.rows = 0;
       while (seq < p.batch) {
-        const Line line(q, p.per_item);
+        const Line line(q, p.per_item, item_cost);
         if (t >= line.items) {
           t = 0;
           head_at += line.length;
@@ -519,8 +526,8 @@ attention_kernel(const __grid_constant__ CUtensorMap map_q, const __grid_constan
           }
           continue;
         }
-        const int64_t at = head_at + line.before(t) + kItemCost;  // of tile 0
-        if (at - kItemCost >= x1) break;
+        const int64_t at = head_at + line.before(t) + item_cost;  // of tile 0
+        if (at - item_cost >= x1) break;
         const int row = t * line.per, rows = min(line.per, q.n - row);
         const int end = max(q.off + row + rows, 0);
         const int tiles = max((end + kKeys - 1) / kKeys, 1);
@@ -652,7 +659,7 @@ attention_kernel(const __grid_constant__ CUtensorMap map_q, const __grid_constan
       if (cs.tile == cs.first && cs.row == 0) wait(q_full, (cs.count - 1) & 1);
       const uint32_t d = tmem + (uint32_t)(cs.g & 1) * kKeys;
       const bool last_use = cs.row == NQ - 1;
-#pragma unroll 1
+#pragma unroll
       for (int u = 0; u < kUnits; ++u) {
         const int unit = cs.x * kUnits + u, s = stage_k(unit);
         if (cs.row == 0) wait(full(s), (unit / kK) & 1);
@@ -675,7 +682,7 @@ attention_kernel(const __grid_constant__ CUtensorMap map_q, const __grid_constan
       const uint32_t a = tmem + (uint32_t)(cp.g & 1) * kKeys, o = tmem + 2 * kKeys + (uint32_t)(cp.row * D);
       const bool last_use = cp.row == NQ - 1;
       wait(p_full(cp.g & 1), (cp.g >> 1) & 1);
-#pragma unroll 1
+#pragma unroll
       for (int u = 0; u < kUnits; ++u) {
         const int unit = cp.x * kUnits + u, s = stage_v(unit);
         if (cp.row == 0) wait(full(s), (unit / kV) & 1);
@@ -860,6 +867,7 @@ attention_kernel(const __grid_constant__ CUtensorMap map_q, const __grid_constan
             ok = ok && mbar_wait(full(sv), (unit / kV) & 1, abort, p.dev_status);
             unsigned char* v = ring_ptr + offset(sv);
             if (ok)
+#pragma unroll 1
               for (int i = from * 8 * kBlocks + (int)threadIdx.x; i < to * 8 * kBlocks; i += threads) {
                 const int key = i / (8 * kBlocks), piece = i % (8 * kBlocks);
                 *reinterpret_cast<uint4*>(v + piece / 8 * (kKeys * 128) + key * 128 + piece % 8 * 16) = make_uint4(0, 0, 0, 0);
@@ -1060,7 +1068,7 @@ bool encode_kv(CUtensorMap* map, const kv_pages& x, const paged_attention_input&
 }
 
 template <int D, int NQ>
-int launch(const paged_attention_input& in, const attn_rows& out, void* workspace, int32_t* dev_status,
+int launch(const paged_attention_input& in, bool many, const attn_rows& out, void* workspace, int32_t* dev_status,
            cudaStream_t stream) {
   using L = Tile<D, NQ>;
   Params p;
@@ -1076,6 +1084,7 @@ int launch(const paged_attention_input& in, const attn_rows& out, void* workspac
   p.group = (int)(in.heads / in.kv_heads);
   p.per_tile = kRows / p.group;
   p.per_item = NQ * p.per_tile;
+  p.full_tiles = many;
   p.page_size = (int)in.page_size;
   p.page_shift = -1;
   for (int i = 4; i < 17; ++i)
@@ -1125,13 +1134,12 @@ int launch(const paged_attention_input& in, const attn_rows& out, void* workspac
 int launch_attention(const paged_attention_input* in, const attn_rows* out, void* workspace, int32_t* dev_status,
                      cudaStream_t stream) {
   // Two tiles of rows an item where sequences bring more than one tile's on average.
-  const int64_t rows = in->tokens * (in->heads / in->kv_heads);
-  const bool two = in->dim <= 128 && rows > kRows * in->batch;
+  const bool many = in->tokens * (in->heads / in->kv_heads) > kRows * in->batch;
   switch (in->dim) {
-    case 64: return two ? launch<64, 2>(*in, *out, workspace, dev_status, stream)
-                        : launch<64, 1>(*in, *out, workspace, dev_status, stream);
-    case 128: return two ? launch<128, 2>(*in, *out, workspace, dev_status, stream)
-                         : launch<128, 1>(*in, *out, workspace, dev_status, stream);
-    default: return launch<256, 1>(*in, *out, workspace, dev_status, stream);
+    case 64: return many ? launch<64, 2>(*in, many, *out, workspace, dev_status, stream)
+                         : launch<64, 1>(*in, many, *out, workspace, dev_status, stream);
+    case 128: return many ? launch<128, 2>(*in, many, *out, workspace, dev_status, stream)
+                          : launch<128, 1>(*in, many, *out, workspace, dev_status, stream);
+    default: return launch<256, 1>(*in, many, *out, workspace, dev_status, stream);
   }
 }
