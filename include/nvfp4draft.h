@@ -604,8 +604,8 @@ typedef struct rope_kv_output {
  *   (x, y) -> (x cos t - y sin t, x sin t + y cos t), FP32, rounded once to BF16.
  * The fraction of a turn is exact however far the position; the sines are off by at
  * most 4e-7.  Rotated k and v as they are go to the cache at each token's slot; a
- * negative slot writes nothing, one past the cache neither (NVFP4_ERR_INDEX).  Two
- * tokens of one slot: one of them.  Workspace: none.
+ * negative slot writes nothing, one past the cache neither (NVFP4_ERR_INDEX).  Where
+ * two tokens have one slot, each element there is of one of them.  Workspace: none.
  */
 int rope_kv_write(const rope_kv_input *in, const rope_kv_output *out, const nvfp4_exec *ex);
 
@@ -635,7 +635,8 @@ typedef struct prompt_attention_input {
  * [0, tokens] is clamped, a sequence whose offsets descend is empty (both: NVFP4_ERR_INDEX).
  *   out   [tokens, heads, dim] BF16.
  * Values of tokens that a query does not see but that share a tile of 128 with ones that
- * another query of its sequence sees must be finite.  Other sequences' may be anything.
+ * another query of its sequence sees must be finite.  Other sequences' may be anything.  A
+ * query whose scores are all -inf gets zeros.
  * Sums are split over SMs by a rule on the lengths and joined in a fixed order: the same
  * call gives the same bits.
  * Workspace: ATTENTION_WS_BYTES, 32-byte aligned; nothing need be in it, nothing is kept

@@ -291,7 +291,8 @@ def load(path: str = LIB_PATH):
 
 
 def _load_binding():
-    """The native marshalling of the verify step's calls (csrc/binding.cpp)."""
+    """The native marshalling of the verify step's and the attention step's calls
+    (csrc/binding.cpp)."""
     from . import build
     path = build.binding_path()
     if not os.path.exists(path):

@@ -5,9 +5,9 @@ Each ``csrc/*.cu`` is compiled in parallel with
 ``_build/libnvfp4draft.so`` (CUDA runtime linked statically, so the library
 is self-contained; it shares the process's primary CUDA context).
 ``csrc/binding.cpp``, the native argument marshalling of the verify step's
-calls, is compiled beside them with g++ against PyTorch's headers.  The library
-does not need it: where it does not compile, ``build()`` warns, and the verify
-step's calls raise ImportError.
+and the attention step's calls, is compiled beside them with g++ against PyTorch's
+headers.  The library does not need it: where it does not compile, ``build()`` warns,
+and those calls raise ImportError.
 """
 import concurrent.futures as cf
 import contextlib
@@ -99,7 +99,7 @@ def build(force=False, verbose=False, extra=(), debug=False, withhold=False):
             try:
                 fb.result()
             except RuntimeError as e:
-                warnings.warn(f"the verify step's calls are not available: {e}", RuntimeWarning)
+                warnings.warn(f"the verify step's and the attention step's calls are not available: {e}", RuntimeWarning)
         return lib
     return _build_one(force, verbose, extra, debug, withhold)
 

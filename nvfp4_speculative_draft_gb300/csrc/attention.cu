@@ -22,8 +22,8 @@
 //          warpgroups work on the same tile, half of its keys each, and exchange the
 //          rows' maxima through shared memory; S is double buffered.
 //   warps 0..7  softmax; they rescale and finish O as well
-//   warp 8      allocates TMEM, issues the MMAs (NQ = 2: warps 8 and 11, a tile of rows each)
-//   warp 9      schedules the items and loads K (TMA)
+//   warp 8      allocates TMEM, issues the MMAs
+//   warp 9      finds the items and loads K (TMA)
 //   warp 10     loads Q and V
 //
 // Schedule: the items of all sequences and heads are laid end to end on a line, item_cost units
@@ -36,6 +36,21 @@
 // Keys that a row does not see get weight 0 by selection, and P V stops at the last one that
 // some row of the item sees (rounded up to 16, values behind it zeroed): what lies there, in
 // other sequences or unused slots, does not matter.
+//
+// What bounds it, and what it measured (fractions of a cuBLAS product's burst rate and of a
+// copy's):
+//   long prompts   the chain S -> softmax -> P V of each tile of rows: 3000 cycles a tile of keys
+//                  for 2048 of MMAs, as S of the next tile has to wait for TMEM (O and S of two
+//                  tiles fill it).  16384 tokens, 32 / 8 heads of 128: 1.41 ms, 1560 TFLOP/s
+//                  (0.81), less in long runs, where power limits it; 8192 tokens 383 us (0.75),
+//                  heads of 64 331 us.  Heads of 256, S twice in TMEM: 8192 tokens, 32 / 4 heads,
+//                  650 us, 1690 TFLOP/s (0.88).
+//   short prompts  an item's start and end, about 4500 cycles: its first loads, the last P V, O's
+//                  way through registers.  11 prompts of up to 1900 tokens, 28 / 4 heads: 71 us
+//                  (0.40); one of 77 tokens: 7.8 us.
+//   the cache      HBM: 64 sequences of up to 16000 keys, up to 5 queries each: 158 us, 6.1 TB/s
+//                  (0.91); one token over 4000 keys, 32 / 4 heads of 256: 13.7 us, of which finding
+//                  the share and the join are 3 us each.
 #include <cuda_bf16.h>
 
 #include <type_traits>
@@ -289,7 +304,8 @@ __device__ __forceinline__ bool softmax_agree(bool ok) {
 
 // ----------------------------------------------------------------- kernel
 
-// The roles' code has to fit the SM's instruction cache together, so each part stands once and
+// The roles' code has to fit the SM's instruction cache together (32 KB; beyond it a warp gets an
+// instruction every 2.6 cycles), so each part stands once, K and V are loaded by the same code, and
 // loops are rolled where a trip takes longer than fetching its instructions (30 packed prompts of
 // 300 tokens: 77 us with 23 % of the instruction requests missing, 65 us with 10 %).
 template <int D, int NQ>
@@ -1133,7 +1149,9 @@ int launch(const paged_attention_input& in, bool many, const attn_rows& out, voi
 
 int launch_attention(const paged_attention_input* in, const attn_rows* out, void* workspace, int32_t* dev_status,
                      cudaStream_t stream) {
-  // Two tiles of rows an item where sequences bring more than one tile's on average.
+  // Two tiles of rows an item where sequences bring more than one tile's on average (32 / 8 heads
+  // of 128 over 2000 keys, 16 sequences: 24 tokens each 37 us, with two tiles 40; 48 tokens 48, with
+  // one tile 58).
   const bool many = in->tokens * (in->heads / in->kv_heads) > kRows * in->batch;
   switch (in->dim) {
     case 64: return many ? launch<64, 2>(*in, many, *out, workspace, dev_status, stream)
