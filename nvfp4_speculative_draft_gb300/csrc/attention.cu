@@ -445,29 +445,35 @@ attention_kernel(const __grid_constant__ CUtensorMap map_q, const __grid_constan
         }
       }
     };
-    // This CTA's share [x0, x1) of the line: a lane a sequence.  (By this warp alone: the others
-    // get their items from it, and a pass over 32 sequences takes less than the block's barriers
-    // and loads up to some hundreds of them.)
+    // This CTA's share [x0, x1) of the line: a lane a run of neighbouring sequences, whose offsets
+    // it finds in the L1 but for the first of a cache line (every 32nd sequence to a lane, a miss
+    // each: 1000 sequences of 50 keys 142 us instead of 122).  (By this warp alone: the others get
+    // their items from it, and up to some hundreds of sequences take less than the block's barriers.)
     const int item_cost = NQ == 2 ? kItemCost : D == 256 && p.full_tiles ? kItemCostWide : kItemCostFew;
-    int64_t total = 0, chunk = 0;  // of all sequences; this lane's of the first 32
-    Sequence q{};
-    for (int s = lane; keys && s < p.batch; s += 32) {
-      const Raw raw = load_raw(p, s);
-      const Sequence x = sequence(p, raw);
-      const int64_t length = p.kv_heads * Line(x, p.per_item, item_cost).length;
-      if (blockIdx.x == 0 && !consistent(p, raw)) nvfp4::report(p.dev_status, NVFP4_ERR_INDEX);
-      if (s < 32) {
-        q = x;
-        chunk = length;
+    const int run = (p.batch + 31) >> 5;
+    int64_t chunk = 0;  // of the lane's sequences
+    Sequence q{};       // the last of them
+    bool sound = true;
+    if (keys) {
+      const int end = min(p.batch, (lane + 1) * run);
+      for (int s = lane * run; s < end; ++s) {
+        const Raw raw = load_raw(p, s);
+        q = sequence(p, raw);
+        chunk += p.kv_heads * Line(q, p.per_item, item_cost).length;
+        sound = sound && consistent(p, raw);
       }
-      total += length;
     }
-    if (p.batch == 1) {
-      total = __shfl_sync(0xFFFFFFFFu, total, 0);
-    } else {
+    if (blockIdx.x == 0 && !sound) nvfp4::report(p.dev_status, NVFP4_ERR_INDEX);
+    auto scan = [&](int64_t v) -> int64_t {  // inclusive prefix sums over the lanes
 #pragma unroll
-      for (int d = 16; d; d >>= 1) total += __shfl_xor_sync(0xFFFFFFFFu, total, d);
-    }
+      for (int d = 1; d < 32; d <<= 1) {
+        const int64_t o = __shfl_up_sync(0xFFFFFFFFu, v, d);
+        if (lane >= d) v += o;
+      }
+      return v;
+    };
+    int64_t upto = p.batch > 1 ? scan(chunk) : chunk;
+    const int64_t total = __shfl_sync(0xFFFFFFFFu, upto, p.batch > 1 ? 31 : 0);
     // total = shares * each + rest: the first `rest` shares are one longer
     const int shares = total >= (int64_t)kMinShare * gridDim.x ? (int)gridDim.x : max((int)((uint32_t)total / kMinShare), 1);
     const int64_t each = quotient(total, shares), rest = total - each * shares;
@@ -476,29 +482,24 @@ attention_kernel(const __grid_constant__ CUtensorMap map_q, const __grid_constan
     int seq = p.batch, head = 0, t = 0;
     int64_t head_at = 0;
     if (keys && x0 < x1) {  // the sequence, head and item that x0 lies in
-      int64_t at = 0;
-      int who = 0;
-      for (int base = 0; base < p.batch; base += 32) {
-        if (base > 0) {
-          q = base + lane < p.batch ? sequence(p, load_raw(p, base + lane)) : Sequence{};
+      int who = __ffs((int)__ballot_sync(0xFFFFFFFFu, upto > x0)) - 1;
+      int64_t at = __shfl_sync(0xFFFFFFFFu, upto - chunk, who);
+      seq = who * run;
+      if (run > 1) {  // within the run, 32 sequences at a time
+        const int end = min(p.batch, seq + run);
+        for (int base = seq; base < end; base += 32) {
+          q = base + lane < end ? sequence(p, load_raw(p, base + lane)) : Sequence{};
           chunk = p.kv_heads * Line(q, p.per_item, item_cost).length;
-        }
-        int64_t upto = chunk;
-        if (p.batch > 1) {
-#pragma unroll
-          for (int d = 1; d < 32; d <<= 1) {
-            const int64_t o = __shfl_up_sync(0xFFFFFFFFu, upto, d);
-            if (lane >= d) upto += o;
+          upto = scan(chunk);
+          const unsigned past = __ballot_sync(0xFFFFFFFFu, at + upto > x0);
+          if (past != 0u) {
+            who = __ffs((int)past) - 1;
+            seq = base + who;
+            at += __shfl_sync(0xFFFFFFFFu, upto - chunk, who);
+            break;
           }
+          at += __shfl_sync(0xFFFFFFFFu, upto, 31);
         }
-        const unsigned past = __ballot_sync(0xFFFFFFFFu, at + upto > x0);
-        if (past != 0u) {
-          who = __ffs((int)past) - 1;
-          seq = base + who;
-          at += __shfl_sync(0xFFFFFFFFu, upto - chunk, who);
-          break;
-        }
-        at += __shfl_sync(0xFFFFFFFFu, upto, 31);
       }
       q.begin = __shfl_sync(0xFFFFFFFFu, q.begin, who);
       q.n = __shfl_sync(0xFFFFFFFFu, q.n, who);
