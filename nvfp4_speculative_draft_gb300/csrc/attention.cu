@@ -394,10 +394,9 @@ attention_kernel(const __grid_constant__ CUtensorMap map_q, const __grid_constan
     int page, token, count;
   };
   auto place_of = [&](const Item& it, int tile) -> Place {
-    const int boxes = kKeys / p.box;
-    const int j = tile * kKeys + lane * p.box;
-    const int count = min(max((it.end - tile * kKeys + p.box - 1) / p.box, 0), boxes);
+    const int count = (min(it.end - tile * kKeys, kKeys) + p.box - 1) / p.box;
     if (lane >= count) return Place{0, 0, count};
+    const int j = tile * kKeys + lane * p.box;
     if (p.table == nullptr) return Place{0, it.begin + j, count};
     const int entry = p.page_shift >= 0 ? j >> p.page_shift : j / p.page_size;
     const int id = ld_ro(p.table + it.table + entry);
@@ -547,7 +546,7 @@ attention_kernel(const __grid_constant__ CUtensorMap map_q, const __grid_constan
         if (at - item_cost >= x1) break;
         const int row = t * line.per, rows = min(line.per, q.n - row);
         const int end = max(q.off + row + rows, 0);
-        const int tiles = max((end + kKeys - 1) / kKeys, 1);
+        const int tiles = max((int)(((uint32_t)end + kKeys - 1) / kKeys), 1);
         const int64_t a = at >= x0 ? 0 : (x0 - at + kKeys - 1) >> 7;
         const int64_t b = at >= x1 ? 0 : (x1 - at + kKeys - 1) >> 7;
         static_assert(kKeys == 1 << 7, "shift");
@@ -870,7 +869,7 @@ attention_kernel(const __grid_constant__ CUtensorMap map_q, const __grid_constan
         // Values behind the last key that any row sees may be anything: zeros for those of
         // them that the last 16 keys of P V take in.  (NQ = 2: by the first tile of rows' threads:
         // the second's P V is issued behind theirs.)
-        if (tile * kKeys + kKeys > it.end && t == 0) {
+        if (it.end - tile * kKeys < kKeys && t == 0) {
           const int from = max(it.end - tile * kKeys, 0), to = (max(from, 1) + 15) / 16 * 16;
           constexpr int threads = 32 * kSoftmaxWarps / NQ;
           // A stage's barrier tells this load from the one before only once that one is complete:

@@ -60,6 +60,22 @@ def test_very_long_sequence(dev, d, page):
     check_paged(dev, [2, 1], [260003, 7], 2, 1, d, page)
 
 
+def test_as_many_positions_as_an_int32_counts(dev):
+    """2^31 - 1 cached tokens, by a table that names one page over and over: equal scores, so the
+    values' mean, and nothing of the slot behind the last token."""
+    m, page, pages = nd(), 65536, 32768
+    kc = torch.zeros((2, page, 1, 64), dtype=BF16, device=dev)
+    value = torch.tensor([1.0, 0.5, 0.0, -1.0], dtype=BF16, device=dev).repeat(16)
+    vc = value.expand(2, page, 1, 64).contiguous()
+    kc[1, -1], vc[1, -1] = float("nan"), float("nan")
+    table = torch.zeros((1, pages), dtype=torch.int32, device=dev)
+    table[0, -1] = 1
+    q = randn(gen(dev, 1), 1, 4, 64).to(BF16)
+    status = ints(dev, [0])
+    out = m.paged_attention(q, kc, vc, table, ints(dev, [2 ** 31 - 1]), ints(dev, [0, 1]), dev_status=status)
+    assert torch.equal(out, value.expand(1, 4, 64)) and status.item() == 0
+
+
 def test_padded_batch_and_rows(dev):
     """Sequences without tokens at the end, rows of q behind the last one: as they were."""
     m = nd()
