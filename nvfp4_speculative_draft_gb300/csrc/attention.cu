@@ -978,7 +978,9 @@ attention_kernel(const __grid_constant__ CUtensorMap map_q, const __grid_constan
 // added in order.  The weights come first, so that the sums' loads wait for nothing.
 
 constexpr int kJoinWarps = 8;
-constexpr int kJoinFew = 8;  // parts that one warp takes
+// Parts that one warp takes: where each row has a block of its own (one token over 1000 keys 9.4 us,
+// up to 8 parts by a warp 11.7), and where rows are more (20 rows 11.9 us, up to 4 parts 12.3).
+constexpr int kJoinFewRows = 2, kJoinFew = 8;
 
 template <int D, int NQ>
 __global__ void __launch_bounds__(32 * kJoinWarps) attention_join_kernel(const __grid_constant__ Params p) {
@@ -991,7 +993,7 @@ __global__ void __launch_bounds__(32 * kJoinWarps) attention_join_kernel(const _
   const int parts = rec.parts, rows = rec.rows * p.group;
   if (parts <= 0) return;
   const int per_tile = p.per_tile;
-  const bool few = parts <= kJoinFew;
+  const bool few = parts <= (rows <= (int)gridDim.y ? kJoinFewRows : kJoinFew);
   const float* slots = reinterpret_cast<const float*>(p.ws + kRecordBytes) + 2 * (int64_t)c * slot_floats(D, NQ);
   // part 0 is the first CTA's second place, the others are the next CTAs' first
   auto slot_of = [&](int k) { return slots + (k == 0 ? 1 : 2 * k) * slot_floats(D, NQ); };
