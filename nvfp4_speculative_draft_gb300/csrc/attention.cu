@@ -28,7 +28,7 @@
 //
 // Schedule: the items of all sequences and heads are laid end to end on a line, item_cost units
 // for an item's start and end, then 128 for a tile of keys, and every CTA takes an equal share of
-// it, whatever the lengths: each finds its share from the lengths on the device.  An item
+// it, whatever the lengths: each finds its share from the lengths on the device.  A longer item
 // that a share's border cuts leaves the parts' (maximum, sum, O) in the workspace, FP32, and
 // a second kernel joins them in the order of the keys.  The borders depend on the lengths
 // alone, so results do not depend on timing.
@@ -73,6 +73,11 @@ constexpr int kDescs = 4;                     // item descriptors in flight
 //   heads of 256, 8192 tokens             864    825    772    722    690    650    639    641
 // and with few rows, where keys arrive no faster, no difference up to 256 and 1 % more at 512.
 constexpr int kItemCostFew = 128, kItemCost = 224, kItemCostWide = 512;
+// Items of full tiles of rows are not cut up to so many tiles of keys: parts of 256 rows cost more
+// than shares that differ.  Prompts of 32 / 8 heads of 128, cut and whole: 512 tokens 20 and 16 us,
+// 1024 30 and 22, eight of 1024 (28 / 4 heads) 81 and 74; up to 12 tiles 2048 tokens 47 and 52.
+// With few rows parts are small: cut always (whole up to 4 tiles: one token over 300 keys 9.0, 10.3).
+constexpr int kWhole = 8;
 constexpr int kMinShare = kKeys;              // of a CTA, where there is that little
 constexpr float kRescale = 8.0f;              // log2 of what the maximum may lag behind
 constexpr float kLog2e = 1.4426950408889634f;
@@ -449,6 +454,7 @@ attention_kernel(const __grid_constant__ CUtensorMap map_q, const __grid_constan
     // each: 1000 sequences of 50 keys 142 us instead of 122).  (By this warp alone: the others get
     // their items from it, and up to some hundreds of sequences take less than the block's barriers.)
     const int item_cost = NQ == 2 ? kItemCost : D == 256 && p.full_tiles ? kItemCostWide : kItemCostFew;
+    const int whole = NQ == 2 || (D == 256 && p.full_tiles) ? kWhole : 0;
     const int run = (p.batch + 31) >> 5;
     int64_t chunk = 0;  // of the lane's sequences
     Sequence q{};       // the last of them
@@ -547,9 +553,15 @@ attention_kernel(const __grid_constant__ CUtensorMap map_q, const __grid_constan
         const int row = t * line.per, rows = min(line.per, q.n - row);
         const int end = max(q.off + row + rows, 0);
         const int tiles = max((int)(((uint32_t)end + kKeys - 1) / kKeys), 1);
-        const int64_t a = at >= x0 ? 0 : (x0 - at + kKeys - 1) >> 7;
-        const int64_t b = at >= x1 ? 0 : (x1 - at + kKeys - 1) >> 7;
+        int64_t a = at >= x0 ? 0 : (x0 - at + kKeys - 1) >> 7;
+        int64_t b = at >= x1 ? 0 : (x1 - at + kKeys - 1) >> 7;
         static_assert(kKeys == 1 << 7, "shift");
+        if (tiles <= whole) {  // all of it to the share that its middle lies in
+          const int64_t middle = at + (tiles * kKeys - item_cost) / 2;
+          if (middle >= x1) break;
+          a = middle < x0 ? tiles : 0;
+          b = tiles;
+        }
         ++t;
         if (a >= tiles || b <= a) continue;
         r.it.row0 = q.begin + row;
