@@ -46,8 +46,8 @@
 //                  heads of 64 331 us.  Heads of 256, S twice in TMEM: 8192 tokens, 32 / 4 heads,
 //                  650 us, 1690 TFLOP/s (0.88).
 //   short prompts  an item's start and end, about 4500 cycles: its first loads, the last P V, O's
-//                  way through registers.  11 prompts of up to 1900 tokens, 28 / 4 heads: 71 us
-//                  (0.40); one of 77 tokens: 7.8 us.
+//                  way through registers.  11 prompts of up to 1900 tokens, 28 / 4 heads: 73 us
+//                  (0.39); one of 77 tokens: 7.8 us.
 //   the cache      HBM: 64 sequences of up to 16000 keys, up to 5 queries each: 158 us, 6.1 TB/s
 //                  (0.91); one token over 4000 keys, 32 / 4 heads of 256: 13.7 us, of which finding
 //                  the share and the join are 3 us each.
@@ -74,8 +74,9 @@ constexpr int kDescs = 4;                     // item descriptors in flight
 // and with few rows, where keys arrive no faster, no difference up to 256 and 1 % more at 512.
 constexpr int kItemCostFew = 128, kItemCost = 224, kItemCostWide = 512;
 // Items of full tiles of rows are not cut up to so many tiles of keys: parts of 256 rows cost more
-// than shares that differ.  Prompts of 32 / 8 heads of 128, cut and whole: 512 tokens 20 and 16 us,
-// 1024 30 and 22, eight of 1024 (28 / 4 heads) 81 and 74; up to 12 tiles 2048 tokens 47 and 52.
+// than shares that differ, and where no item is longer there is nothing to join.  Prompts of 32 / 8
+// heads of 128, cut and whole: 512 tokens 20 and 13 us, 1024 30 and 20, eight of 1024 (28 / 4 heads)
+// 81 and 73, 11 of up to 1900 71 and 73; up to 12 tiles 2048 tokens 47 and 52.
 // With few rows parts are small: cut always (whole up to 4 tiles: one token over 300 keys 9.0, 10.3).
 constexpr int kWhole = 8;
 constexpr int kMinShare = kKeys;              // of a CTA, where there is that little
@@ -1150,8 +1151,9 @@ int launch(const paged_attention_input& in, bool many, const attn_rows& out, voi
   void* args[] = {&mq, &mk, &mv, &p};
   if (nvfp4::launch_dependent(kern, dim3(grid), dim3(kThreads), L::kSmemBytes, stream, 1, args) != cudaSuccess)
     return NVFP4_ERR_CUDA;
-  // (an item of one tile of keys is no border's)
-  if ((in.block_table != nullptr ? capacity : in.tokens) <= kKeys) return NVFP4_OK;
+  // (no item can be cut)
+  const int64_t uncut = NQ == 2 || (D == 256 && many) ? kWhole * kKeys : kKeys;
+  if ((in.block_table != nullptr ? capacity : in.tokens) <= uncut) return NVFP4_OK;
   // A block a row up to 24 rows (5 tokens of 4 heads over 4000 keys: 8 blocks 15.4 us, 20 13.5); more
   // blocks cost more to launch than they save (24 instead of 8 for 4 rows 11.1 -> 12.3 us).
   const int64_t rows = in.tokens * p.group;
