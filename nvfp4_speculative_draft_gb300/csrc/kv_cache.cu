@@ -112,8 +112,10 @@ __global__ void __launch_bounds__(kPlanThreads, 1) kv_plan_kernel(const __grid_c
   const int first = min(batch, (int)threadIdx.x * run), last = min(batch, first + run);
   int64_t mine = 0;
   for (int s = first; s < last; ++s) {
-    const int32_t n = max(nvfp4::ld_ro(p.in.num_new + s), 0), len = max(nvfp4::ld_ro(p.in.lens + s), 0);
-    const int32_t given = p.in.held != nullptr ? max(nvfp4::ld_ro(p.in.held + s), 0) : 0;
+    // (plain loads: lens and held may be outputs of this call, and of the one before it on the
+    // stream, which the read-only path does not allow for)
+    const int32_t n = max(p.in.num_new[s], 0), len = max(p.in.lens[s], 0);
+    const int32_t given = p.in.held != nullptr ? max(p.in.held[s], 0) : 0;
     const int64_t have = p.in.held != nullptr ? given : pages_of((uint32_t)len + (uint32_t)page - 1u);
     s_token[s] = n;
     s_len[s] = len;
