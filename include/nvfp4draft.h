@@ -530,7 +530,8 @@ typedef struct kv_pages {
 typedef struct kv_plan_input {
     const int32_t *lens;        /* [batch] tokens in the cache                      */
     const int32_t *num_new;     /* [batch] tokens that come; 0 or less: none        */
-    const int32_t *held;        /* [batch] pages held, or NULL: ceil(lens / page)   */
+    const int32_t *held;        /* [batch] pages held, or NULL: ceil(lens / page),
+                                   max_pages at most                                */
     int32_t *block_table;       /* [batch, ld_table]: the pages held; the new ones
                                    are written behind them                          */
     int64_t ld_table, max_pages; /* entries of a row in use: 0 < max_pages <= ld    */
@@ -564,7 +565,8 @@ typedef struct kv_plan_output {
  * do all later ones that need pages, once the stack is exceeded.  (A refused token whose
  * position no int32 holds gets 2^31 - 1.)  Rows past the last
  * new token get position 0 and slot -1 (a padded batch).  Pages kept from refused
- * drafts (held above ceil(lens / page_size)) are used before new ones.
+ * drafts (held above ceil(lens / page_size)) are used before new ones.  A held count past
+ * max_pages is kept as it is (such a sequence has all of its row and takes no page).
  * lens, num_new, held, free_pages and free_count are only read, unless given as outputs:
  * the same call on the same inputs writes the same.
  * A free count outside [0, free_capacity] is clamped, a slot that no int32 holds or of a

@@ -856,7 +856,7 @@ def kv_plan(lens: torch.Tensor, num_new: torch.Tensor, block_table: torch.Tensor
 
     New pages come off the top of the stack ``free_pages[:free_count]`` and are written to
     ``block_table`` [batch, max_pages] behind the ``held`` ones (default ceil(lens /
-    page_size)).  ``tokens`` rows of positions and slots are written; those past the last new
+    page_size), max_pages at most).  ``tokens`` rows of positions and slots are written; those past the last new
     token, and those of a sequence without a page (NVFP4_ERR_PAGES to dev_status), get slot -1.
 
     Nothing but the table's new entries is changed, unless ``out`` holds the inputs: its

@@ -115,11 +115,11 @@ __global__ void __launch_bounds__(kPlanThreads, 1) kv_plan_kernel(const __grid_c
     // (plain loads: lens and held may be outputs of this call, and of the one before it on the
     // stream, which the read-only path does not allow for)
     const int32_t n = max(p.in.num_new[s], 0), len = max(p.in.lens[s], 0);
-    const int32_t given = p.in.held != nullptr ? max(p.in.held[s], 0) : 0;
-    const int64_t have = p.in.held != nullptr ? given : pages_of((uint32_t)len + (uint32_t)page - 1u);
     s_token[s] = n;
     s_len[s] = len;
-    s_held[s] = (int32_t)min(have, width);
+    // (a count that is given stays what it is, past the table's row too: those pages are not lost)
+    s_held[s] = p.in.held != nullptr ? max(p.in.held[s], 0)
+                                     : (int32_t)min((int64_t)pages_of((uint32_t)len + (uint32_t)page - 1u), width);
     mine += n;
   }
   int64_t total;

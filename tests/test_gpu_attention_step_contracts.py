@@ -1,4 +1,5 @@
-"""The attention step's contracts that its other tests leave open: calls in place one right behind the other."""
+"""The attention step's contracts that its other tests leave open: calls in place one right behind the other,
+counts past a table's row."""
 import random
 
 import pytest
@@ -47,3 +48,19 @@ def test_plan_in_place_back_to_back(dev, batch, most, captured):
         assert out.cu_new.tolist() == cu and out.positions.tolist() == positions and out.slots.tolist() == slots
     assert table.tolist() == state[0] and lens.tolist() == state[1] and held.tolist() == state[2]
     assert count.item() == state[3]
+
+
+def test_plan_keeps_counts_past_the_row(dev):
+    """held comes back as max(held, need), also where it is more than a table's row has; such a sequence takes
+    no page, and one whose tokens do not fit its row is refused with its count unchanged."""
+    m, page, width = nd(), 16, 2
+    lens, new, held = [20, 0, 40, 3, 31], [1, 0, 8, 20, 2], [5, 3, 9, 2 ** 31 - 1, 2]
+    table = ints(dev, [[7, 4], [1, 2], [3, 5], [6, 8], [9, 10]])
+    before, status = table.clone(), ints(dev, [0])
+    p = m.kv_plan(ints(dev, lens), ints(dev, new), table, ints(dev, [11, 12, 13]), ints(dev, [3]), page, 31,
+                  held=ints(dev, held), dev_status=status)
+    assert p.held.tolist() == held and p.free_count.item() == 3 and torch.equal(table, before)
+    # 40 + 8 tokens are three pages of two, 31 + 2 as well
+    assert p.kv_lens.tolist() == [21, 0, 40, 23, 31] and status.item() == 10
+    slots = [4 * 16 + 4] + [-1] * 8 + [6 * 16 + i for i in range(3, 16)] + [8 * 16 + i for i in range(7)] + [-1] * 2
+    assert p.slots.tolist() == slots
