@@ -31,6 +31,7 @@ struct OccEntry {
 std::mutex g_occ_mutex;
 OccEntry g_occ[256];
 int g_nocc = 0;
+long g_occ_asked = 0;  // queries that the table did not answer
 }  // namespace
 
 int occupancy(const void* func, int threads, size_t smem) {
@@ -41,6 +42,7 @@ int occupancy(const void* func, int threads, size_t smem) {
     if (g_occ[i].dev == dev && g_occ[i].func == func && g_occ[i].threads == threads &&
         g_occ[i].smem == smem)
       return g_occ[i].occ;
+  ++g_occ_asked;
   int maxopt = 0;
   if (cudaDeviceGetAttribute(&maxopt, cudaDevAttrMaxSharedMemoryPerBlockOptin, dev) != cudaSuccess)
     return 0;
@@ -58,6 +60,14 @@ int occupancy(const void* func, int threads, size_t smem) {
 }
 
 }  // namespace nvfp4
+
+#ifdef NVFP4_TEST_WITHHOLD
+// Test build: how many occupancy queries went to the runtime so far.
+extern "C" long nvfp4_test_occupancy_asked() {
+  std::lock_guard<std::mutex> lock(nvfp4::g_occ_mutex);
+  return nvfp4::g_occ_asked;
+}
+#endif
 
 namespace nvfp4 {
 

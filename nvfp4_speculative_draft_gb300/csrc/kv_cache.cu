@@ -361,7 +361,9 @@ int launch_kv_plan(const kv_plan_input* in, const kv_plan_output* out, int32_t* 
   for (int i = 0; i < 17; ++i)
     if (in->page_size == (int64_t)1 << i) p.page_shift = i;
   const size_t smem = (size_t)in->batch * 16;
-  if (nvfp4::occupancy((const void*)kv_plan_kernel, kPlanThreads, smem) < 1) return NVFP4_ERR_CUDA;
+  // (asked for the largest batch, whatever this one's: one entry of the table that all calls share)
+  if (nvfp4::occupancy((const void*)kv_plan_kernel, kPlanThreads, (size_t)KV_PLAN_MAX_BATCH * 16) < 1)
+    return NVFP4_ERR_CUDA;
   // One CTA while each thread has two tokens at most, else a cluster of eight: 200 requests of 5
   // tokens 5.2 us (a cluster 5.5), 1000 of 1 6.1 (6.4); 400 of 5 6.6 (5.8), 1000 of 8 13.5 (6.4).
   const unsigned ranks = in->tokens + in->batch <= 2 * kPlanThreads ? 1 : 8;

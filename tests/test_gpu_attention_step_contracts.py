@@ -1,5 +1,7 @@
 """The attention step's contracts that its other tests leave open: calls in place one right behind the other,
-counts past a table's row."""
+counts past a table's row, host queries that every batch size would repeat."""
+import ctypes
+import os
 import random
 
 import pytest
@@ -64,3 +66,47 @@ def test_plan_keeps_counts_past_the_row(dev):
     assert p.kv_lens.tolist() == [21, 0, 40, 23, 31] and status.item() == 10
     slots = [4 * 16 + 4] + [-1] * 8 + [6 * 16 + i for i in range(3, 16)] + [8 * 16 + i for i in range(7)] + [-1] * 2
     assert p.slots.tolist() == slots
+
+
+def test_batch_sizes_of_the_plan_do_not_fill_the_table_of_queries(dev):
+    """Several hundred batch sizes: the runtime is asked about kv_plan's kernel once, and a kernel that is first
+    used behind them once too.  (The test build counts its queries; none of these calls withholds anything.)"""
+    from nvfp4_speculative_draft_gb300 import build
+    m = nd()
+    if not os.path.exists(build.WITHHOLD_LIB):
+        build.build(withhold=True)
+    L = ctypes.CDLL(build.WITHHOLD_LIB)
+    L.nvfp4_test_occupancy_asked.restype = ctypes.c_long
+    L.fp8w_quantize.argtypes = [ctypes.c_void_p, ctypes.c_int64, ctypes.c_int64, ctypes.c_void_p, ctypes.c_void_p,
+                                ctypes.POINTER(m._Exec)]
+    most = 700
+    zeros = lambda n: ints(dev, [0] * n)  # noqa: E731
+    lens, new, table, free, count = zeros(most), ints(dev, [1] * most), zeros(most * 2), ints(dev, list(range(most))), ints(dev, [most])
+    cu, kv, positions, slots = zeros(most + 1), zeros(most), zeros(most), zeros(most)
+    ex = m._Exec(torch.cuda.current_stream().cuda_stream, None, 0, None)
+
+    def plan(batch):
+        i = m._PlanInput(lens.data_ptr(), new.data_ptr(), None, table.data_ptr(), 2, 2, free.data_ptr(), most, count.data_ptr(),
+                         batch, 16, most)
+        o = m._PlanOutput(cu.data_ptr(), kv.data_ptr(), positions.data_ptr(), slots.data_ptr(), None, None)
+        assert L.kv_plan(ctypes.byref(i), ctypes.byref(o), ctypes.byref(ex)) == 0
+
+    w = torch.ones((64, 64), dtype=torch.bfloat16, device=dev)
+    codes, scale = torch.zeros((64, 64), dtype=torch.uint8, device=dev), torch.zeros(64, device=dev)
+
+    def other():
+        assert L.fp8w_quantize(w.data_ptr(), 64, 64, codes.data_ptr(), scale.data_ptr(), ctypes.byref(ex)) == 0
+
+    plan(1)
+    asked = L.nvfp4_test_occupancy_asked()
+    for batch in range(1, most + 1):
+        plan(batch)
+    assert L.nvfp4_test_occupancy_asked() == asked
+    other()
+    asked = L.nvfp4_test_occupancy_asked()
+    for _ in range(5):
+        other()
+        plan(most)
+    assert L.nvfp4_test_occupancy_asked() == asked
+    torch.cuda.synchronize()
+    assert cu.tolist() == list(range(most + 1)) and slots.tolist() == [16 * (most - 1 - s) for s in range(most)]
