@@ -860,12 +860,16 @@ def kv_plan(lens: torch.Tensor, num_new: torch.Tensor, block_table: torch.Tensor
     token, and those of a sequence without a page (NVFP4_ERR_PAGES to dev_status), get slot -1.
 
     Nothing but the table's new entries is changed, unless ``out`` holds the inputs: its
-    ``kv_lens``, ``held`` and ``free_count`` may be lens, held and free_count."""
+    ``kv_lens``, ``held`` and ``free_count`` may be lens, held and free_count.  Members of
+    ``out`` that are None are made and filled in."""
     o = (None,) * 6 if out is None else (out.cu_new, out.kv_lens, out.positions, out.slots, out.held,
                                          out.free_count)
     r = _native().plan(lens, num_new, block_table, free_pages, free_count, page_size, tokens, held, *o,
                        _raw(stream), dev_status)
-    return KvPlan(*r) if out is None else out
+    if out is None:
+        return KvPlan(*r)
+    out.cu_new, out.kv_lens, out.positions, out.slots, out.held, out.free_count = r
+    return out
 
 
 def rope_kv_write(q: torch.Tensor, k: torch.Tensor, v: Optional[torch.Tensor], positions: torch.Tensor,

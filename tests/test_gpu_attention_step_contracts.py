@@ -1,5 +1,5 @@
 """The attention step's contracts that its other tests leave open: calls in place one right behind the other,
-counts past a table's row, host queries that every batch size would repeat."""
+outputs given in part, counts past a table's row, host queries that every batch size would repeat."""
 import ctypes
 import os
 import random
@@ -11,6 +11,18 @@ import attention_step_ref as ref
 from test_gpu_attention_step import ints, nd
 
 pytestmark = pytest.mark.gpu
+
+
+def test_plan_outputs_given_in_part(dev):
+    """A plan whose `out` holds only the state that is updated in place: the others are made and come with it."""
+    m = nd()
+    lens, new, held, table = [3, 16, 5], [2, 1, 0], [1, 1, 1], [[7, 0], [4, 0], [9, 0]]
+    tl, th, tc, t = ints(dev, lens), ints(dev, held), ints(dev, [3]), ints(dev, table)
+    out = m.KvPlan(None, tl, None, None, th, tc)
+    p = m.kv_plan(tl, ints(dev, new), t, ints(dev, [1, 2, 8]), tc, 16, 4, held=th, out=out)
+    want = ref.plan(lens, new, held, table, [1, 2, 8], 3, 16, 4)
+    assert p is out and p.kv_lens is tl and p.held is th and p.free_count is tc
+    assert (t.tolist(), p.cu_new.tolist(), tl.tolist(), p.positions.tolist(), p.slots.tolist(), th.tolist(), tc.item()) == tuple(want)
 
 
 # (one CTA; a cluster; a cluster whose threads have several sequences each)
