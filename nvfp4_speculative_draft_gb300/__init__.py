@@ -66,6 +66,7 @@ import importlib.util
 import math
 import os
 from dataclasses import dataclass
+from fractions import Fraction
 from typing import Optional, Sequence
 
 import torch
@@ -826,7 +827,10 @@ def rotary_table(rot_dim: int, theta: float = 10000.0, sections: Optional[Sequen
           f"sections must add up to {pairs} pairs")
     if inv_freq is None:
         _need(theta > 0, "theta must be positive")
-        inv_freq = [float(theta) ** (-2.0 * i / rot_dim) for i in range(pairs)]
+        try:
+            inv_freq = [float(theta) ** (-2.0 * i / rot_dim) for i in range(pairs)]
+        except OverflowError:
+            raise ValueError("theta is too small: its frequencies are out of range") from None
     else:
         inv_freq = [float(f) for f in inv_freq]
         _need(len(inv_freq) == pairs and all(math.isfinite(f) for f in inv_freq),
@@ -840,8 +844,8 @@ def rotary_table(rot_dim: int, theta: float = 10000.0, sections: Optional[Sequen
         _need(min(left) == 0 == max(left), "sections cannot be interleaved")
     else:
         axis = [a for a, n in enumerate(sections) for _ in range(n)]
-    # the fraction is kept exactly: Python's integers, then two's complement
-    turns = [int(math.ldexp(f / (2.0 * math.pi), 64)) % (1 << 64) for f in inv_freq]
+    # the quotient's fraction is kept exactly: Python's integers, then two's complement
+    turns = [int(Fraction(f / (2.0 * math.pi)) * (1 << 64)) % (1 << 64) for f in inv_freq]
     turns = [t - (1 << 64) if t >= 1 << 63 else t for t in turns]
     return RotaryTable(torch.tensor(turns, dtype=torch.int64, device=device),
                        torch.tensor(axis, dtype=torch.uint8, device=device), axes)
