@@ -1087,6 +1087,16 @@ __global__ void __launch_bounds__(32 * kJoinWarps) attention_join_kernel(const _
   }
 }
 
+// Blocks that join an item's parts (a column of them for each of the launch's `ctas` records).  One a
+// row up to 24 rows of an item, where items have more parts than one warp takes (they share the CTAs):
+// 5 tokens of 32 / 8 heads over 4000 keys, 8 blocks and 20: one sequence 15.4 and 13.5 us, two 16.9 and
+// 15.6, eight 31.1 and 33.1.  Blocks past an item's rows only cost their launch (one token, 4 rows, of
+// four to six sequences over 4000 keys: 16 to 24 blocks 20.1 to 26.7 us, 8 blocks 19.1 to 25.3).
+unsigned join_blocks(int nq, int64_t tokens, int64_t batch, int kv_heads, int group, int per_item, int ctas) {
+  const int64_t each = nvfp4::cdiv(tokens, batch), rows = (each < per_item ? each : per_item) * group;  // (on average)
+  return nq == 1 && rows > 8 && rows <= 24 && batch * kv_heads * kJoinFew < ctas ? (unsigned)rows : 8 * (unsigned)nq;
+}
+
 // One map for the caches and for packed keys (one page of all tokens).
 bool encode_kv(CUtensorMap* map, const kv_pages& x, const paged_attention_input& in, int box) {
   const cuuint64_t dims[4] = {(cuuint64_t)in.dim, (cuuint64_t)in.kv_heads, (cuuint64_t)in.page_size, (cuuint64_t)in.pages};
@@ -1154,10 +1164,7 @@ int launch(const paged_attention_input& in, bool many, const attn_rows& out, voi
   // (no item can be cut)
   const int64_t uncut = NQ == 2 || (D == 256 && many) ? kWhole * kKeys : kKeys;
   if ((in.block_table != nullptr ? capacity : in.tokens) <= uncut) return NVFP4_OK;
-  // A block a row up to 24 rows (5 tokens of 4 heads over 4000 keys: 8 blocks 15.4 us, 20 13.5); more
-  // blocks cost more to launch than they save (24 instead of 8 for 4 rows 11.1 -> 12.3 us).
-  const int64_t rows = in.tokens * p.group;
-  const unsigned blocks = NQ == 1 && rows > 8 && rows <= 24 ? (unsigned)rows : 8 * NQ;
+  const unsigned blocks = join_blocks(NQ, in.tokens, in.batch, p.kv_heads, p.group, p.per_item, (int)grid);
   void* join_args[] = {&p};
   if (nvfp4::launch_dependent((const void*)attention_join_kernel<D, NQ>, dim3(grid, blocks), dim3(32 * kJoinWarps), 0, stream, 1,
                               join_args) != cudaSuccess)
@@ -1181,3 +1188,10 @@ int launch_attention(const paged_attention_input* in, const attn_rows* out, void
     default: return launch<256, 1>(*in, many, *out, workspace, dev_status, stream);
   }
 }
+
+#ifdef NVFP4_TEST_WITHHOLD
+// Test build: the rule for the joining kernel's blocks.
+extern "C" int nvfp4_test_join_blocks(int nq, int64_t tokens, int64_t batch, int kv_heads, int group, int per_item, int ctas) {
+  return (int)join_blocks(nq, tokens, batch, kv_heads, group, per_item, ctas);
+}
+#endif

@@ -1,4 +1,6 @@
-"""Contracts of the attention step that are kept on the host: the rotary table's range."""
+"""Contracts of the attention step that are kept on the host: the rotary table's range, the launch of the kernel that
+joins partial results."""
+import ctypes
 import math
 from fractions import Fraction
 
@@ -20,3 +22,17 @@ def test_rotary_table_of_any_finite_frequency():
 def test_rotary_table_refuses_frequencies_out_of_range():
     with pytest.raises(ValueError):
         nd.rotary_table(256, theta=5e-324, device="cpu")  # theta^(-254 / 256) is no binary64
+
+
+@pytest.mark.parametrize("tokens,batch,kv_heads,group,blocks", [
+    (1, 1, 8, 4, 8), (5, 1, 8, 4, 20), (6, 1, 8, 4, 24), (7, 1, 8, 4, 8),   # one sequence: its rows, up to 24
+    (2, 2, 8, 4, 8), (4, 4, 8, 4, 8), (6, 6, 8, 4, 8), (6, 3, 8, 4, 8),     # an item's 4 or 8 rows, whatever the batch's
+    (10, 2, 8, 4, 20), (15, 3, 8, 4, 8), (20, 4, 4, 4, 20), (40, 8, 8, 4, 8),  # parts of an item: more than 8, or not
+    (3, 1, 4, 8, 24), (1, 1, 1, 16, 16), (9, 2, 2, 4, 20), (2 ** 31 - 600, 2 ** 20 - 1, 1, 1, 8)])
+def test_blocks_that_join(tokens, batch, kv_heads, group, blocks):
+    from nvfp4_speculative_draft_gb300 import build
+    build.build()
+    f = ctypes.CDLL(build.WITHHOLD_LIB).nvfp4_test_join_blocks
+    f.argtypes = [ctypes.c_int, ctypes.c_int64, ctypes.c_int64] + [ctypes.c_int] * 4
+    assert f(1, tokens, batch, kv_heads, group, 128 // group, 152) == blocks
+    assert f(2, tokens, batch, kv_heads, group, 256 // group, 152) == 16
