@@ -89,3 +89,24 @@ def gather(cache, table_row, m):
         return cache.new_zeros((0, *cache.shape[2:]))
     pages = table_row[: -(-m // page)].long()
     return cache[pages].flatten(0, 1)[:m]
+
+
+def norm_bound(q, k, v, first, scale=None):
+    """The result in binary64 and the root mean square error, summed over all its elements, that the kernels'
+    two BF16 roundings may come to.
+
+    The result's rounding is off by at most 2^-8 |out| an element; each weight's by at most 2^-8 of it, with
+    signs that v's do not follow, so that the squares add: 2^-16 (|out|^2 + sum_j w_j^2 |v_j|^2).  (Evenly spread
+    errors have a third of that mean square; FP32's are a thousandth.)  A tile of keys lost or counted twice is
+    off by its share of sum_j w_j v_j, of which this sees one in ten thousand."""
+    n, heads, d = q.shape
+    m, group = k.shape[0], heads // k.shape[1]
+    scale = d ** -0.5 if scale is None else scale
+    out, square = torch.zeros((n, heads, d), dtype=torch.float64, device=q.device), 0.0
+    hidden = torch.arange(m, device=q.device)[None] > first + torch.arange(n, device=q.device)[:, None]
+    for h in range(heads):
+        kh, vh = k[:, h // group].double(), v[:, h // group].double()
+        w = torch.softmax(((q[:, h].double() @ kh.t()) * scale).masked_fill(hidden, -math.inf), 1)
+        out[:, h] = w @ vh
+        square += float((w.square() @ vh.square()).sum() + out[:, h].square().sum())
+    return out, 2.0 ** -8 * math.sqrt(square)

@@ -1,11 +1,13 @@
 """Contracts of the attention step that are kept on the host: the rotary table's range, the launch of the kernel that
-joins partial results."""
+joins partial results; and what the GPU tests' bound on an error's norm tells apart."""
 import ctypes
 import math
 from fractions import Fraction
 
 import pytest
+import torch
 
+import attention_step_ref as ref
 import nvfp4_speculative_draft_gb300 as nd
 
 
@@ -36,3 +38,26 @@ def test_blocks_that_join(tokens, batch, kv_heads, group, blocks):
     f.argtypes = [ctypes.c_int, ctypes.c_int64, ctypes.c_int64] + [ctypes.c_int] * 4
     assert f(1, tokens, batch, kv_heads, group, 128 // group, 152) == blocks
     assert f(2, tokens, batch, kv_heads, group, 256 // group, 152) == 16
+
+
+def test_the_norm_sees_a_tile_that_is_lost_or_doubled():
+    """The tests' bound on the error's norm, with the kernels' roundings, and with a tile's weights 0 or twice."""
+    g = torch.Generator().manual_seed(3)
+    n, heads, m, d = 1, 4, 60000, 64
+    q = (torch.randn((n, heads, d), generator=g) * 0.5).to(torch.bfloat16)
+    k, v = (torch.randn((m, 1, d), generator=g).to(torch.bfloat16) for _ in range(2))
+    want, most = ref.norm_bound(q, k, v, m - n)
+    assert torch.allclose(want, ref.attend(q, k, v, m - n)[0], rtol=1e-12, atol=1e-15)
+
+    def kernel(weight):  # weights in BF16 relative to the maximum, their sum before rounding
+        s = q.float()[0] @ k.float()[:, 0].t() * d ** -0.5
+        p = (s - s.amax(1, keepdim=True)).exp() * weight
+        return ((p.to(torch.bfloat16).double() @ v[:, 0].double()) / p.double().sum(1, keepdim=True)).to(torch.bfloat16)
+
+    ones = torch.ones(m)
+    assert (kernel(ones).double() - want[0]).norm().item() <= most
+    for tile in torch.randint(0, m // 128, (20,), generator=g).tolist():
+        for factor in (0.0, 2.0):
+            weight = ones.clone()
+            weight[128 * tile:128 * tile + 128] = factor
+            assert (kernel(weight).double() - want[0]).norm().item() > most
