@@ -604,10 +604,11 @@ typedef struct rope_kv_output {
  * rope_kv_write -- pair i of a head is its elements i and rot_dim / 2 + i:
  *   t = positions[axis[i]] * 2 pi turns[i] 2^-64;
  *   (x, y) -> (x cos t - y sin t, x sin t + y cos t), FP32, rounded once to BF16.
- * The fraction of a turn is exact however far the position; the sines are off by at
- * most 4e-7.  Rotated k and v as they are go to the cache at each token's slot; a
- * negative slot writes nothing, one past the cache neither (NVFP4_ERR_INDEX).  Where
- * two tokens have one slot, each element there is of one of them.  Workspace: none.
+ * Position times turns, modulo a turn, is exact however far the position; the sines are
+ * off by at most 4e-7 from those of the turns given.  Rotated k and v as they are go to
+ * the cache at each token's slot; a negative slot writes nothing, one past the cache
+ * neither (NVFP4_ERR_INDEX).  Where two tokens have one slot, each element there is of
+ * one of them.  Workspace: none.
  */
 int rope_kv_write(const rope_kv_input *in, const rope_kv_output *out, const nvfp4_exec *ex);
 

@@ -818,7 +818,10 @@ def rotary_table(rot_dim: int, theta: float = 10000.0, sections: Optional[Sequen
 
     ``sections``: pairs of each position axis (time, height, width, ...), rot_dim / 2 in all;
     default one axis.  They lie one after the other, or ``interleaved``: pair i belongs to axis
-    i modulo the number of axes while that axis has pairs left, else to axis 0."""
+    i modulo the number of axes while that axis has pairs left, else to axis 0.
+
+    The table is formed in binary64: an angle is off by at most 3 x 2^-53 of itself (7e-7 radians
+    at 2^31 radians, the frequency 1 at the last position)."""
     pairs = rot_dim // 2
     _need(rot_dim >= 16 and rot_dim % 16 == 0, "rot_dim must be a multiple of 16")
     sections = [pairs] if sections is None else [int(n) for n in sections]

@@ -40,16 +40,17 @@
 // What bounds it, and what it measured (fractions of a cuBLAS product's burst rate and of a
 // copy's):
 //   long prompts   the chain S -> softmax -> P V of each tile of rows: 3000 cycles a tile of keys
-//                  for 2048 of MMAs, as S of the next tile has to wait for TMEM (O and S of two
-//                  tiles fill it).  16384 tokens, 32 / 8 heads of 128: 1.41 ms, 1560 TFLOP/s
-//                  (0.81), less in long runs, where power limits it; 8192 tokens 383 us (0.75),
-//                  heads of 64 331 us.  Heads of 256, S twice in TMEM: 8192 tokens, 32 / 4 heads,
-//                  650 us, 1690 TFLOP/s (0.88).
+//                  for 2048 of MMAs, as S of the next tile waits for P V of this one, whose P lies
+//                  over S (heads of 128: O and S of two tiles fill TMEM; heads of 64 would leave P
+//                  a place of its own).  16384 tokens, 32 / 8 heads of 128: 1.42 ms, 1550 TFLOP/s
+//                  (0.81), 1.53 (0.75) in long runs, where power limits it; 8192 tokens 383 us
+//                  (0.75), heads of 64 331 us.  Heads of 256, S twice in TMEM: 8192 tokens, 32 / 4
+//                  heads, 650 us, 1690 TFLOP/s (0.88).
 //   short prompts  an item's start and end, about 4500 cycles: its first loads, the last P V, O's
-//                  way through registers.  11 prompts of up to 1900 tokens, 28 / 4 heads: 73 us
-//                  (0.39); one of 77 tokens: 7.8 us.
-//   the cache      HBM: 64 sequences of up to 16000 keys, up to 5 queries each: 158 us, 6.1 TB/s
-//                  (0.91); one token over 4000 keys, 32 / 4 heads of 256: 13.7 us, of which finding
+//                  way through registers.  11 prompts of up to 1900 tokens, 28 / 4 heads: 74 us
+//                  (0.38); one of 77 tokens: 7.5 us.
+//   the cache      HBM: 64 sequences of up to 16000 keys, up to 5 queries each: 159 us, 6.1 TB/s
+//                  (0.90); one token over 4000 keys, 32 / 4 heads of 256: 13.4 us, of which finding
 //                  the share and the join are 3 us each.
 #include <cuda_bf16.h>
 

@@ -20,7 +20,7 @@ namespace cg = cooperative_groups;
 //
 // What bounds it is the chain of dependent steps (launch, the lengths' load, two prefix
 // sums, bisection, the table's load), not the bytes: 24 requests of up to 6 tokens take
-// 4.5 us, 1000 of up to 400 (a chunk in eight of them) 9.1 us.
+// 4.2 us, 1000 of up to 400 (a chunk in eight of them) 8.8 us.
 
 constexpr int kPlanThreads = 1024;
 constexpr int kPlanWarps = kPlanThreads / 32;
@@ -214,8 +214,8 @@ __global__ void __launch_bounds__(kPlanThreads, 1) kv_plan_kernel(const __grid_c
 // The sines of a CTA's tokens are formed once, in shared memory; FP32 arithmetic, one
 // rounding to BF16.
 //
-// HBM bounds it: 16384 tokens of 40 / 8 heads of 128 take 71 us, 6.6 TB/s (0.97 of a copy's
-// rate).  Few tokens are a launch and a load's latency: one token 2.3 us, 315 tokens 3.3 us.
+// HBM bounds it: 16384 tokens of 40 / 8 heads of 128 take 71 us, 6.6 TB/s (0.98 of a copy's
+// rate).  Few tokens are a launch and a load's latency: one token 1.9 us, 315 tokens 3.1 us.
 
 constexpr int kRopeThreads = 256;
 
