@@ -66,7 +66,6 @@ import importlib.util
 import math
 import os
 from dataclasses import dataclass
-from fractions import Fraction
 from typing import Optional, Sequence
 
 import torch
@@ -847,8 +846,8 @@ def rotary_table(rot_dim: int, theta: float = 10000.0, sections: Optional[Sequen
         _need(min(left) == 0 == max(left), "sections cannot be interleaved")
     else:
         axis = [a for a, n in enumerate(sections) for _ in range(n)]
-    # the quotient's fraction is kept exactly: Python's integers, then two's complement
-    turns = [int(Fraction(f / (2.0 * math.pi)) * (1 << 64)) % (1 << 64) for f in inv_freq]
+    # the quotient's fraction is kept exactly (fmod is exact), then two's complement
+    turns = [int(math.ldexp(math.fmod(f / (2.0 * math.pi), 1.0), 64)) % (1 << 64) for f in inv_freq]
     turns = [t - (1 << 64) if t >= 1 << 63 else t for t in turns]
     return RotaryTable(torch.tensor(turns, dtype=torch.int64, device=device),
                        torch.tensor(axis, dtype=torch.uint8, device=device), axes)
