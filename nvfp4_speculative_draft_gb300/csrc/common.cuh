@@ -34,7 +34,8 @@ __device__ __forceinline__ bool guard(bool ok, int tag, int32_t* st) {
 // never issues one copy -- the GEMV's warp 0 its first weight stage, the
 // GEMM's producer its first A tile -- so the bounded wait on it runs out (the
 // limit is 20 ms there) and the unwinding after a timeout runs.  Nothing of
-// the withheld copy is ever in flight.
+// the withheld copy is ever in flight.  It also exports what tests ask of the host's rules
+// (nvfp4_test_*).
 #ifdef NVFP4_TEST_WITHHOLD
 constexpr unsigned long long kWaitLimit = 20000000ull;  // ns of globaltimer
 constexpr bool kWithhold = true;
